@@ -67,11 +67,9 @@ def listed():
 
 
 def _log(rng, lo, hi):
-    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
-
-
-def _no_contest(n):
-    return n + 1 if n == 3072 else n
+    """A size between lo and hi, spread over its logarithm; off the multiples of 1024 by one."""
+    n = max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+    return n - 1 if n % 1024 == 0 and n > lo else n
 
 
 def draw(rng):
@@ -89,24 +87,24 @@ def draw(rng):
         heads = dict(P=P, Hq=Hkv * rng.choice([1, 2, 3, 4, 5, 8]), Hkv=Hkv, D=D)
         if op == "plan":
             B = _log(rng, 1, 3000)
-            c = dict(op=op, B=B, T=_no_contest(B if rng.random() < 0.4 else _log(rng, B, 200000)),
+            c = dict(op=op, B=B, T=B if rng.random() < 0.4 else _log(rng, B, 200000),
                      page=rng.choice([8, 16, 32, 64, 128]), past=_log(rng, 1, 1000))
         elif op in ("rope", "ropeg"):
-            c = dict(op=op, T=_no_contest(_log(rng, 1, 12000)), rot=rng.choice([D, D, D // 2, D // 4]),
+            c = dict(op=op, T=_log(rng, 1, 12000), rot=rng.choice([D, D, D // 2, D // 4]),
                      f32=rng.random() < 0.5, **heads)
             if op == "rope":
                 c.update(cache=rng.random() < 0.6, page=rng.choice([8, 16, 64]))
                 c["keep"] = not c["cache"] or rng.random() < 0.5
         elif op in ("attn", "train"):
             B = _log(rng, 1, 40)
-            c = dict(op="attn", B=B, T=_no_contest(_log(rng, max(4, B), 16384)), past=rng.choice([0, 0, 0, 5, 300]),
+            c = dict(op="attn", B=B, T=_log(rng, max(4, B), 16384), past=rng.choice([0, 0, 0, 5, 300]),
                      causal=rng.random() < 0.85, train=op == "train", packed=rng.random() < 0.5, **heads)
             lq, lk = _lens(c)
             if c["P"] * c["Hq"] * B * max(lq) * max(lk) > (1 << 32):
                 continue                       # the plain form pads every prompt to the longest
         else:
-            c = dict(op=op, B=_log(rng, 1, 200), L=_no_contest(_log(rng, 1, 60000)),
-                     prefix=0 if rng.random() < 0.5 else _no_contest(_log(rng, 16, 16384)),
+            c = dict(op=op, B=_log(rng, 1, 200), L=_log(rng, 1, 60000),
+                     prefix=0 if rng.random() < 0.5 else _log(rng, 16, 16384),
                      page=rng.choice([8, 16, 32, 64, 128]), **heads)
             if c["P"] * c["B"] * c["L"] * c["Hkv"] * c["D"] > (1 << 29):
                 continue
