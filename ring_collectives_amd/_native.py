@@ -25,6 +25,8 @@ _vp = ctypes.c_void_p
 _pp = ctypes.POINTER(ctypes.c_void_p)
 _sz = ctypes.c_size_t
 _i = ctypes.c_int
+_ll = ctypes.c_longlong
+_f = ctypes.c_float
 
 SIGNATURES = {
     "ring_workspace_bytes": (_sz, [_i, _i, _sz, _i]),
@@ -40,6 +42,12 @@ SIGNATURES = {
     "all_gather_gemm": (_i, [_pp, _pp, _pp, _pp, _i, _i, _i, _i, _vp, _sz, _vp]),
     "tp_mlp_layer": (_i, [_pp, _pp, _pp, _pp, _pp, _pp, _i, _i, _i, _i, _vp, _sz, _vp]),
     "tp_mlp_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "kv_plan": (_i, [_vp] * 10 + [_i] * 6 + [_vp]),
+    "tp_qk_norm_rope": (_i, [_pp, _pp, _pp, _vp, _vp, _pp, _pp, _pp, _pp, _pp, _vp] + [_i] * 6 +
+                        [_ll, _ll, _ll, _f, _i, _vp]),
+    "tp_qk_norm_rope_grad": (_i, [_pp] * 6 + [_vp, _vp, _pp, _pp, _pp] + [_i] * 6 + [_ll, _ll, _f, _i, _vp, _sz, _vp]),
+    "tp_qk_norm_rope_grad_workspace_bytes": (_sz, [_i, _i]),
+    "tp_attention": (_i, [_pp] * 5 + [_vp, _vp] + [_i] * 7 + [_ll] * 4 + [_i, _f, _vp]),
     "ring_last_error": (_i, [_vp, _sz, _vp, ctypes.POINTER(ctypes.c_int)]),
     "ring_strerror": (ctypes.c_char_p, [_i]),
 }

@@ -1,0 +1,200 @@
+// attn_core.h -- what the attention kernels share: the LDS placement of a tile
+// of rows, the direct global->LDS loads that fill it, the two kinds of MFMA
+// fragment reads from it, and the search of a tile's prompt.
+//
+// Every product runs on v_mfma_f32_32x32x16_bf16 with the streamed operand (a
+// tile of key, value, query or gradient rows in LDS) as A and the stationary
+// one (32 rows per wave, in registers) as B:
+//   S^T = K Q^T       A = the rows of K as they lie, B = rows of Q
+//   O^T += V^T P^T    A = V read transposed,        B = P^T, the accumulators
+//                     of S^T themselves, rounded to bf16
+// Lane l of a wave owns column n = l % 32 of every product (one query, or one
+// key in the pass over dK and dV), so softmax statistics are one value per
+// lane and the row operations never leave the lane but for one exchange with
+// lane l ^ 32, which holds the other half of the column's rows.
+#pragma once
+
+#include "gemm_core.h"
+
+namespace ringc {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Geometry of rows of D bf16 values in LDS: 2 D bytes each, unpadded, in C
+// chunks of 16 bytes.  Chunk c of row r is stored at chunk c ^ swz(r).  With
+// these swizzles the 16 rows that a row-fragment read touches in one LDS cycle
+// and the 4 rows x 32 columns of a transposed read fall on distinct banks.
+template <int D> struct Rows {
+    static_assert(D == 64 || D == 128, "head width");
+    static constexpr int RB = 2 * D;             // bytes of a row
+    static constexpr int C = D / 8;              // 16-byte chunks of a row
+    static constexpr int RPI = 64 / C;           // rows filled by one load instruction (1 KiB)
+    static constexpr int KK = D / 16;            // MFMA k-steps over a row
+    static constexpr int DB = D / 32;            // 32-wide blocks of a row
+    static __device__ __forceinline__ int swz(int r) {
+        return D == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : ((r & 2) << 1) | ((r >> 2) & 3);
+    }
+};
+
+// The direct loads of one wave into tiles of ROWS rows shared by NW waves:
+// wave w issues instructions w J .. w J + J - 1, each filling RPI rows.  Rows
+// past the view's end are filled with zeros by the hardware's bounds check.
+template <int D, int ROWS, int NW> struct TileLoad {
+    static constexpr int J = ROWS / Rows<D>::RPI / NW;
+    static_assert(J * NW * Rows<D>::RPI == ROWS, "load split");
+    unsigned voff[J];       // byte offset of this lane's chunk in instruction j, without the tile's start
+    int first;              // LDS byte of this wave's first instruction within the tile
+    __device__ __forceinline__ void init(int lane, int wave, unsigned row_bytes) {
+        first = wave * J * 1024;
+#pragma unroll
+        for (int j = 0; j < J; ++j) {
+            const int r = (wave * J + j) * Rows<D>::RPI + lane / Rows<D>::C;
+            voff[j] = (unsigned)r * row_bytes + (unsigned)(((lane % Rows<D>::C) ^ Rows<D>::swz(r)) * 16);
+        }
+    }
+    __device__ __forceinline__ void issue(rsrc_t view, unsigned short* lds, int at) const {
+#pragma unroll
+        for (int j = 0; j < J; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(view, lds_at(lds, (unsigned)(at + first + j * 1024)), 16, voff[j],
+                                                     0, 0, POL_PLAIN);
+    }
+};
+
+// A view of `rows` rows of D values that start `row_bytes` apart (none for
+// rows <= 0, at most `most`): it ends with the last row's last value.
+template <int D>
+__device__ __forceinline__ rsrc_t rows_view(const unsigned short* base, long long rows, int most, unsigned row_bytes) {
+    const long long n = rows < 0 ? 0 : rows < most ? rows : most;
+    return tile_view(base, n ? (n - 1) * (long long)row_bytes + Rows<D>::RB : 0);
+}
+
+// Fragment reads from a tile at byte `at` of LDS (a multiple of 4096).
+template <int D> struct Frags {
+    unsigned row0;          // row fragment: row l % 32, chunk l / 32
+    unsigned tr[2];         // transposed: rows 4 (l / 32) + .., and the same 8 rows further down
+    __device__ __forceinline__ void init(int lane) {
+        typedef Rows<D> R;
+        row0 = (unsigned)((lane & 31) * R::RB + (((lane >> 5) ^ R::swz(lane & 31)) * 16));
+        const int g = lane >> 4, i = lane & 15;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int r = 8 * t + 4 * (g >> 1) + (i >> 2);
+            tr[t] = (unsigned)(r * R::RB + (((2 * (g & 1) + ((i & 3) >> 1)) ^ R::swz(r)) * 16) + (i & 1) * 8);
+        }
+    }
+    // A[m = row 32 b + l % 32][k = 16 kk + 8 (l / 32) + t]
+    __device__ __forceinline__ bf16x8 rows(const unsigned short* lds, int at, int b, int kk) const {
+        return *(const bf16x8*)((const char*)lds + at + (row0 ^ (unsigned)(kk * 32)) + b * 32 * Rows<D>::RB);
+    }
+    // A[m = column 32 db + l % 32][k]: rows 16 ks + 4 (l / 32) + {0 .. 3} for
+    // t = 0 .. 3 and 8 rows further for t = 4 .. 7, the order in which the
+    // accumulators of a product hold its rows.
+    __device__ __forceinline__ bf16x8 cols(unsigned short* lds, int at, int db, int ks) const {
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        const unsigned o = (unsigned)(at + ks * 16 * Rows<D>::RB);
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)lds_at(lds, (tr[0] ^ (unsigned)(db * 64)) + o));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)lds_at(lds, (tr[1] ^ (unsigned)(db * 64)) + o));
+        const s16x8 v = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+        return __builtin_bit_cast(bf16x8, v);
+    }
+};
+
+// Accumulators 8 ks .. 8 ks + 7 of a 32 x 32 block, rounded to bf16 (nearest
+// even), as the B operand of k-step ks of the next product.
+__device__ __forceinline__ bf16x8 round8(const f32x16& x, int ks) {
+    typedef float f32x8 __attribute__((ext_vector_type(8)));
+    const f32x8 y = {x[8 * ks], x[8 * ks + 1], x[8 * ks + 2], x[8 * ks + 3],
+                     x[8 * ks + 4], x[8 * ks + 5], x[8 * ks + 6], x[8 * ks + 7]};
+    return __builtin_convertvector(y, bf16x8);
+}
+
+// Row of accumulator v of lane half h within its 32 x 32 block.
+__device__ __forceinline__ int acc_row(int v, int h) { return 8 * (v / 4) + 4 * h + v % 4; }
+
+// The lower and the upper half's value of x, in both halves.  The two operands
+// of the swap have to differ for the compiler: it takes the results of
+// swapping a register with itself for equal.
+struct Halves {
+    float lo, hi;
+};
+__device__ __forceinline__ Halves both_halves(float x) {
+    const unsigned u = __builtin_bit_cast(unsigned, x);
+    unsigned w = u;
+    asm("" : "+v"(w));
+    const auto r = __builtin_amdgcn_permlane32_swap(u, w, false, false);
+    return Halves{__builtin_bit_cast(float, (unsigned)r[0]), __builtin_bit_cast(float, (unsigned)r[1])};
+}
+__device__ __forceinline__ float max_halves(float x) {
+    const Halves h = both_halves(x);
+    return fmaxf(h.lo, h.hi);
+}
+__device__ __forceinline__ float sum_halves(float x) {
+    const Halves h = both_halves(x);
+    return h.lo + h.hi;
+}
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The prompt and tile of work slot `slot`, where prompt b has
+// ceil(len_b * per / rows) tiles, len_b = cu[b + 1] - cu[b] clamped to the
+// `total` rows there are.  Every lane of the wave looks at one prompt at a
+// time.  Returns false past the last tile.
+struct PromptTile {
+    int b, tile, tiles;
+};
+__device__ __forceinline__ int clamp_cu(int x, int total) { return x < 0 ? 0 : x > total ? total : x; }
+__device__ inline bool find_tile(const int* cu, int B, int total, int per, int rows, int slot, int lane, PromptTile& t) {
+    int before = 0;
+    for (int b0 = 0; b0 < B; b0 += 64) {
+        int n = 0;
+        if (b0 + lane < B) {
+            const int lo = clamp_cu(cu[b0 + lane], total), hi = clamp_cu(cu[b0 + lane + 1], total);
+            if (hi > lo) n = (int)(((long long)(hi - lo) * per + rows - 1) / rows);
+        }
+        int sum = n;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int y = __shfl_up(sum, d);
+            if (lane >= d) sum += y;
+        }
+        const unsigned long long past = __ballot(before + sum > slot);
+        if (past) {
+            const int at = __builtin_ctzll(past);
+            t.b = b0 + at;
+            t.tiles = __builtin_amdgcn_readlane(n, at);
+            t.tile = slot - (before + __builtin_amdgcn_readlane(sum, at) - t.tiles);
+            return true;
+        }
+        before += __builtin_amdgcn_readlane(sum, 63);
+    }
+    return false;
+}
+
+// Arguments of the packed-prompt kernels (per-rank pointers by value).
+struct PromptArgs {
+    const unsigned short *q[RING_MAX_RANKS], *k[RING_MAX_RANKS], *v[RING_MAX_RANKS];
+    const int *cu_q, *cu_k;
+    long long q_stride, k_stride, v_stride;   // elements from a token's row to the next
+    int B, Tq, Tk, P, Hq, Hkv, causal;
+    float c;                                   // scale * log2(e)
+};
+
+// Work units (rank, key head) vary fastest over the launch, eight at a time:
+// workgroups go to the eight XCDs in turn, so one unit's keys and values stay
+// with one XCD's L2 and the tiles of one unit run there together.
+__device__ __forceinline__ void unit_slot(int units, int slots, int block, int& unit, int& slot) {
+    const int full = units / 8 * 8;
+    const int g = block / (8 * slots);                     // group of eight units
+    if (g * 8 < full) {
+        const int i = block - g * 8 * slots;
+        unit = g * 8 + i % 8;
+        slot = i / 8;
+    } else {
+        const int i = block - full * slots, n = units - full;
+        unit = full + i % n;
+        slot = i / n;
+    }
+}
+
+}  // namespace ringc

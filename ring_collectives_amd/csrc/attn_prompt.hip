@@ -1,0 +1,261 @@
+// attn_prompt.hip -- attention over packed prompts with grouped heads.
+//
+//   S = scale Q K^T over the keys a query sees, m = max S, P = exp(S - m),
+//   l = sum P, O = P V / l, lse = m + log l.
+//
+// One pass over the keys with the running maximum and sum.  A workgroup of
+// four waves takes 128 rows of one (rank, key head): row i G + g is query i of
+// the prompt and query head g of the G that share the key head, so the group
+// reads every key tile once.  Each wave keeps 32 of the rows (its Q fragments
+// and the accumulators of O^T) in registers; key and value tiles of 64 rows go
+// through two LDS buffers each, the next tile loading while one is computed.
+#include "attn_core.h"
+#include "attn_internal.h"
+
+#include <hip/hip_runtime.h>
+
+namespace ringc {
+namespace {
+
+constexpr int kTileRows = 128;     // rows (query, head of the group) of a workgroup
+constexpr int kTileKeys = 64;      // keys of a tile
+constexpr int kWaves = 4;
+
+struct FwdArgs {
+    PromptArgs p;
+    unsigned short* o[RING_MAX_RANKS];
+    float* lse[RING_MAX_RANKS];               // may be null
+    long long o_stride;
+    int slots;
+};
+
+template <int D>
+__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
+    typedef Rows<D> R;
+    constexpr int kTileBytes = kTileKeys * R::RB;
+    __shared__ __align__(4096) unsigned short lds[4 * kTileBytes / 2];   // K 0, K 1, V 0, V 1
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = lane >> 5;
+    int unit, slot;
+    unit_slot(a.p.P * a.p.Hkv, a.slots, blockIdx.x, unit, slot);
+    const int G = a.p.Hq / a.p.Hkv, rank = unit / a.p.Hkv, kvh = unit % a.p.Hkv;
+    PromptTile pt;
+    if (!find_tile(a.p.cu_q, a.p.B, a.p.Tq, G, kTileRows, slot, lane, pt)) return;
+    const int b = pt.b, tile = pt.tiles - 1 - pt.tile;       // the longest first
+    const int q0 = clamp_cu(a.p.cu_q[b], a.p.Tq), nq = clamp_cu(a.p.cu_q[b + 1], a.p.Tq) - q0;
+    const int k0 = clamp_cu(a.p.cu_k[b], a.p.Tk), k1 = clamp_cu(a.p.cu_k[b + 1], a.p.Tk);
+    const int nk = k1 > k0 ? k1 - k0 : 0;
+    const long long rows = (long long)nq * G;
+    const long long m0 = (long long)tile * kTileRows + wave * 32;
+    // this lane's row; rows past the end repeat the last one and are not stored
+    const long long m = m0 + (lane & 31) < rows ? m0 + (lane & 31) : rows - 1;
+    const int qi = (int)(m / G), head = kvh * G + (int)(m % G);
+
+    // keys [0, seen) are visible to this lane's query, [0, every) to every row
+    // of the wave, [0, some) to one of them at least, [0, most) to one of the
+    // workgroup's
+    const int off = nk - nq;
+    int seen = nk, every = nk, some = nk, most = nk;
+    if (a.p.causal) {
+        auto upto = [&](long long row) {
+            const long long s = (row < rows ? row : rows - 1) / G + off + 1;
+            return (int)(s < 0 ? 0 : s < nk ? s : nk);
+        };
+        seen = upto(m);
+        every = upto(m0);
+        some = upto(m0 + 31);
+        most = upto((long long)tile * kTileRows + kTileRows - 1);
+    }
+
+    bf16x8 qf[R::KK];
+    {
+        const unsigned short* qp = a.p.q[rank] + (q0 + (long long)qi) * a.p.q_stride + (long long)head * D + 8 * half;
+#pragma unroll
+        for (int kk = 0; kk < R::KK; ++kk) qf[kk] = *(const bf16x8*)(qp + 16 * kk);
+    }
+    const unsigned krow = (unsigned)(a.p.k_stride * 2), vrow = (unsigned)(a.p.v_stride * 2);
+    const unsigned short* kp = a.p.k[rank] + (long long)k0 * a.p.k_stride + (long long)kvh * D;
+    const unsigned short* vp = a.p.v[rank] + (long long)k0 * a.p.v_stride + (long long)kvh * D;
+    TileLoad<D, kTileKeys, kWaves> kl, vl;
+    kl.init(lane, wave, krow);
+    vl.init(lane, wave, vrow);
+    Frags<D> fr;
+    fr.init(lane);
+    auto load = [&](int j, int buf) {
+        kl.issue(rows_view<D>(kp + (long long)j * kTileKeys * a.p.k_stride, nk - (long long)j * kTileKeys, kTileKeys, krow), lds,
+                 buf * kTileBytes);
+        vl.issue(rows_view<D>(vp + (long long)j * kTileKeys * a.p.v_stride, nk - (long long)j * kTileKeys, kTileKeys, vrow), lds,
+                 (2 + buf) * kTileBytes);
+    };
+
+    f32x16 o[R::DB];
+#pragma unroll
+    for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) o[db][v] = 0.0f;
+    float mc = -INFINITY, l = 0.0f;       // running maximum times c (both halves), this half's share of the sum
+    const float c = a.p.c;
+
+    const int tiles = (most + kTileKeys - 1) / kTileKeys;
+    if (tiles) load(0, 0);
+    for (int j = 0; j < tiles; ++j) {
+        const int buf = j & 1;
+        wait_vm(0);                       // tile j has landed
+        lds_barrier();                    // everyone's has; the buffers of tile j - 1 are free
+        if (j + 1 < tiles) load(j + 1, buf ^ 1);
+        if (j * kTileKeys >= some) continue;    // nothing here for this wave's rows
+        const int ka = buf * kTileBytes, va = (2 + buf) * kTileBytes;
+        f32x16 s[2];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+            for (int v = 0; v < 16; ++v) s[kb][v] = 0.0f;
+#pragma unroll
+            for (int kk = 0; kk < R::KK; ++kk)
+                s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, ka, kb, kk), qf[kk], s[kb], 0, 0, 0);
+        }
+        if ((j + 1) * kTileKeys > every) {
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+                    if (j * kTileKeys + kb * 32 + acc_row(v, half) >= seen) s[kb][v] = -INFINITY;
+        }
+        float mx = s[0][0];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) mx = fmaxf(mx, s[kb][v]);
+        mx = max_halves(mx) * c;
+        // The maximum only keeps the exponents in range: it moves when some
+        // row's grows by more than 2^8, which P in bf16 and its fp32 sums hold
+        // as exactly as values up to 1.
+        if (__any(mx > mc + 8.0f)) {
+            const float mn = fmaxf(mc, mx);
+            const float alpha = mn == -INFINITY ? 1.0f : exp2_hw(mc - mn);
+            mc = mn;
+            l *= alpha;
+#pragma unroll
+            for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) o[db][v] *= alpha;
+        }
+        const float sub = mc == -INFINITY ? 0.0f : mc;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                s[kb][v] = exp2_hw(__builtin_fmaf(s[kb][v], c, -sub));
+                l += s[kb][v];
+            }
+        // P is rounded to bf16 for the matrix cores (relative error 2^-9 of
+        // each weight; l sums the unrounded ones in fp32).
+#pragma unroll
+        for (int ks = 0; ks < kTileKeys / 16; ++ks) {
+            const bf16x8 pf = round8(s[ks / 2], ks % 2);
+#pragma unroll
+            for (int db = 0; db < R::DB; ++db)
+                o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, va, db, ks), pf, o[db], 0, 0, 0);
+        }
+    }
+
+    if (m0 + (lane & 31) >= rows) return;
+    l = sum_halves(l);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;          // a row that sees no key gives zeros
+    unsigned short* op = a.o[rank] + (q0 + (long long)qi) * a.o_stride + (long long)head * D + 4 * half;
+#pragma unroll
+    for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+        for (int v = 0; v < 16; v += 4) {
+            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+            const f32x4 y = {o[db][v] * inv, o[db][v + 1] * inv, o[db][v + 2] * inv, o[db][v + 3] * inv};
+            *(bf16x4*)(op + 32 * db + 2 * v) = __builtin_convertvector(y, bf16x4);
+        }
+    if (a.lse[rank] && half == 0)
+        a.lse[rank][(long long)head * a.p.Tq + q0 + qi] = l == 0.0f ? -INFINITY : (mc + __log2f(l)) * kLn2;
+}
+
+}  // namespace
+
+bool fill_prompt_args(PromptArgs& p, const void* const* q, const void* const* k, const void* const* v, const int* cu_q,
+                      const int* cu_k, int P, int B, int Tq, int Tk, int Hq, int Hkv, int D, long long q_stride,
+                      long long k_stride, long long v_stride, int causal, float scale) {
+    for (int r = 0; r < P; ++r) {
+        p.q[r] = (const unsigned short*)q[r];
+        p.k[r] = (const unsigned short*)k[r];
+        p.v[r] = (const unsigned short*)v[r];
+        if (!q[r] || (Tk && (!k[r] || !v[r]))) return false;
+        if (((uintptr_t)q[r] | (uintptr_t)k[r] | (uintptr_t)v[r]) & 15) return false;
+    }
+    p.cu_q = cu_q;
+    p.cu_k = cu_k;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.B = B;
+    p.Tq = Tq;
+    p.Tk = Tk;
+    p.P = P;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.causal = causal;
+    p.c = scale * kLog2e;
+    return true;
+}
+
+// What every packed-prompt call checks of its sizes.  Row strides are whole
+// 16-byte chunks, so that every head row is 16-byte aligned, and below 2^21
+// elements, so that a tile's view stays below 2 GiB.
+int prompt_shape(int P, int B, int Tq, int Tk, int Hq, int Hkv, int D, float scale) {
+    if (P < 1 || P > RING_MAX_RANKS || B < 0 || Tq < 0 || Tk < 0 || Hq < 1 || Hkv < 1) return RING_EINVAL;
+    if (!(scale > 0.0f) || !(scale <= 3.0e38f)) return RING_EINVAL;
+    if (Hq % Hkv || (D != 64 && D != 128) || (long long)Hq * D >= kMaxRow || (long long)Hkv * D >= kMaxRow)
+        return RING_EUNSUPPORTED;
+    return RING_OK;
+}
+bool row_stride_ok(long long stride, int heads, int D) {
+    return stride >= (long long)heads * D && stride < kMaxRow && stride % 8 == 0;
+}
+// Tiles of `rows` rows that prompts of `total` tokens, `per` rows each, can
+// make: 0 if there are too many for a launch.
+int prompt_slots(int B, int total, int per, int rows, int units) {
+    const long long n = (long long)total * per / rows + (B < total ? B : total);
+    return n * (units > 8 ? units : 8) < (1LL << 31) ? (int)n : 0;
+}
+
+}  // namespace ringc
+
+using namespace ringc;
+
+extern "C" int tp_attention(const void* const* q, const void* const* k, const void* const* v, void* const* o,
+                            float* const* lse, const int* cu_q, const int* cu_k, int P, int B, int Tq, int Tk, int Hq,
+                            int Hkv, int D, long long q_stride, long long k_stride, long long v_stride,
+                            long long o_stride, int causal, float scale, void* stream) {
+    int rc = prompt_shape(P, B, Tq, Tk, Hq, Hkv, D, scale);
+    if (rc != RING_OK) return rc;
+    if (!q || !k || !v || !o) return RING_EINVAL;
+    if (!row_stride_ok(q_stride, Hq, D) || !row_stride_ok(k_stride, Hkv, D) || !row_stride_ok(v_stride, Hkv, D) ||
+        !row_stride_ok(o_stride, Hq, D))
+        return RING_EINVAL;
+    if (Tq == 0 || B == 0) return RING_OK;
+    if (!cu_q || !cu_k) return RING_EINVAL;
+    FwdArgs a;
+    if (!fill_prompt_args(a.p, q, k, v, cu_q, cu_k, P, B, Tq, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride,
+                          causal ? 1 : 0, scale))
+        return RING_EINVAL;
+    for (int r = 0; r < P; ++r) {
+        if (!o[r] || ((uintptr_t)o[r] & 15) || (lse && (!lse[r] || ((uintptr_t)lse[r] & 3)))) return RING_EINVAL;
+        a.o[r] = (unsigned short*)o[r];
+        a.lse[r] = lse ? lse[r] : nullptr;
+    }
+    a.o_stride = o_stride;
+    const int units = P * Hkv;
+    a.slots = prompt_slots(B, Tq, Hq / Hkv, kTileRows, units);
+    if (!a.slots) return RING_EUNSUPPORTED;
+    const dim3 grid((unsigned)a.slots * (unsigned)units);
+    if (D == 128)
+        hipLaunchKernelGGL(attn_fwd_kernel<128>, grid, dim3(256), 0, (hipStream_t)stream, a);
+    else
+        hipLaunchKernelGGL(attn_fwd_kernel<64>, grid, dim3(256), 0, (hipStream_t)stream, a);
+    return hipGetLastError() == hipSuccess ? RING_OK : RING_EHIP;
+}

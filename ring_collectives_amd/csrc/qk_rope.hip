@@ -1,0 +1,417 @@
+// qk_rope.hip -- per-head RMS norm of queries and keys with the position
+// rotation and the cache write in one pass, and its gradient.
+//
+//   n = x / sqrt(mean(x^2) + eps),  y = n gain,
+//   z_i = y_i cos - y_{i+h} sin,  z_{i+h} = y_{i+h} cos + y_i sin   (i < h = rot / 2)
+// and back, with u = dy gain, dy the gradient turned the other way:
+//   dx = (u - n mean(n u)) / sqrt(mean(x^2) + eps),   dgain = sum dy n.
+//
+// Memory bounds both: every value is read and written once.  D / 8 lanes hold
+// one head row, 8 values each, so a wave covers 512 / D head rows of one token
+// with 16-byte accesses; the row's mean is a reduction over those lanes and
+// the rotation's partner values come from the lane rot / 16 further on.  A
+// wave keeps its token's cos and sin in registers for all of its heads.
+#include "ring_device.h"
+#include "tp_attention.h"
+
+#include <hip/hip_runtime.h>
+
+namespace ringc {
+namespace {
+
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+
+struct RopeArgs {
+    const void* qkv[RING_MAX_RANKS];
+    const float *gq[RING_MAX_RANKS], *gk[RING_MAX_RANKS];
+    unsigned short *q[RING_MAX_RANKS], *k[RING_MAX_RANKS], *v[RING_MAX_RANKS];      // the gradients, going back
+    unsigned short *kc[RING_MAX_RANKS], *vc[RING_MAX_RANKS];
+    const float* cs;
+    const int* pos;
+    const long long* slots;
+    long long table_rows, cache_rows, stride;
+    int P, T, Hq, Hkv, rot;
+    float eps;
+};
+
+__device__ __forceinline__ f32x8 load8(const float* p) {
+    const f32x4 a = *(const f32x4*)p, b = *(const f32x4*)(p + 4);
+    return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+}
+__device__ __forceinline__ f32x8 load8(const unsigned short* p) {
+    return __builtin_convertvector(*(const bf16x8*)p, f32x8);
+}
+__device__ __forceinline__ void store8(float* p, const f32x8& x) {
+    *(f32x4*)p = f32x4{x[0], x[1], x[2], x[3]};
+    *(f32x4*)(p + 4) = f32x4{x[4], x[5], x[6], x[7]};
+}
+__device__ __forceinline__ void store8(unsigned short* p, const f32x8& x) {
+    *(bf16x8*)p = __builtin_convertvector(x, bf16x8);
+}
+
+// Sum over the W lanes that share a head row.
+template <int W> __device__ __forceinline__ float row_sum(float x) {
+#pragma unroll
+    for (int d = 1; d < W; d *= 2) x += __shfl_xor(x, d);
+    return x;
+}
+
+// This lane's cos and sin (its 8 values' pairs), as x -> a x + b partner(x).
+struct Turn {
+    f32x8 a, b;
+    int partner;        // lane that holds the other values of the pairs
+    bool turns;
+};
+template <int D>
+__device__ __forceinline__ Turn make_turn(const float* cs, const int* pos, long long table_rows, int rot, int t, int lane) {
+    Turn r;
+    const int i = lane % (D / 8), w = rot / 16;          // lanes [0, w) hold the pairs' first values, [w, 2 w) the second
+    r.turns = i < 2 * w;
+    r.partner = lane + (r.turns ? (i < w ? w : -w) : 0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        r.a[e] = 1.0f;
+        r.b[e] = 0.0f;
+    }
+    const long long p = pos[t];
+    if (p < 0 || p >= table_rows) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.a[e] = __builtin_nanf("");
+    } else if (r.turns) {
+        const float* c = cs + p * rot + (i < w ? i : i - w) * 8;
+        r.a = load8(c);
+        r.b = load8(c + rot / 2);
+        if (i < w)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) r.b[e] = -r.b[e];
+    }
+    return r;
+}
+__device__ __forceinline__ f32x8 turn(const Turn& r, const f32x8& y) {
+    f32x8 z;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) z[e] = r.a[e] * y[e] + r.b[e] * __shfl(y[e], r.partner);
+    return z;
+}
+
+template <int D, class X>
+__global__ __launch_bounds__(256) void qk_rope_kernel(RopeArgs a) {
+    constexpr int W = D / 8, HW = 64 / W;          // lanes of a head row, head rows of a wave
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int sub = lane / W, i = lane % W;
+    const int H = a.Hq + 2 * a.Hkv;
+    const long long items = (long long)a.P * a.T;
+    for (long long it = (long long)blockIdx.x * 4 + wave; it < items; it += (long long)gridDim.x * 4) {
+        const int rank = (int)(it / a.T), t = (int)(it % a.T);
+        const Turn r = make_turn<D>(a.cs, a.pos, a.table_rows, a.rot, t, lane);
+        const X* x = (const X*)a.qkv[rank] + t * a.stride;
+        f32x8 gq, gk;
+        const bool norm = a.gq[rank] != nullptr;
+        if (norm) {
+            gq = load8(a.gq[rank] + 8 * i);
+            gk = load8(a.gk[rank] + 8 * i);
+        }
+        const long long slot = a.slots ? a.slots[t] : -1;
+        const bool cached = slot >= 0 && slot < a.cache_rows;
+        for (int h0 = 0; h0 < H; h0 += HW) {
+            const int h = h0 + sub;
+            f32x8 y;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = 0.0f;
+            if (h < H) y = load8(x + h * D + 8 * i);
+            const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
+            f32x8 z = y;
+            if (norm) {
+                float s = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s += y[e] * y[e];
+                const float inv = 1.0f / sqrtf(row_sum<W>(s) * (1.0f / D) + a.eps);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) z[e] = y[e] * inv * (is_q ? gq[e] : gk[e]);
+            }
+            z = turn(r, z);
+            if (h >= H) continue;
+            if (is_q) {
+                store8(a.q[rank] + ((long long)t * a.Hq + h) * D + 8 * i, z);
+            } else if (is_k) {
+                const int g = h - a.Hq;
+                if (a.k[rank]) store8(a.k[rank] + ((long long)t * a.Hkv + g) * D + 8 * i, z);
+                if (cached) store8(a.kc[rank] + (slot * a.Hkv + g) * D + 8 * i, z);
+            } else {
+                const int g = h - a.Hq - a.Hkv;
+                if (a.v[rank]) store8(a.v[rank] + ((long long)t * a.Hkv + g) * D + 8 * i, y);
+                if (cached) store8(a.vc[rank] + (slot * a.Hkv + g) * D + 8 * i, y);
+            }
+        }
+    }
+}
+
+constexpr int kGradBlocks = 256;       // workgroups per rank that leave a partial sum of the gains' gradients
+
+struct RopeGradArgs {
+    RopeArgs f;                        // q, k, v: the gradients read; kc: unused
+    void* dx[RING_MAX_RANKS];
+    float* part;                       // [P][blocks][2][D]
+    Status* status;
+    WsSpan data;
+    int blocks;
+};
+
+template <int D, class X>
+__global__ __launch_bounds__(256) void qk_rope_grad_kernel(RopeGradArgs g) {
+    constexpr int W = D / 8, HW = 64 / W;
+    __shared__ float sum[4][HW][2][D];
+    const RopeArgs& a = g.f;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int sub = lane / W, i = lane % W;
+    const int H = a.Hq + 2 * a.Hkv, rank = blockIdx.y;
+    if (blockIdx.x == 0 && rank == 0 && threadIdx.x == 0) ws_add_data(g.status, g.data);
+    const bool norm = a.gq[rank] != nullptr;
+    f32x8 gq, gk, sq, sk;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sq[e] = sk[e] = 0.0f;
+    if (norm) {
+        gq = load8(a.gq[rank] + 8 * i);
+        gk = load8(a.gk[rank] + 8 * i);
+    }
+    for (long long t = (long long)blockIdx.x * 4 + wave; t < a.T; t += (long long)gridDim.x * 4) {
+        Turn r = make_turn<D>(a.cs, a.pos, a.table_rows, a.rot, (int)t, lane);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) r.b[e] = -r.b[e];          // the other way
+        const long long p = a.pos[t];
+        const bool known = p >= 0 && p < a.table_rows;
+        const X* x = (const X*)a.qkv[rank] + t * a.stride;
+        X* dx = (X*)g.dx[rank] + t * (long long)H * D;
+        for (int h0 = 0; h0 < H; h0 += HW) {
+            const int h = h0 + sub;
+            const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
+            f32x8 y, dz;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = dz[e] = 0.0f;
+            if (h < H) {
+                const unsigned short* dp = is_q ? a.q[rank] + (t * a.Hq + h) * D
+                                         : is_k ? a.k[rank] + (t * a.Hkv + h - a.Hq) * D
+                                                : a.v[rank] + (t * a.Hkv + h - a.Hq - a.Hkv) * D;
+                dz = load8(dp + 8 * i);
+                if (norm && (is_q || is_k)) y = load8(x + h * D + 8 * i);
+            }
+            f32x8 d = turn(r, dz);
+            if (norm) {
+                float s = 0.0f, c = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s += y[e] * y[e];
+                const float inv = 1.0f / sqrtf(row_sum<W>(s) * (1.0f / D) + a.eps);
+                f32x8 n;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    n[e] = y[e] * inv;
+                    if (known && is_q) sq[e] += d[e] * n[e];
+                    if (known && is_k) sk[e] += d[e] * n[e];
+                    d[e] *= is_q ? gq[e] : gk[e];
+                    c += d[e] * n[e];
+                }
+                c = row_sum<W>(c) * (1.0f / D);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) d[e] = (d[e] - n[e] * c) * inv;
+            }
+            if (h < H) store8(dx + h * D + 8 * i, is_q || is_k ? d : dz);
+        }
+    }
+    if (!norm) return;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        sum[wave][sub][0][8 * i + e] = sq[e];
+        sum[wave][sub][1][8 * i + e] = sk[e];
+    }
+    __syncthreads();
+    for (int j = threadIdx.x; j < 2 * D; j += 256) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+#pragma unroll
+            for (int u = 0; u < HW; ++u) s += sum[w][u][j / D][j % D];
+        g.part[(((long long)rank * g.blocks + blockIdx.x) * 2 + j / D) * D + j % D] = s;
+    }
+}
+
+struct GainArgs {
+    const float* part;
+    float *dgq[RING_MAX_RANKS], *dgk[RING_MAX_RANKS];
+    int blocks;
+};
+
+// dgain = the workgroups' partial sums, added in a fixed order: 256 / D
+// interleaved sums per value, then those.
+template <int D>
+__global__ __launch_bounds__(256) void gain_sum_kernel(GainArgs g) {
+    __shared__ float sum[256];
+    const int rank = blockIdx.x, which = blockIdx.y, d = threadIdx.x % D, u = threadIdx.x / D;
+    float s = 0.0f;
+    for (int b = u; b < g.blocks; b += 256 / D) s += g.part[(((long long)rank * g.blocks + b) * 2 + which) * D + d];
+    sum[threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.x < D) {
+        for (int w = 1; w < 256 / D; ++w) s += sum[w * D + d];
+        (which ? g.dgk : g.dgq)[rank][d] = s;
+    }
+}
+
+int rope_shape(int P, int T, int Hq, int Hkv, int D, int rot, long long table_rows, long long cache_rows,
+               long long stride, float eps, int dtype) {
+    if (P < 1 || P > RING_MAX_RANKS || T < 0 || Hq < 1 || Hkv < 1 || table_rows < 0 || cache_rows < 0) return RING_EINVAL;
+    if (!(eps >= 0.0f) || !(eps <= 3.0e38f)) return RING_EINVAL;
+    if (dtype != RING_F32 && dtype != RING_BF16) return RING_EUNSUPPORTED;
+    if ((D != 64 && D != 128) || Hq % Hkv) return RING_EUNSUPPORTED;
+    if (rot < 0 || rot > D || rot % 16) return RING_EINVAL;
+    const long long H = Hq + 2 * (long long)Hkv;
+    if (H * D >= (1LL << 21)) return RING_EUNSUPPORTED;
+    if (stride < H * D || stride >= (1LL << 21) || stride % 8) return RING_EINVAL;
+    return RING_OK;
+}
+
+bool all16(const void* const* p, int P) {
+    for (int r = 0; r < P; ++r)
+        if (!p[r] || ((uintptr_t)p[r] & 15)) return false;
+    return true;
+}
+
+int rope_inputs(RopeArgs& a, const void* const* qkv, const float* const* gain_q, const float* const* gain_k,
+                const float* cos_sin, const int* pos, int P, int rot) {
+    if (!qkv || !all16(qkv, P) || !gain_q != !gain_k || !pos || ((uintptr_t)pos & 3)) return RING_EINVAL;
+    if (gain_q && (!all16((const void* const*)gain_q, P) || !all16((const void* const*)gain_k, P))) return RING_EINVAL;
+    if ((rot && !cos_sin) || ((uintptr_t)cos_sin & 15)) return RING_EINVAL;
+    for (int r = 0; r < P; ++r) {
+        a.qkv[r] = qkv[r];
+        a.gq[r] = gain_q ? gain_q[r] : nullptr;
+        a.gk[r] = gain_k ? gain_k[r] : nullptr;
+    }
+    a.cs = cos_sin;
+    a.pos = pos;
+    a.P = P;
+    a.rot = rot;
+    return RING_OK;
+}
+
+}  // namespace
+}  // namespace ringc
+
+using namespace ringc;
+
+extern "C" int tp_qk_norm_rope(const void* const* qkv, const float* const* gain_q, const float* const* gain_k,
+                               const float* cos_sin, const int* pos, void* const* q, void* const* k, void* const* v,
+                               void* const* k_cache, void* const* v_cache, const long long* slots, int P, int T, int Hq,
+                               int Hkv, int D, int rot, long long table_rows, long long cache_rows, long long qkv_stride,
+                               float eps, int dtype, void* stream) {
+    int rc = rope_shape(P, T, Hq, Hkv, D, rot, table_rows, cache_rows, qkv_stride, eps, dtype);
+    if (rc != RING_OK) return rc;
+    if (!k != !v || !k_cache != !v_cache || !k_cache != !slots || ((uintptr_t)slots & 7)) return RING_EINVAL;
+    if (T == 0) return RING_OK;
+    RopeArgs a;
+    rc = rope_inputs(a, qkv, gain_q, gain_k, cos_sin, pos, P, rot);
+    if (rc != RING_OK) return rc;
+    if (!q || !all16(q, P) || (k && (!all16(k, P) || !all16(v, P))) ||
+        (k_cache && (!all16(k_cache, P) || !all16(v_cache, P))))
+        return RING_EINVAL;
+    for (int r = 0; r < P; ++r) {
+        a.q[r] = (unsigned short*)q[r];
+        a.k[r] = k ? (unsigned short*)k[r] : nullptr;
+        a.v[r] = v ? (unsigned short*)v[r] : nullptr;
+        a.kc[r] = k_cache ? (unsigned short*)k_cache[r] : nullptr;
+        a.vc[r] = v_cache ? (unsigned short*)v_cache[r] : nullptr;
+    }
+    a.slots = slots;
+    a.table_rows = table_rows;
+    a.cache_rows = cache_rows;
+    a.stride = qkv_stride;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.eps = eps;
+    long long blocks = ((long long)P * T + 3) / 4;
+    const long long most = 16LL * dev_info().cus;
+    if (blocks > most) blocks = most;
+    const dim3 grid((unsigned)blocks);
+    hipStream_t s = (hipStream_t)stream;
+    if (dtype == RING_F32) {
+        if (D == 128) hipLaunchKernelGGL((qk_rope_kernel<128, float>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((qk_rope_kernel<64, float>), grid, dim3(256), 0, s, a);
+    } else {
+        if (D == 128) hipLaunchKernelGGL((qk_rope_kernel<128, unsigned short>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((qk_rope_kernel<64, unsigned short>), grid, dim3(256), 0, s, a);
+    }
+    return hipGetLastError() == hipSuccess ? RING_OK : RING_EHIP;
+}
+
+extern "C" size_t tp_qk_norm_rope_grad_workspace_bytes(int P, int D) {
+    if (P < 1 || P > RING_MAX_RANKS || (D != 64 && D != 128)) return 0;
+    return kStatusBytes + (size_t)P * kGradBlocks * 2 * D * sizeof(float);
+}
+
+extern "C" int tp_qk_norm_rope_grad(const void* const* dq, const void* const* dk, const void* const* dv,
+                                    const void* const* qkv, const float* const* gain_q, const float* const* gain_k,
+                                    const float* cos_sin, const int* pos, void* const* dqkv, float* const* dgain_q,
+                                    float* const* dgain_k, int P, int T, int Hq, int Hkv, int D, int rot,
+                                    long long table_rows, long long qkv_stride, float eps, int dtype, void* ws,
+                                    size_t ws_bytes, void* stream) {
+    int rc = rope_shape(P, T, Hq, Hkv, D, rot, table_rows, 0, qkv_stride, eps, dtype);
+    if (rc != RING_OK) return rc;
+    if (gain_q && (!dgain_q || !dgain_k)) return RING_EINVAL;
+    RopeGradArgs g;
+    if (T) {
+        rc = rope_inputs(g.f, qkv, gain_q, gain_k, cos_sin, pos, P, rot);
+        if (rc != RING_OK) return rc;
+        if (!dq || !dk || !dv || !dqkv || !all16(dq, P) || !all16(dk, P) || !all16(dv, P) || !all16(dqkv, P))
+            return RING_EINVAL;
+    } else if (!gain_q) {
+        return RING_OK;
+    }
+    if (gain_q && (!all16((const void* const*)dgain_q, P) || !all16((const void* const*)dgain_k, P))) return RING_EINVAL;
+    if (!ws || ((uintptr_t)ws & 255) || ws_bytes < tp_qk_norm_rope_grad_workspace_bytes(P, D)) return RING_EWORKSPACE;
+    hipStream_t s = (hipStream_t)stream;
+    int blocks = (T + 3) / 4;
+    const int most = (4 * dev_info().cus + P - 1) / P;
+    if (blocks > most) blocks = most;
+    if (blocks > kGradBlocks) blocks = kGradBlocks;
+    g.part = (float*)((char*)ws + kStatusBytes);
+    g.status = (Status*)ws;
+    g.data = WsSpan{kStatusBytes, kStatusBytes + (unsigned long long)P * blocks * 2 * D * sizeof(float)};
+    g.blocks = blocks;
+    if (T) {
+        for (int r = 0; r < P; ++r) {
+            g.f.q[r] = (unsigned short*)const_cast<void*>(dq[r]);
+            g.f.k[r] = (unsigned short*)const_cast<void*>(dk[r]);
+            g.f.v[r] = (unsigned short*)const_cast<void*>(dv[r]);
+            g.dx[r] = dqkv[r];
+        }
+        g.f.table_rows = table_rows;
+        g.f.stride = qkv_stride;
+        g.f.T = T;
+        g.f.Hq = Hq;
+        g.f.Hkv = Hkv;
+        g.f.eps = eps;
+        const dim3 grid((unsigned)blocks, (unsigned)P);
+        if (dtype == RING_F32) {
+            if (D == 128) hipLaunchKernelGGL((qk_rope_grad_kernel<128, float>), grid, dim3(256), 0, s, g);
+            else hipLaunchKernelGGL((qk_rope_grad_kernel<64, float>), grid, dim3(256), 0, s, g);
+        } else {
+            if (D == 128) hipLaunchKernelGGL((qk_rope_grad_kernel<128, unsigned short>), grid, dim3(256), 0, s, g);
+            else hipLaunchKernelGGL((qk_rope_grad_kernel<64, unsigned short>), grid, dim3(256), 0, s, g);
+        }
+        if (hipGetLastError() != hipSuccess) return RING_EHIP;
+    }
+    if (gain_q) {
+        GainArgs w;
+        w.part = g.part;
+        w.blocks = blocks;
+        for (int r = 0; r < P; ++r) {
+            w.dgq[r] = dgain_q[r];
+            w.dgk[r] = dgain_k[r];
+        }
+        const dim3 grid((unsigned)P, 2);
+        if (D == 128) hipLaunchKernelGGL(gain_sum_kernel<128>, grid, dim3(256), 0, s, w);
+        else hipLaunchKernelGGL(gain_sum_kernel<64>, grid, dim3(256), 0, s, w);
+        if (hipGetLastError() != hipSuccess) return RING_EHIP;
+    }
+    return RING_OK;
+}
