@@ -134,6 +134,43 @@ int tp_attention(const void *const *q, const void *const *k, const void *const *
                  long long q_stride, long long k_stride, long long v_stride, long long o_stride, int causal, float scale,
                  void *stream);
 
+/*
+ * Its gradient, from dout[r] (the gradient of o) and tp_attention's inputs
+ * and outputs: dq[r] (Tq rows), dk[r], dv[r] (Tk rows), bf16, with fp32 sums
+ * in a fixed order (the same bits every time).  P and dS = P (dP - sum(dout
+ * o)) are computed again from q, k, v and lse in fp32 and rounded to bf16 for
+ * the products that they enter.  A query that sees no key gives dq = 0 and
+ * adds nothing; a key that no query sees gives dk = dv = 0.
+ */
+int tp_attention_grad(const void *const *dout, const void *const *q, const void *const *k, const void *const *v,
+                      const void *const *o, const float *const *lse, void *const *dq, void *const *dk, void *const *dv,
+                      const int *cu_q, const int *cu_k, int P, int B, int Tq, int Tk, int Hq, int Hkv, int D,
+                      long long q_stride, long long k_stride, long long v_stride, long long o_stride,
+                      long long dout_stride, long long dq_stride, long long dk_stride, long long dv_stride, int causal,
+                      float scale, void *ws, size_t ws_bytes, void *stream);
+size_t tp_attention_grad_workspace_bytes(int P, int Tq, int Hq);
+
+/*
+ * Attention of one query token per request over a paged cache.  q[r], o[r]: B
+ * rows of Hq heads (bf16).  k_cache[r], v_cache[r]: pages * page_size packed
+ * rows of Hkv heads.  Request b's keys are the prefix's, key j at row
+ * prefix_pages[j / page_size] * page_size + j % page_size for j < prefix_len,
+ * shared by all requests, and its own, key j at page block_table[b *
+ * table_stride + j / page_size] likewise for j < lengths[b] (the new token's
+ * row among them, if it is to be seen).  o[r] = softmax(scale q k^T) v over
+ * both; the prefix is read once for all requests.
+ * Lengths are clamped to [0, table_stride * page_size]; keys whose page lies
+ * outside [0, pages) take no part; a request without keys gives o = 0.
+ * pages * page_size and table_stride * page_size stay below 2^31.
+ * scale > 0.  The workspace's size depends on the device's compute units.
+ */
+int tp_attention_decode(const void *const *q, const void *const *k_cache, const void *const *v_cache, void *const *o,
+                        const int *block_table, const int *lengths, const int *prefix_pages, int P, int B, int Hq,
+                        int Hkv, int D, int table_stride, int page_size, int pages, int prefix_len, long long q_stride,
+                        long long o_stride, float scale, void *ws, size_t ws_bytes, void *stream);
+size_t tp_attention_decode_workspace_bytes(int P, int B, int Hq, int Hkv, int D, int table_stride, int page_size,
+                                           int prefix_len);
+
 #ifdef __cplusplus
 }
 #endif

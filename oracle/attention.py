@@ -151,3 +151,15 @@ def attention_grad(do, q, k, v, see, scale):
     edq = ((eds + 2 * n * ads) @ np.abs(k)) * scale + UB * np.abs(dq)
     edk = ((eds + 2 * n * ads).T @ np.abs(q)) * scale + UB * np.abs(dk)
     return (dq, dk, dv), (edq, edk, edv)
+
+
+def decode(q, k_cache, v_cache, table, length, prefix_pages, prefix_len, page_size, scale):
+    """One request and head: o and its bound.  Keys whose page is not in the
+    cache take no part."""
+    pages = k_cache.shape[0] // page_size
+    rows = [(list(prefix_pages), j) for j in range(prefix_len)]
+    rows += [(list(table), j) for j in range(max(0, min(int(length), len(table) * page_size)))]
+    at = [int(p[j // page_size]) * page_size + j % page_size for p, j in rows if 0 <= p[j // page_size] < pages]
+    k, v = k_cache[at], v_cache[at]
+    o, _, eo, _, _, _ = attention(q[None, :], k, v, np.ones((1, len(at)), bool), scale)
+    return o[0], eo[0]

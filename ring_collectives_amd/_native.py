@@ -48,6 +48,10 @@ SIGNATURES = {
     "tp_qk_norm_rope_grad": (_i, [_pp] * 6 + [_vp, _vp, _pp, _pp, _pp] + [_i] * 6 + [_ll, _ll, _f, _i, _vp, _sz, _vp]),
     "tp_qk_norm_rope_grad_workspace_bytes": (_sz, [_i, _i]),
     "tp_attention": (_i, [_pp] * 5 + [_vp, _vp] + [_i] * 7 + [_ll] * 4 + [_i, _f, _vp]),
+    "tp_attention_grad": (_i, [_pp] * 9 + [_vp, _vp] + [_i] * 7 + [_ll] * 8 + [_i, _f, _vp, _sz, _vp]),
+    "tp_attention_grad_workspace_bytes": (_sz, [_i] * 3),
+    "tp_attention_decode": (_i, [_pp] * 4 + [_vp] * 3 + [_i] * 9 + [_ll, _ll, _f, _vp, _sz, _vp]),
+    "tp_attention_decode_workspace_bytes": (_sz, [_i] * 8),
     "ring_last_error": (_i, [_vp, _sz, _vp, ctypes.POINTER(ctypes.c_int)]),
     "ring_strerror": (ctypes.c_char_p, [_i]),
 }

@@ -186,6 +186,10 @@ def tp_qk_norm_rope_grad(dq, dk, dv, qkv, gain_q, gain_k, cos_sin, pos, dqkv, dg
     return ws
 
 
+def _scale(scale, D: int) -> float:
+    return float(scale) if scale is not None else 1.0 / math.sqrt(D) if D else 0.0
+
+
 def _attn(q, k, v, o, cu_q, cu_k, what):
     """Pointers and sizes of a packed-prompt call."""
     P = _lists(what, q, k, v, o)
@@ -215,4 +219,57 @@ def tp_attention(q, k, v, o, cu_q, cu_k, lse=None, causal: bool = True, scale=No
     P, _, Tq, _, Hq, _, D = sizes
     lp = None if lse is None else _rows(lse, what, "lse", P, (Hq, Tq), torch.float32, packed=True)[0]
     N.check(N.lib().tp_attention(qp, kp, vp, op, lp, cq, ck, *sizes, *strides, int(bool(causal)),
-                                 1.0 / math.sqrt(D) if scale is None and D else scale or 0.0, _stream(stream)), what)
+                                 _scale(scale, D), _stream(stream)), what)
+
+
+def tp_attention_grad(do, q, k, v, o, lse, dq, dk, dv, cu_q, cu_k, causal: bool = True, scale=None, ws=None, stream=None):
+    """dq[r], dk[r], dv[r] <- the gradient of tp_attention for do[r], the
+    gradient of o[r], from its inputs and outputs (the same bits every time)."""
+    what = "tp_attention_grad"
+    qp, kp, vp, op, cq, ck, sizes, strides = _attn(q, k, v, o, cu_q, cu_k, what)
+    P, _, Tq, Tk, Hq, Hkv, D = sizes
+    _lists(what, q, do, dq, dk, dv, lse)
+    gp, gs = _rows(do, what, "do", P, (Tq, Hq, D))
+    lp = _rows(lse, what, "lse", P, (Hq, Tq), torch.float32, packed=True)[0]
+    dqp, dqs = _rows(dq, what, "dq", P, (Tq, Hq, D))
+    dkp, dks = _rows(dk, what, "dk", P, (Tk, Hkv, D))
+    dvp, dvs = _rows(dv, what, "dv", P, (Tk, Hkv, D))
+    if ws is None:
+        nb = int(N.lib().tp_attention_grad_workspace_bytes(P, Tq, Hq))
+        ws = _ordered(torch.zeros(max(nb, 256), dtype=torch.uint8, device=q[0].device), stream)
+    N.check(N.lib().tp_attention_grad(gp, qp, kp, vp, op, lp, dqp, dkp, dvp, cq, ck, *sizes, *strides, gs, dqs, dks, dvs,
+                                      int(bool(causal)), _scale(scale, D), *_wsarg(ws, what), _stream(stream)), what)
+    return ws
+
+
+def tp_attention_decode(q, k_cache, v_cache, o, block_table, lengths, page_size: int, prefix_pages=None,
+                        prefix_len: int = 0, scale=None, ws=None, stream=None):
+    """o[r] <- attention of one query token per request, q[r] (B, Hq, D), over
+    the paged cache k_cache[r], v_cache[r] (rows, Hkv, D): the first prefix_len
+    rows of prefix_pages, shared by all requests and read once, and the first
+    lengths[b] rows of block_table[b] (B, W int32)."""
+    what = "tp_attention_decode"
+    P = _lists(what, q, k_cache, v_cache, o)
+    B, Hq, D = _heads(q[0], what, "q")
+    rows, Hkv, _ = _heads(k_cache[0], what, "k_cache")
+    dev = q[0].device
+    qp, qs = _rows(q, what, "q", P, (B, Hq, D))
+    op, os_ = _rows(o, what, "o", P, (B, Hq, D))
+    kp, vp = (_rows(t, what, n, P, (rows, Hkv, D), packed=True)[0] for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")))
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("%s: block_table is (requests, pages), got %s" % (what, tuple(block_table.shape)))
+    tab, lens = _one(block_table, what, "block_table", dev), _one(lengths, what, "lengths", dev, numel=B)
+    if page_size < 1 or rows % page_size:
+        raise ValueError("%s: the cache's %d rows are not whole pages of %d" % (what, rows, page_size))
+    pp = None
+    if prefix_len:
+        if prefix_pages is None or prefix_pages.numel() * page_size < prefix_len:
+            raise ValueError("%s: prefix_pages does not hold %d tokens" % (what, prefix_len))
+        pp = _one(prefix_pages, what, "prefix_pages", dev)
+    W = block_table.shape[1]
+    if ws is None:
+        nb = int(N.lib().tp_attention_decode_workspace_bytes(P, B, Hq, Hkv, D, W, page_size, prefix_len))
+        ws = _ordered(torch.zeros(max(nb, 256), dtype=torch.uint8, device=dev), stream)
+    N.check(N.lib().tp_attention_decode(qp, kp, vp, op, tab, lens, pp, P, B, Hq, Hkv, D, W, page_size, rows // page_size,
+                                        prefix_len, qs, os_, _scale(scale, D), *_wsarg(ws, what), _stream(stream)), what)
+    return ws

@@ -37,6 +37,14 @@ template <int D> struct Rows {
     }
 };
 
+// A view of `rows` rows of D values that start `row_bytes` apart (none for
+// rows <= 0, at most `most`): it ends with the last row's last value.
+template <int D>
+__device__ __forceinline__ rsrc_t rows_view(const unsigned short* base, long long rows, int most, unsigned row_bytes) {
+    const long long n = rows < 0 ? 0 : rows < most ? rows : most;
+    return tile_view(base, n ? (n - 1) * (long long)row_bytes + Rows<D>::RB : 0);
+}
+
 // The direct loads of one wave into tiles of ROWS rows shared by NW waves:
 // wave w issues instructions w J .. w J + J - 1, each filling RPI rows.  Rows
 // past the view's end are filled with zeros by the hardware's bounds check.
@@ -53,20 +61,27 @@ template <int D, int ROWS, int NW> struct TileLoad {
             voff[j] = (unsigned)r * row_bytes + (unsigned)(((lane % Rows<D>::C) ^ Rows<D>::swz(r)) * 16);
         }
     }
-    __device__ __forceinline__ void issue(rsrc_t view, unsigned short* lds, int at) const {
+    // The tile at LDS byte `at` from `rows` rows (at most ROWS of them) on from
+    // base.  For the device pass alone: buffer views have no host type, and the
+    // host pass silently leaves out all but one of the kernel templates that
+    // instantiate a member naming one.
+    __device__ __forceinline__ void issue(const unsigned short* base, long long rows, unsigned row_bytes,
+                                          unsigned short* lds, int at) const {
+#ifdef __HIP_DEVICE_COMPILE__
+        const rsrc_t view = rows_view<D>(base, rows, ROWS, row_bytes);
 #pragma unroll
         for (int j = 0; j < J; ++j)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(view, lds_at(lds, (unsigned)(at + first + j * 1024)), 16, voff[j],
                                                      0, 0, POL_PLAIN);
+#endif
     }
 };
 
-// A view of `rows` rows of D values that start `row_bytes` apart (none for
-// rows <= 0, at most `most`): it ends with the last row's last value.
-template <int D>
-__device__ __forceinline__ rsrc_t rows_view(const unsigned short* base, long long rows, int most, unsigned row_bytes) {
-    const long long n = rows < 0 ? 0 : rows < most ? rows : most;
-    return tile_view(base, n ? (n - 1) * (long long)row_bytes + Rows<D>::RB : 0);
+// `n` floats (at most 64) straight into LDS at byte `at`, one per lane, zeros
+// past them.
+__device__ __forceinline__ void load_floats(const float* p, int n, unsigned short* lds, int at, int lane) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(tile_view(p, n * 4), lds_at(lds, (unsigned)at), 4, (unsigned)lane * 4, 0, 0,
+                                             POL_PLAIN);
 }
 
 // Fragment reads from a tile at byte `at` of LDS (a multiple of 4096).

@@ -1,0 +1,501 @@
+// attn_decode.hip -- attention of one query token per request over a paged
+// cache, with a prefix that every request shares.
+//
+// A request's keys are the prefix's and its own; over any split of them,
+//   m = max of the parts' m,  l = sum l_i 2^(m_i - m),  o = sum o_i 2^(m_i - m) / l
+// gives the whole from parts that hold (m_i, l_i, o_i = sum of weighted
+// values).  One launch makes the parts, a second joins them:
+//   - prefix workgroups: 128 rows (request, head of the group) of one (rank,
+//     key head) against a range of the prefix, whose tiles all rows share, so
+//     the prefix is read once per 128 rows instead of once per request;
+//   - own-key workgroups: one request and (rank, key head), up to 32 heads of
+//     the group, against a range of its own keys; each of the four waves takes
+//     a part of the range through LDS of its own, key and value tiles of 32
+//     rows in flight in turn, and the four results join in LDS.
+// The cache rows read bound it: the ranges are cut so that every compute unit
+// has two workgroups' loads in flight, whatever the number of requests.
+#include "attn_core.h"
+#include "attn_internal.h"
+
+#include <hip/hip_runtime.h>
+
+namespace ringc {
+namespace {
+
+constexpr int kWaves = 4;
+constexpr int kPreRows = 128, kPreKeys = 64;   // prefix: rows of a workgroup, keys of a tile
+constexpr int kOwnKeys = 32;                   // own keys: keys of a wave's tile
+constexpr int kIds = 512;                      // cache rows looked up at a time by a wave
+constexpr int kMaxParts = 64;                  // of each kind
+
+struct DecodeArgs {
+    const unsigned short *q[RING_MAX_RANKS], *kc[RING_MAX_RANKS], *vc[RING_MAX_RANKS];
+    unsigned short* o[RING_MAX_RANKS];
+    const int *table, *lengths, *prefix_pages;
+    long long q_stride, o_stride, kv_stride;
+    int P, B, Hq, Hkv, width, shift, pages, prefix;
+    int pre_parts, own_parts, pre_blocks, row_tiles;   // row_tiles: tiles of 32 heads of the group
+    float c;
+    float* part_o;             // [P Hkv][parts][B G][D]
+    float* part_ml;            // [P Hkv][parts][B G][2]
+    Status* status;
+    WsSpan data;
+};
+
+// The running state of a wave's 32 columns.
+template <int D> struct Soft {
+    f32x16 o[Rows<D>::DB];
+    float mc, l;               // maximum times c, this half's share of the sum
+    __device__ __forceinline__ void init() {
+#pragma unroll
+        for (int db = 0; db < Rows<D>::DB; ++db)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) o[db][v] = 0.0f;
+        mc = -INFINITY;
+        l = 0.0f;
+    }
+    // NB blocks of 32 scores (masked ones -inf) become weights.
+    template <int NB> __device__ __forceinline__ void weigh(f32x16 (&s)[NB], float c) {
+        float mx = s[0][0];
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) mx = fmaxf(mx, s[kb][v]);
+        mx = max_halves(mx) * c;
+        if (__any(mx > mc + 8.0f)) {
+            const float mn = fmaxf(mc, mx);
+            const float alpha = mn == -INFINITY ? 1.0f : exp2_hw(mc - mn);
+            mc = mn;
+            l *= alpha;
+#pragma unroll
+            for (int db = 0; db < Rows<D>::DB; ++db)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) o[db][v] *= alpha;
+        }
+        const float sub = mc == -INFINITY ? 0.0f : mc;
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                s[kb][v] = exp2_hw(__builtin_fmaf(s[kb][v], c, -sub));
+                l += s[kb][v];
+            }
+    }
+};
+
+// One instruction's rows of a gathered tile: row r of the lane at cache row
+// id (none: id < 0, its LDS bytes keep what they hold).
+template <int D>
+__device__ __forceinline__ void gather(const unsigned short* base, long long stride, int id, int r, int lane,
+                                       unsigned short* lds, int at) {
+    if (id >= 0) {
+        const unsigned short* p = base + id * stride + ((lane % Rows<D>::C) ^ Rows<D>::swz(r)) * 8;
+        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p, lds_at(lds, (unsigned)at), 16, 0, 0);
+    }
+}
+
+__device__ __forceinline__ void lds_settled() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+template <int D>
+__global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a) {
+    typedef Rows<D> R;
+    constexpr int kPreBytes = kPreKeys * R::RB, kOwnBytes = kOwnKeys * R::RB;
+    static_assert(4 * kPreBytes == 2 * kWaves * kOwnBytes, "one LDS size for both kinds");
+    __shared__ __align__(4096) unsigned short lds[4 * kPreBytes / 2];
+    __shared__ int ids[kWaves][kIds];
+    __shared__ float wave_ml[kWaves][32][2];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = lane >> 5, col = lane & 31;
+    if (blockIdx.x == 0 && threadIdx.x == 0 && a.part_o) ws_add_data(a.status, a.data);
+    const int units = a.P * a.Hkv, G = a.Hq / a.Hkv;
+    const int parts = a.pre_parts + a.own_parts;
+    const bool pre = (int)blockIdx.x < a.pre_blocks;
+    const int blk = pre ? blockIdx.x : blockIdx.x - a.pre_blocks;
+    const int unit = blk % units, rest = blk / units, rank = unit / a.Hkv, kvh = unit % a.Hkv;
+    const unsigned short* kbase = a.kc[rank] + (long long)kvh * D;
+    const unsigned short* vbase = a.vc[rank] + (long long)kvh * D;
+    const long long all = (long long)a.B * G;
+    Frags<D> fr;
+    fr.init(lane);
+    Soft<D> st;
+    st.init();
+    bf16x8 qf[R::KK];
+    long long m;               // this lane's row (request, head of the group)
+    bool live;
+    int part;
+    auto load_q = [&](long long row) {
+        const int b = (int)(row / G), head = kvh * G + (int)(row % G);
+        const unsigned short* qp = a.q[rank] + b * a.q_stride + (long long)head * D + 8 * half;
+#pragma unroll
+        for (int kk = 0; kk < R::KK; ++kk) qf[kk] = *(const bf16x8*)(qp + 16 * kk);
+    };
+    auto page_row = [&](const int* pages, int key) {      // the cache row of a key, -1 if its page is not one
+        const int p = pages[key >> a.shift];
+        return p >= 0 && p < a.pages ? (int)(((long long)p << a.shift) + (key & ((1 << a.shift) - 1))) : -1;
+    };
+
+    if (pre) {
+        part = rest % a.pre_parts;
+        const int tile = rest / a.pre_parts;
+        const long long m0 = (long long)tile * kPreRows + wave * 32 + col;
+        live = m0 < all;
+        m = live ? m0 : all - 1;
+        load_q(m);
+        const int n = (a.prefix + kPreKeys - 1) / kPreKeys;
+        const int j0 = (int)((long long)n * part / a.pre_parts), j1 = (int)((long long)n * (part + 1) / a.pre_parts);
+        constexpr int J = kPreKeys / R::RPI / kWaves;
+        int id[J];
+        unsigned long long seen_next = 0;
+        unsigned long long seen = 0;
+        auto look_up = [&](int j) {                       // the rows of tile j this lane loads, and which keys there are
+            const int k0 = j * kPreKeys;
+#pragma unroll
+            for (int i = 0; i < J; ++i) {
+                const int key = k0 + (wave * J + i) * R::RPI + lane / R::C;
+                id[i] = key < a.prefix ? page_row(a.prefix_pages, key) : -1;
+            }
+            const int key = k0 + lane;
+            seen_next = __ballot(key < a.prefix && page_row(a.prefix_pages, key) >= 0);
+        };
+        auto load = [&](int buf) {
+#pragma unroll
+            for (int i = 0; i < J; ++i) {
+                const int at = buf * kPreBytes + (wave * J + i) * 1024;
+                if (~seen_next) {                          // rows that no key fills are zeros
+                    const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if (id[i] < 0) {
+                        *(f32x4*)((char*)lds + at + lane * 16) = z;
+                        *(f32x4*)((char*)lds + at + 2 * kPreBytes + lane * 16) = z;
+                    }
+                    lds_settled();
+                }
+                const int r = (wave * J + i) * R::RPI + lane / R::C;
+                gather<D>(kbase, a.kv_stride, id[i], r, lane, lds, at);
+                gather<D>(vbase, a.kv_stride, id[i], r, lane, lds, at + 2 * kPreBytes);
+            }
+        };
+        if (j0 < j1) {
+            look_up(j0);
+            load(0);
+        }
+        for (int j = j0; j < j1; ++j) {
+            const int buf = (j - j0) & 1;
+            seen = seen_next;
+            if (j + 1 < j1) look_up(j + 1);
+            wait_vm(0);
+            lds_barrier();
+            if (j + 1 < j1) load(buf ^ 1);
+            f32x16 s[2];
+#pragma unroll
+            for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+                for (int v = 0; v < 16; ++v) s[kb][v] = 0.0f;
+#pragma unroll
+                for (int kk = 0; kk < R::KK; ++kk)
+                    s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, buf * kPreBytes, kb, kk), qf[kk], s[kb], 0, 0, 0);
+            }
+            if (~seen) {
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v)
+                        if (!((seen >> (kb * 32 + acc_row(v, half))) & 1)) s[kb][v] = -INFINITY;
+            }
+            st.weigh(s, a.c);
+#pragma unroll
+            for (int ks = 0; ks < kPreKeys / 16; ++ks) {
+                const bf16x8 pf = round8(s[ks / 2], ks % 2);
+#pragma unroll
+                for (int db = 0; db < R::DB; ++db)
+                    st.o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, (2 + buf) * kPreBytes, db, ks), pf, st.o[db], 0, 0, 0);
+            }
+        }
+        st.l = sum_halves(st.l);
+    } else {
+        part = a.pre_parts + rest % a.own_parts;
+        const int rt = rest / a.own_parts % a.row_tiles, b = rest / a.own_parts / a.row_tiles;
+        live = rt * 32 + col < G;
+        m = (long long)b * G + (live ? rt * 32 + col : G - 1);
+        load_q(m);
+        const long long room = (long long)a.width << a.shift;
+        const int len0 = a.lengths[b], len = len0 < 0 ? 0 : len0 < room ? len0 : (int)room;
+        const int* pages = a.table + (long long)b * a.width;
+        const int n = (len + kOwnKeys - 1) / kOwnKeys, cuts = a.own_parts * kWaves;
+        const int cut = (part - a.pre_parts) * kWaves + wave;
+        const int j0 = (int)((long long)n * cut / cuts), j1 = (int)((long long)n * (cut + 1) / cuts);
+        const int ka = wave * 2 * kOwnBytes, va = ka + kOwnBytes;
+        constexpr int J = kOwnKeys / R::RPI, kTiles = kIds / kOwnKeys;
+        unsigned seen_next = 0;
+        auto load = [&](const unsigned short* base, int j, int at) {
+            const int* tid = ids[wave] + (j - j0) % kTiles * kOwnKeys;
+            seen_next = (unsigned)__ballot(tid[col] >= 0);
+            const bool whole = seen_next == ~0u;
+#pragma unroll
+            for (int i = 0; i < J; ++i) {
+                const int r = i * R::RPI + lane / R::C, id = tid[r];
+                if (!whole) {
+                    const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if (id < 0) *(f32x4*)((char*)lds + at + i * 1024 + lane * 16) = z;
+                    lds_settled();
+                }
+                gather<D>(base, a.kv_stride, id, r, lane, lds, at + i * 1024);
+            }
+        };
+        auto look_up = [&](int j) {                       // the cache rows of tiles j .. j + kTiles - 1
+            for (int i = lane; i < kIds; i += 64) {
+                const long long key = (long long)j * kOwnKeys + i;
+                ids[wave][i] = key < len ? page_row(pages, (int)key) : -1;
+            }
+            lds_settled();
+        };
+        for (int c0 = j0; c0 < j1; c0 += kTiles) {
+            const int c1 = c0 + kTiles < j1 ? c0 + kTiles : j1;
+            look_up(c0);
+            load(kbase, c0, ka);
+            load(vbase, c0, va);
+            for (int j = c0; j < c1; ++j) {
+                const unsigned seen = seen_next;
+                // The keys of tile j have landed, its values may be in flight:
+                // J loads, unless rows of it are left out and with them, it
+                // may be, whole loads.
+                wait_vm(~seen ? 0 : J);
+                f32x16 s[1];
+#pragma unroll
+                for (int v = 0; v < 16; ++v) s[0][v] = 0.0f;
+#pragma unroll
+                for (int kk = 0; kk < R::KK; ++kk)
+                    s[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, ka, 0, kk), qf[kk], s[0], 0, 0, 0);
+                lds_settled();
+                if (j + 1 < c1) load(kbase, j + 1, ka);
+                if (~seen) {
+#pragma unroll
+                    for (int v = 0; v < 16; ++v)
+                        if (!((seen >> acc_row(v, half)) & 1)) s[0][v] = -INFINITY;
+                }
+                st.weigh(s, a.c);
+                wait_vm(j + 1 < c1 && !~seen_next ? J : 0);   // its values have; the next keys may be in flight
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    const bf16x8 pf = round8(s[0], ks);
+#pragma unroll
+                    for (int db = 0; db < R::DB; ++db)
+                        st.o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, va, db, ks), pf, st.o[db], 0, 0, 0);
+                }
+                lds_settled();
+                if (j + 1 < c1) load(vbase, j + 1, va);
+            }
+        }
+        // join the four waves in LDS: every wave's share in turn goes through
+        // [d][column] floats at the wave's own tiles
+        st.l = sum_halves(st.l);
+        if (half == 0) {
+            wave_ml[wave][col][0] = st.mc;
+            wave_ml[wave][col][1] = st.l;
+        }
+        float* mine = (float*)((char*)lds + ka);
+        static_assert(D * 32 * 4 <= 2 * kOwnBytes, "a wave's output fits its tiles");
+#pragma unroll
+        for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) mine[(32 * db + acc_row(v, half)) * 32 + col] = st.o[db][v];
+        __syncthreads();
+        if (wave) return;
+        float mx = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, wave_ml[w][col][0]);
+        float f[kWaves];
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            f[w] = mx == -INFINITY ? 0.0f : exp2_hw(wave_ml[w][col][0] - mx);
+            l += f[w] * wave_ml[w][col][1];
+        }
+        st.mc = mx;
+        st.l = l;
+#pragma unroll
+        for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                float x = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w)
+                    x += f[w] * ((const float*)((const char*)lds + w * 2 * kOwnBytes))[(32 * db + acc_row(v, half)) * 32 + col];
+                st.o[db][v] = x;
+            }
+    }
+
+    if (!live) return;
+    if (!a.part_o) {                                      // one part in all: the result itself
+        const int b = (int)(m / G), head = kvh * G + (int)(m % G);
+        const float inv = st.l == 0.0f ? 0.0f : 1.0f / st.l;
+        unsigned short* op = a.o[rank] + b * a.o_stride + (long long)head * D + 4 * half;
+#pragma unroll
+        for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+            for (int v = 0; v < 16; v += 4) {
+                typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+                const f32x4 y = {st.o[db][v] * inv, st.o[db][v + 1] * inv, st.o[db][v + 2] * inv, st.o[db][v + 3] * inv};
+                *(bf16x4*)(op + 32 * db + 2 * v) = __builtin_convertvector(y, bf16x4);
+            }
+        return;
+    }
+    const long long at = ((long long)unit * parts + part) * all + m;
+    float* po = a.part_o + at * D + 4 * half;
+#pragma unroll
+    for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+        for (int v = 0; v < 16; v += 4)
+            *(f32x4*)(po + 32 * db + 2 * v) = f32x4{st.o[db][v], st.o[db][v + 1], st.o[db][v + 2], st.o[db][v + 3]};
+    if (half == 0) {
+        a.part_ml[2 * at] = st.mc;
+        a.part_ml[2 * at + 1] = st.l;
+    }
+}
+
+// The parts of every row, joined: D / 4 lanes hold a row.
+template <int D>
+__global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
+    constexpr int L = D / 4;
+    const int parts = a.pre_parts + a.own_parts, G = a.Hq / a.Hkv, units = a.P * a.Hkv;
+    const long long all = (long long)a.B * G;
+    const long long row = (long long)blockIdx.x * (256 / L) + threadIdx.x / L;
+    if (row >= all * units) return;
+    const int unit = (int)(row / all), i = threadIdx.x % L;
+    const long long m = row % all, first = (long long)unit * parts * all + m;
+    float mx = -INFINITY;
+    for (int p = 0; p < parts; ++p) mx = fmaxf(mx, a.part_ml[2 * (first + p * all)]);
+    f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f};
+    float l = 0.0f;
+    for (int p = 0; p < parts; ++p) {
+        const long long at = first + p * all;
+        const float w = mx == -INFINITY ? 0.0f : exp2_hw(a.part_ml[2 * at] - mx);
+        l += w * a.part_ml[2 * at + 1];
+        const f32x4 y = *(const f32x4*)(a.part_o + at * D + 4 * i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] += w * y[e];
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] *= inv;
+    typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+    const int rank = unit / a.Hkv, head = unit % a.Hkv * G + (int)(m % G);
+    *(bf16x4*)(a.o[rank] + m / G * a.o_stride + (long long)head * D + 4 * i) = __builtin_convertvector(x, bf16x4);
+}
+
+struct Cuts {
+    int pre, own, row_tiles;
+    long long pre_tiles;
+};
+
+// Parts of the prefix and of the own keys.  Two workgroups run on a compute
+// unit: each kind is cut until it alone would fill them, as far as every
+// prefix part keeps four tiles and every wave of an own-key part two.
+Cuts decode_cuts(int P, int B, int Hq, int Hkv, int width, int page, int prefix, int cus) {
+    Cuts c;
+    const long long units = (long long)P * Hkv, G = Hq / Hkv;
+    c.row_tiles = (int)((G + 31) / 32);
+    c.pre_tiles = (B * G + kPreRows - 1) / kPreRows;
+    auto cut = [&](long long blocks, long long tiles, int per) {
+        long long n = (2LL * cus + blocks - 1) / blocks;
+        const long long most = tiles / per;
+        if (n > most) n = most;
+        if (n > kMaxParts) n = kMaxParts;
+        return (int)(n < 1 ? 1 : n);
+    };
+    c.pre = prefix ? cut(units * c.pre_tiles, (prefix + kPreKeys - 1) / kPreKeys, 4) : 0;
+    c.own = cut(units * B * c.row_tiles, ((long long)width * page + kOwnKeys - 1) / kOwnKeys, 2 * kWaves);
+    return c;
+}
+
+size_t decode_ws(int P, int B, int Hq, int Hkv, int D, const Cuts& c) {
+    const size_t parts = (size_t)c.pre + c.own;
+    if (parts < 2) return kStatusBytes;
+    return kStatusBytes + (parts * P * B * Hq * (D + 2) * sizeof(float) + 255) / 256 * 256;
+}
+
+bool decode_shape(int P, int B, int Hq, int Hkv, int D, int width, int page, int prefix) {
+    return P >= 1 && P <= RING_MAX_RANKS && B >= 0 && Hq >= 1 && Hkv >= 1 && width >= 0 && prefix >= 0 && page >= 1 &&
+           !(page & (page - 1)) && page <= (1 << 20) && Hq % Hkv == 0 && (D == 64 || D == 128) &&
+           (long long)Hq * D < kMaxRow && (long long)width * page < (1LL << 31) && B <= (1 << 20);
+}
+
+}  // namespace
+}  // namespace ringc
+
+using namespace ringc;
+
+extern "C" size_t tp_attention_decode_workspace_bytes(int P, int B, int Hq, int Hkv, int D, int table_stride,
+                                                      int page_size, int prefix_len) {
+    if (!decode_shape(P, B, Hq, Hkv, D, table_stride, page_size, prefix_len)) return 0;
+    return decode_ws(P, B, Hq, Hkv, D, decode_cuts(P, B ? B : 1, Hq, Hkv, table_stride, page_size, prefix_len, dev_info().cus));
+}
+
+extern "C" int tp_attention_decode(const void* const* q, const void* const* k_cache, const void* const* v_cache,
+                                   void* const* o, const int* block_table, const int* lengths, const int* prefix_pages,
+                                   int P, int B, int Hq, int Hkv, int D, int table_stride, int page_size, int pages,
+                                   int prefix_len, long long q_stride, long long o_stride, float scale, void* ws,
+                                   size_t ws_bytes, void* stream) {
+    if (P < 1 || P > RING_MAX_RANKS || B < 0 || Hq < 1 || Hkv < 1 || table_stride < 0 || pages < 0 || prefix_len < 0)
+        return RING_EINVAL;
+    if (page_size < 1 || (page_size & (page_size - 1)) || page_size > (1 << 20)) return RING_EINVAL;
+    if (!(scale > 0.0f) || !(scale <= 3.0e38f)) return RING_EINVAL;
+    if (!decode_shape(P, B, Hq, Hkv, D, table_stride, page_size, prefix_len) || (long long)pages * page_size >= (1LL << 31))
+        return RING_EUNSUPPORTED;
+    if (!row_stride_ok(q_stride, Hq, D) || !row_stride_ok(o_stride, Hq, D)) return RING_EINVAL;
+    if (B == 0) return RING_OK;
+    if (!q || !k_cache || !v_cache || !o || !lengths || ((uintptr_t)lengths & 3) || (table_stride && !block_table) ||
+        ((uintptr_t)block_table & 3) || (prefix_len && !prefix_pages) || ((uintptr_t)prefix_pages & 3))
+        return RING_EINVAL;
+    DecodeArgs a;
+    for (int r = 0; r < P; ++r) {
+        if (!q[r] || !o[r] || (pages && (!k_cache[r] || !v_cache[r]))) return RING_EINVAL;
+        if (((uintptr_t)q[r] | (uintptr_t)o[r] | (uintptr_t)k_cache[r] | (uintptr_t)v_cache[r]) & 15) return RING_EINVAL;
+        a.q[r] = (const unsigned short*)q[r];
+        a.kc[r] = (const unsigned short*)k_cache[r];
+        a.vc[r] = (const unsigned short*)v_cache[r];
+        a.o[r] = (unsigned short*)o[r];
+    }
+    const Cuts c = decode_cuts(P, B, Hq, Hkv, table_stride, page_size, prefix_len, dev_info().cus);
+    const size_t need = decode_ws(P, B, Hq, Hkv, D, c);
+    if (!ws || ((uintptr_t)ws & 255) || ws_bytes < need) return RING_EWORKSPACE;
+    const int units = P * Hkv;
+    const long long pre = c.pre_tiles * c.pre * units, own = (long long)B * c.row_tiles * c.own * units;
+    if (pre + own >= (1LL << 31)) return RING_EUNSUPPORTED;
+    a.table = block_table;
+    a.lengths = lengths;
+    a.prefix_pages = prefix_pages;
+    a.q_stride = q_stride;
+    a.o_stride = o_stride;
+    a.kv_stride = (long long)Hkv * D;
+    a.P = P;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.width = table_stride;
+    a.shift = 0;
+    while ((1 << a.shift) < page_size) ++a.shift;
+    a.pages = pages;
+    a.prefix = prefix_len;
+    a.pre_parts = c.pre;
+    a.own_parts = c.own;
+    a.pre_blocks = (int)pre;
+    a.row_tiles = c.row_tiles;
+    a.c = scale * kLog2e;
+    const bool join = c.pre + c.own > 1;
+    a.part_o = join ? (float*)((char*)ws + kStatusBytes) : nullptr;
+    a.part_ml = join ? a.part_o + (size_t)(c.pre + c.own) * P * B * Hq * D : nullptr;
+    a.status = (Status*)ws;
+    a.data = WsSpan{kStatusBytes, need};
+    hipStream_t s = (hipStream_t)stream;
+    const dim3 grid((unsigned)(pre + own));
+    if (D == 128) hipLaunchKernelGGL(attn_decode_kernel<128>, grid, dim3(256), 0, s, a);
+    else hipLaunchKernelGGL(attn_decode_kernel<64>, grid, dim3(256), 0, s, a);
+    if (hipGetLastError() != hipSuccess) return RING_EHIP;
+    if (join) {
+        const int per = 256 / (D / 4);
+        const dim3 jg((unsigned)(((long long)P * B * Hq + per - 1) / per));
+        if (D == 128) hipLaunchKernelGGL(attn_join_kernel<128>, jg, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL(attn_join_kernel<64>, jg, dim3(256), 0, s, a);
+        if (hipGetLastError() != hipSuccess) return RING_EHIP;
+    }
+    return RING_OK;
+}

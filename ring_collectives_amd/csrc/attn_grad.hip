@@ -1,0 +1,357 @@
+// attn_grad.hip -- gradient of the packed-prompt attention.
+//
+//   P = exp(S - lse),  delta = sum(dO O),  dP = dO V^T,  dS = P (dP - delta),
+//   dQ = scale dS K,   dK = scale dS^T Q,  dV = P^T dO.
+//
+// Two passes, each summing its results in registers in a fixed order: one per
+// 128 query rows over the keys (dQ; it also leaves lse and delta of its rows
+// in the workspace), one per 128 keys over the queries of every head of the
+// group (dK, dV).  S and dP are computed in both, seven products in all where
+// five would do, but no result is added up through memory: no atomics, whose
+// order would change the results, and no fp32 copy of dQ.
+#include "attn_core.h"
+#include "attn_internal.h"
+
+#include <hip/hip_runtime.h>
+
+namespace ringc {
+namespace {
+
+constexpr int kRowsWG = 128;   // query rows, or keys, of a workgroup
+constexpr int kStep = 64;      // keys, or queries, of a tile
+constexpr int kWaves = 4;
+
+struct GradArgs {
+    PromptArgs p;
+    const unsigned short *o[RING_MAX_RANKS], *go[RING_MAX_RANKS];
+    const float* lse[RING_MAX_RANKS];
+    unsigned short *dq[RING_MAX_RANKS], *dk[RING_MAX_RANKS], *dv[RING_MAX_RANKS];
+    long long o_stride, go_stride, dq_stride, dk_stride, dv_stride;
+    float* lse2;               // [P][Hq][Tq] lse log2(e), +inf for a row that sees no key
+    float* delta;              // [P][Hq][Tq]
+    Status* status;
+    WsSpan data;
+    float scale;
+    int slots;
+};
+
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+// Store the lane's column of a D x 32 block of accumulators, times f, as bf16.
+template <int D, class Acc>
+__device__ __forceinline__ void store_column(unsigned short* p, const Acc& x, float f) {
+#pragma unroll
+    for (int db = 0; db < Rows<D>::DB; ++db)
+#pragma unroll
+        for (int v = 0; v < 16; v += 4) {
+            const f32x4 y = {x[db][v] * f, x[db][v + 1] * f, x[db][v + 2] * f, x[db][v + 3] * f};
+            *(bf16x4*)(p + 32 * db + 2 * v) = __builtin_convertvector(y, bf16x4);
+        }
+}
+
+template <int D>
+__global__ __launch_bounds__(256, 2) void attn_dq_kernel(GradArgs a) {
+    typedef Rows<D> R;
+    constexpr int kTileBytes = kStep * R::RB;
+    __shared__ __align__(4096) unsigned short lds[4 * kTileBytes / 2];   // K 0, K 1, V 0, V 1
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = lane >> 5;
+    if (blockIdx.x == 0 && threadIdx.x == 0) ws_add_data(a.status, a.data);
+    int unit, slot;
+    unit_slot(a.p.P * a.p.Hkv, a.slots, blockIdx.x, unit, slot);
+    const int G = a.p.Hq / a.p.Hkv, rank = unit / a.p.Hkv, kvh = unit % a.p.Hkv;
+    PromptTile pt;
+    if (!find_tile(a.p.cu_q, a.p.B, a.p.Tq, G, kRowsWG, slot, lane, pt)) return;
+    const int b = pt.b, tile = pt.tiles - 1 - pt.tile;
+    const int q0 = clamp_cu(a.p.cu_q[b], a.p.Tq), nq = clamp_cu(a.p.cu_q[b + 1], a.p.Tq) - q0;
+    const int k0 = clamp_cu(a.p.cu_k[b], a.p.Tk), k1 = clamp_cu(a.p.cu_k[b + 1], a.p.Tk);
+    const int nk = k1 > k0 ? k1 - k0 : 0;
+    const long long rows = (long long)nq * G;
+    const long long m0 = (long long)tile * kRowsWG + wave * 32;
+    const long long m = m0 + (lane & 31) < rows ? m0 + (lane & 31) : rows - 1;
+    const int qi = (int)(m / G), head = kvh * G + (int)(m % G);
+    const int off = nk - nq;
+    int seen = nk, every = nk, some = nk, most = nk;
+    if (a.p.causal) {
+        auto upto = [&](long long row) {
+            const long long s = (row < rows ? row : rows - 1) / G + off + 1;
+            return (int)(s < 0 ? 0 : s < nk ? s : nk);
+        };
+        seen = upto(m);
+        every = upto(m0);
+        some = upto(m0 + 31);
+        most = upto((long long)tile * kRowsWG + kRowsWG - 1);
+    }
+
+    bf16x8 qf[R::KK], gf[R::KK];
+    float delta = 0.0f;
+    {
+        const long long t = q0 + (long long)qi;
+        const unsigned short* qp = a.p.q[rank] + t * a.p.q_stride + (long long)head * D + 8 * half;
+        const unsigned short* op = a.o[rank] + t * a.o_stride + (long long)head * D + 8 * half;
+        const unsigned short* gp = a.go[rank] + t * a.go_stride + (long long)head * D + 8 * half;
+#pragma unroll
+        for (int kk = 0; kk < R::KK; ++kk) {
+            qf[kk] = *(const bf16x8*)(qp + 16 * kk);
+            gf[kk] = *(const bf16x8*)(gp + 16 * kk);
+            const bf16x8 of = *(const bf16x8*)(op + 16 * kk);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) delta = __builtin_fmaf((float)gf[kk][e], (float)of[e], delta);
+        }
+        delta = sum_halves(delta);
+    }
+    const long long at = ((long long)rank * a.p.Hq + head) * a.p.Tq + q0 + qi;
+    float lse2 = a.lse[rank][(long long)head * a.p.Tq + q0 + qi] * kLog2e;
+    if (lse2 == -INFINITY) lse2 = INFINITY;              // no key seen: every weight is 0
+    if (half == 0 && m0 + (lane & 31) < rows) {
+        a.lse2[at] = lse2;
+        a.delta[at] = delta;
+    }
+
+    const unsigned krow = (unsigned)(a.p.k_stride * 2), vrow = (unsigned)(a.p.v_stride * 2);
+    const unsigned short* kp = a.p.k[rank] + (long long)k0 * a.p.k_stride + (long long)kvh * D;
+    const unsigned short* vp = a.p.v[rank] + (long long)k0 * a.p.v_stride + (long long)kvh * D;
+    TileLoad<D, kStep, kWaves> kl, vl;
+    kl.init(lane, wave, krow);
+    vl.init(lane, wave, vrow);
+    Frags<D> fr;
+    fr.init(lane);
+    auto load = [&](int j, int buf) {
+        kl.issue(kp + (long long)j * kStep * a.p.k_stride, nk - (long long)j * kStep, krow, lds, buf * kTileBytes);
+        vl.issue(vp + (long long)j * kStep * a.p.v_stride, nk - (long long)j * kStep, vrow, lds, (2 + buf) * kTileBytes);
+    };
+    f32x16 dq[R::DB];
+#pragma unroll
+    for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) dq[db][v] = 0.0f;
+    const float c = a.p.c;
+    const int tiles = (most + kStep - 1) / kStep;
+    if (tiles) load(0, 0);
+    for (int j = 0; j < tiles; ++j) {
+        const int buf = j & 1;
+        wait_vm(0);
+        lds_barrier();
+        if (j + 1 < tiles) load(j + 1, buf ^ 1);
+        if (j * kStep >= some) continue;
+        const int ka = buf * kTileBytes, va = (2 + buf) * kTileBytes;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            f32x16 s, dp;
+#pragma unroll
+            for (int v = 0; v < 16; ++v) s[v] = dp[v] = 0.0f;
+#pragma unroll
+            for (int kk = 0; kk < R::KK; ++kk) {
+                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, ka, kb, kk), qf[kk], s, 0, 0, 0);
+                dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, va, kb, kk), gf[kk], dp, 0, 0, 0);
+            }
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const float p = exp2_hw(__builtin_fmaf(s[v], c, -lse2));
+                s[v] = p * (dp[v] - delta);
+            }
+            if ((j + 1) * kStep > every) {
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+                    if (j * kStep + kb * 32 + acc_row(v, half) >= seen) s[v] = 0.0f;
+            }
+            // dS is rounded to bf16 for the matrix cores, as P is going forward
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const bf16x8 sf = round8(s, ks);
+#pragma unroll
+                for (int db = 0; db < R::DB; ++db)
+                    dq[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, ka, db, 2 * kb + ks), sf, dq[db], 0, 0, 0);
+            }
+        }
+    }
+    if (m0 + (lane & 31) >= rows) return;
+    store_column<D>(a.dq[rank] + (q0 + (long long)qi) * a.dq_stride + (long long)head * D + 4 * half, dq, a.scale);
+}
+
+template <int D>
+__global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_kernel(GradArgs a) {
+    typedef Rows<D> R;
+    constexpr int kTileBytes = kStep * R::RB;
+    // Q 0, Q 1, dO 0, dO 1, then lse and delta of each buffer's rows
+    __shared__ __align__(4096) unsigned short lds[(4 * kTileBytes + 4 * kStep * 4) / 2];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = lane >> 5;
+    int unit, slot;
+    unit_slot(a.p.P * a.p.Hkv, a.slots, blockIdx.x, unit, slot);
+    const int G = a.p.Hq / a.p.Hkv, rank = unit / a.p.Hkv, kvh = unit % a.p.Hkv;
+    PromptTile pt;
+    if (!find_tile(a.p.cu_k, a.p.B, a.p.Tk, 1, kRowsWG, slot, lane, pt)) return;
+    const int b = pt.b, tile = pt.tile;                   // the first keys are seen by the most queries
+    const int k0 = clamp_cu(a.p.cu_k[b], a.p.Tk), nk = clamp_cu(a.p.cu_k[b + 1], a.p.Tk) - k0;
+    const int q0 = clamp_cu(a.p.cu_q[b], a.p.Tq), q1 = clamp_cu(a.p.cu_q[b + 1], a.p.Tq);
+    const int nq = q1 > q0 ? q1 - q0 : 0, off = nk - nq;
+    const int key0 = tile * kRowsWG + wave * 32;          // this wave's first key
+    const int key = key0 + (lane & 31), keyc = key < nk ? key : nk - 1;
+
+    bf16x8 kf[R::KK], vf[R::KK];
+    {
+        const unsigned short* kp = a.p.k[rank] + (k0 + (long long)keyc) * a.p.k_stride + (long long)kvh * D + 8 * half;
+        const unsigned short* vp = a.p.v[rank] + (k0 + (long long)keyc) * a.p.v_stride + (long long)kvh * D + 8 * half;
+#pragma unroll
+        for (int kk = 0; kk < R::KK; ++kk) {
+            kf[kk] = *(const bf16x8*)(kp + 16 * kk);
+            vf[kk] = *(const bf16x8*)(vp + 16 * kk);
+        }
+    }
+    // query i sees key j when i >= j - off
+    const int first = a.p.causal ? tile * kRowsWG - off : 0;          // first query that sees a key of the workgroup
+    const int t0 = first > 0 ? first / kStep : 0, t1 = (nq + kStep - 1) / kStep;
+    const int per = t1 > t0 ? t1 - t0 : 0, total = per * G;            // tiles of a head, of the group
+    const unsigned qrow = (unsigned)(a.p.q_stride * 2), grow = (unsigned)(a.go_stride * 2);
+    TileLoad<D, kStep, kWaves> ql, gl;
+    ql.init(lane, wave, qrow);
+    gl.init(lane, wave, grow);
+    Frags<D> fr;
+    fr.init(lane);
+    int lg = 0, lt = t0;                                               // the next tile to load: head of the group, tile
+    auto load = [&](int buf) {
+        const int head = kvh * G + lg;
+        const long long t = q0 + (long long)lt * kStep;
+        const long long left = nq - (long long)lt * kStep;
+        ql.issue(a.p.q[rank] + t * a.p.q_stride + (long long)head * D, left, qrow, lds, buf * kTileBytes);
+        gl.issue(a.go[rank] + t * a.go_stride + (long long)head * D, left, grow, lds, (2 + buf) * kTileBytes);
+        if (wave < 2) {                                                // wave 0: lse, wave 1: delta, one value per lane
+            const float* st = (wave ? a.delta : a.lse2) + ((long long)rank * a.p.Hq + head) * a.p.Tq + t;
+            load_floats(st, left < kStep ? (int)left : kStep, lds, 4 * kTileBytes + (2 * buf + wave) * kStep * 4, lane);
+        }
+        if (++lt == t1) {
+            lt = t0;
+            ++lg;
+        }
+    };
+    f32x16 dk[R::DB], dv[R::DB];
+#pragma unroll
+    for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) dk[db][v] = dv[db][v] = 0.0f;
+    const float c = a.p.c;
+    if (total) load(0);
+    int ct = t0;                                                       // the tile being computed
+    for (int it = 0; it < total; ++it) {
+        const int buf = it & 1;
+        wait_vm(0);
+        lds_barrier();
+        if (it + 1 < total) load(buf ^ 1);
+        const int q = ct * kStep;
+        if (++ct == t1) ct = t0;
+        const int qa = buf * kTileBytes, ga = (2 + buf) * kTileBytes;
+        const float* stat = (const float*)((const char*)lds + 4 * kTileBytes + 2 * buf * kStep * 4);
+#pragma unroll
+        for (int qb = 0; qb < kStep / 32; ++qb) {
+            const int qr = q + qb * 32;
+            if (a.p.causal && qr + 31 + off < key0) continue;          // none of these queries sees a key of the wave
+            f32x16 s, dp;
+#pragma unroll
+            for (int v = 0; v < 16; ++v) s[v] = dp[v] = 0.0f;
+#pragma unroll
+            for (int kk = 0; kk < R::KK; ++kk) {
+                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, qa, qb, kk), kf[kk], s, 0, 0, 0);
+                dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, ga, qb, kk), vf[kk], dp, 0, 0, 0);
+            }
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int r = qb * 32 + acc_row(v, half);
+                s[v] = exp2_hw(__builtin_fmaf(s[v], c, -stat[r]));
+                dp[v] = s[v] * (dp[v] - stat[kStep + r]);
+            }
+            if (a.p.causal && qr + off < key0 + 31) {
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+                    if (qr + acc_row(v, half) + off < key) s[v] = dp[v] = 0.0f;
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const bf16x8 pf = round8(s, ks), sf = round8(dp, ks);
+#pragma unroll
+                for (int db = 0; db < R::DB; ++db) {
+                    dv[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, ga, db, 2 * qb + ks), pf, dv[db], 0, 0, 0);
+                    dk[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, qa, db, 2 * qb + ks), sf, dk[db], 0, 0, 0);
+                }
+            }
+        }
+    }
+    if (key >= nk) return;
+    store_column<D>(a.dk[rank] + (k0 + (long long)key) * a.dk_stride + (long long)kvh * D + 4 * half, dk, a.scale);
+    store_column<D>(a.dv[rank] + (k0 + (long long)key) * a.dv_stride + (long long)kvh * D + 4 * half, dv, 1.0f);
+}
+
+}  // namespace
+}  // namespace ringc
+
+using namespace ringc;
+
+extern "C" size_t tp_attention_grad_workspace_bytes(int P, int Tq, int Hq) {
+    if (P < 1 || P > RING_MAX_RANKS || Tq < 0 || Hq < 1) return 0;
+    return kStatusBytes + ((size_t)P * Hq * Tq * 2 * sizeof(float) + 255) / 256 * 256;
+}
+
+extern "C" int tp_attention_grad(const void* const* dout, const void* const* q, const void* const* k, const void* const* v,
+                                 const void* const* o, const float* const* lse, void* const* dq, void* const* dk,
+                                 void* const* dv, const int* cu_q, const int* cu_k, int P, int B, int Tq, int Tk, int Hq,
+                                 int Hkv, int D, long long q_stride, long long k_stride, long long v_stride,
+                                 long long o_stride, long long dout_stride, long long dq_stride, long long dk_stride,
+                                 long long dv_stride, int causal, float scale, void* ws, size_t ws_bytes, void* stream) {
+    int rc = prompt_shape(P, B, Tq, Tk, Hq, Hkv, D, scale);
+    if (rc != RING_OK) return rc;
+    if (!dout || !q || !k || !v || !o || !lse || !dq || !dk || !dv) return RING_EINVAL;
+    if (!row_stride_ok(q_stride, Hq, D) || !row_stride_ok(k_stride, Hkv, D) || !row_stride_ok(v_stride, Hkv, D) ||
+        !row_stride_ok(o_stride, Hq, D) || !row_stride_ok(dout_stride, Hq, D) || !row_stride_ok(dq_stride, Hq, D) ||
+        !row_stride_ok(dk_stride, Hkv, D) || !row_stride_ok(dv_stride, Hkv, D))
+        return RING_EINVAL;
+    if (B == 0 || (Tq == 0 && Tk == 0)) return RING_OK;
+    if (!cu_q || !cu_k) return RING_EINVAL;
+    GradArgs a;
+    if (!fill_prompt_args(a.p, q, k, v, cu_q, cu_k, P, B, Tq, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride,
+                          causal ? 1 : 0, scale))
+        return RING_EINVAL;
+    for (int r = 0; r < P; ++r) {
+        if (Tq && (!o[r] || !dout[r] || !lse[r] || !dq[r])) return RING_EINVAL;
+        if (Tk && (!dk[r] || !dv[r])) return RING_EINVAL;
+        if ((((uintptr_t)o[r] | (uintptr_t)dout[r] | (uintptr_t)dq[r] | (uintptr_t)dk[r] | (uintptr_t)dv[r]) & 15) ||
+            ((uintptr_t)lse[r] & 3))
+            return RING_EINVAL;
+        a.o[r] = (const unsigned short*)o[r];
+        a.go[r] = (const unsigned short*)dout[r];
+        a.lse[r] = lse[r];
+        a.dq[r] = (unsigned short*)dq[r];
+        a.dk[r] = (unsigned short*)dk[r];
+        a.dv[r] = (unsigned short*)dv[r];
+    }
+    const size_t need = tp_attention_grad_workspace_bytes(P, Tq, Hq);
+    if (!ws || ((uintptr_t)ws & 255) || ws_bytes < need) return RING_EWORKSPACE;
+    a.o_stride = o_stride;
+    a.go_stride = dout_stride;
+    a.dq_stride = dq_stride;
+    a.dk_stride = dk_stride;
+    a.dv_stride = dv_stride;
+    a.lse2 = (float*)((char*)ws + kStatusBytes);
+    a.delta = a.lse2 + (size_t)P * Hq * Tq;
+    a.status = (Status*)ws;
+    a.data = WsSpan{kStatusBytes, need};
+    a.scale = scale;
+    const int units = P * Hkv;
+    hipStream_t s = (hipStream_t)stream;
+    if (Tq) {
+        a.slots = prompt_slots(B, Tq, Hq / Hkv, kRowsWG, units);
+        if (!a.slots || (Tk && !prompt_slots(B, Tk, 1, kRowsWG, units))) return RING_EUNSUPPORTED;
+        const dim3 grid((unsigned)a.slots * (unsigned)units);
+        if (D == 128) hipLaunchKernelGGL(attn_dq_kernel<128>, grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL(attn_dq_kernel<64>, grid, dim3(256), 0, s, a);
+        if (hipGetLastError() != hipSuccess) return RING_EHIP;
+    }
+    if (Tk) {
+        a.slots = prompt_slots(B, Tk, 1, kRowsWG, units);
+        if (!a.slots) return RING_EUNSUPPORTED;
+        const dim3 grid((unsigned)a.slots * (unsigned)units);
+        if (D == 128) hipLaunchKernelGGL(attn_dkv_kernel<128>, grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL(attn_dkv_kernel<64>, grid, dim3(256), 0, s, a);
+        if (hipGetLastError() != hipSuccess) return RING_EHIP;
+    }
+    return RING_OK;
+}

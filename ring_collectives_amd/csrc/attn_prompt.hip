@@ -82,10 +82,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
     Frags<D> fr;
     fr.init(lane);
     auto load = [&](int j, int buf) {
-        kl.issue(rows_view<D>(kp + (long long)j * kTileKeys * a.p.k_stride, nk - (long long)j * kTileKeys, kTileKeys, krow), lds,
-                 buf * kTileBytes);
-        vl.issue(rows_view<D>(vp + (long long)j * kTileKeys * a.p.v_stride, nk - (long long)j * kTileKeys, kTileKeys, vrow), lds,
-                 (2 + buf) * kTileBytes);
+        kl.issue(kp + (long long)j * kTileKeys * a.p.k_stride, nk - (long long)j * kTileKeys, krow, lds, buf * kTileBytes);
+        vl.issue(vp + (long long)j * kTileKeys * a.p.v_stride, nk - (long long)j * kTileKeys, vrow, lds, (2 + buf) * kTileBytes);
     };
 
     f32x16 o[R::DB];

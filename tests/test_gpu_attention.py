@@ -287,3 +287,155 @@ def test_attention_offsets_outside_the_tensors_are_not_followed():
     A.tp_attention(q, k, v, o, i32([-5, 20, 10, 1000]), i32([0, 20, 1 << 30, 60]), lse=lse)
     torch.cuda.synchronize()
     check_attention([q[0][:20]], [k[0][:20]], [v[0][:20]], [o[0][:20]], [lse[0][:, :20]], [20], [20], True, 1 / 8)
+
+
+def check_grad(do, q, k, v, dq, dk, dv, lq, lk, causal, scale, ranks=None):
+    Hq, Hkv = q[0].shape[1], k[0].shape[1]
+    G = Hq // Hkv
+    for r in ranks or range(len(q)):
+        t = [f64(x[r]) for x in (do, q, k, v, dq, dk, dv)]
+        a = b = 0
+        for nq, nk in zip(lq, lk):
+            see = oa.visible(nq, nk, causal)
+            A_, B_ = slice(a, a + nq), slice(b, b + nk)
+            for h in range(Hkv):
+                wk = wv = ek = ev = 0
+                for i in range(h * G, h * G + G):
+                    (wq, k1, v1), (eq, k2, v2) = oa.attention_grad(t[0][A_, i], t[1][A_, i], t[2][B_, h], t[3][B_, h], see, scale)
+                    within(t[4][A_, i], wq, eq, "dq, prompt of %d, head %d" % (nq, i))
+                    wk, wv, ek, ev = wk + k1, wv + v1, ek + k2, ev + v2
+                within(t[5][B_, h], wk, ek, "dk, prompt of %d, head %d" % (nq, h))
+                within(t[6][B_, h], wv, ev, "dv, prompt of %d, head %d" % (nq, h))
+            a, b = a + nq, b + nk
+
+
+@pytest.mark.parametrize("lq,lk", LENS)
+@pytest.mark.parametrize("Hq,Hkv,D", [(1, 1, 64), (3, 1, 128), (4, 2, 64), (10, 2, 128)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_attention_grad(lq, lk, Hq, Hkv, D, causal):
+    note("attention_grad lq=%s lk=%s Hq=%d Hkv=%d D=%d causal=%s" % (lq[:8], lk, Hq, Hkv, D, causal))
+    lk = lk or lq
+    P, Tq, Tk = 2, sum(lq), sum(lk)
+    packed = lk is lq and Hq == 4
+    q, k, v = attn_inputs(P, lq, lk, Hq, Hkv, D, seed=Tq + D, layout="packed" if packed else "dense")
+    g = torch.Generator().manual_seed(11)
+    do = [torch.randn(Tq, Hq, D, generator=g).to(BF).cuda() for _ in range(P)]
+    o, lse = [poisoned((Tq, Hq, D)) for _ in range(P)], [poisoned((Hq, Tq), torch.float32) for _ in range(P)]
+    A.tp_attention(q, k, v, o, cu(lq), cu(lk), lse=lse, causal=causal)
+    if packed:                                           # slices of one packed row, as the inputs
+        x = [poisoned((Tq, Hq + 2 * Hkv, D)) for _ in range(P)]
+        dq, dk, dv = [t[:, :Hq] for t in x], [t[:, Hq:Hq + Hkv] for t in x], [t[:, Hq + Hkv:] for t in x]
+    else:
+        dq, (dk, dv) = [poisoned((Tq, Hq, D)) for _ in range(P)], [[poisoned((Tk, Hkv, D)) for _ in range(P)] for _ in range(2)]
+    ws = A.tp_attention_grad(do, q, k, v, o, lse, dq, dk, dv, cu(lq), cu(lk), causal=causal)
+    first = [t.clone() for t in dq + dk + dv]
+    A.tp_attention_grad(do, q, k, v, o, lse, dq, dk, dv, cu(lq), cu(lk), causal=causal, ws=ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, dq + dk + dv))
+    check_grad(do, q, k, v, dq, dk, dv, lq, lk, causal, 1 / math.sqrt(D), ranks=None if Tq < 100 else [1])
+
+
+def test_attention_grad_against_differences():
+    """The gradient along a direction of each input is the change of sum(o do)
+    when the input moves along it, taken from the kernel's own forward pass at
+    steps large enough for bf16.  The step's second-order part cancels in the
+    two-sided difference; what is left of the tolerance is o's bf16 rounding,
+    2^-9 |o do| a term with random signs, over the step."""
+    lq, Hq, Hkv, D = [150, 90], 4, 2, 64
+    q, k, v = attn_inputs(1, lq, lq, Hq, Hkv, D, seed=21)
+    g = torch.Generator().manual_seed(22)
+    do = [torch.randn(240, Hq, D, generator=g).to(BF).cuda()]
+    o, lse = [poisoned((240, Hq, D))], [poisoned((Hq, 240), torch.float32)]
+    A.tp_attention(q, k, v, o, cu(lq), cu(lq), lse=lse)
+    d = [[torch.empty_like(t[0])] for t in (q, k, v)]
+    A.tp_attention_grad(do, q, k, v, o, lse, *d, cu(lq), cu(lq))
+    step = 2.0 ** -4
+    for i in range(3):
+        # a direction along the gradient's signs: moves of one step, kept
+        # exact by rounding both sides to bf16 and taking the move that is left
+        x = [q, k, v]
+        up, down = ((x[i][0].float() + s * d[i][0].float().sign()).to(BF) for s in (step, -step))
+        sums = []
+        for t in (up, down):
+            y = list(x)
+            y[i] = [t]
+            A.tp_attention(*y, o, cu(lq), cu(lq))
+            sums.append((o[0].double() * do[0].double()).sum())
+        want = (d[i][0].double() * (up.double() - down.double())).sum()
+        got = sums[0] - sums[1]
+        noise = 2.0 ** -9 * 8 * (o[0].double() * do[0].double()).norm()
+        # third-order part: up to step^2 of the whole for directions of unit size per element
+        assert abs(float(got - want)) <= float(noise) + 0.1 * abs(float(want)), (i, float(got), float(want), float(noise))
+
+
+# ---------------------------------------------------------------- decode
+def decode_inputs(P, lens, prefix, Hq, Hkv, D, page, seed, spare=3):
+    g = torch.Generator().manual_seed(seed)
+    B, per = len(lens), [-(-max(0, n) // page) for n in lens]
+    shared = -(-prefix // page)
+    pages = sum(per) + shared + spare
+    pool = torch.randperm(pages, generator=g).int()
+    width = max(per + [1])
+    table = torch.full((B, width), -1, dtype=torch.int32)
+    at = shared
+    for b, n in enumerate(per):
+        table[b, :n] = pool[at:at + n]
+        at += n
+    rnd = lambda *s: torch.randn(*s, generator=g).to(BF).cuda()      # noqa: E731
+    kc, vc = ([rnd(pages * page, Hkv, D) for _ in range(P)] for _ in range(2))
+    q = [rnd(B, Hq, D) for _ in range(P)]
+    # rows that no key fills must not matter
+    used = torch.zeros(pages * page, dtype=torch.bool)
+    for p, n in [(pool[:shared], prefix)] + [(table[b, :per[b]], lens[b]) for b in range(B)]:
+        for j in range(max(0, n)):
+            used[int(p[j // page]) * page + j % page] = True
+    for t in kc + vc:
+        t[~used.cuda()] = float("nan")
+    return q, kc, vc, table.cuda(), i32(list(lens)), pool[:shared].cuda() if shared else None
+
+
+def check_decode(q, kc, vc, o, table, lens, pp, prefix, page, scale):
+    tab, pre = table.cpu().numpy(), [] if pp is None else pp.cpu().numpy()
+    for r in range(len(q)):
+        qr, kr, vr, orr = f64(q[r]), f64(kc[r]), f64(vc[r]), f64(o[r])
+        G = qr.shape[1] // kr.shape[1]
+        for b in range(qr.shape[0]):
+            for h in range(qr.shape[1]):
+                w, e = oa.decode(qr[b, h], kr[:, h // G], vr[:, h // G], tab[b], lens[b], pre, prefix, page, scale)
+                within(orr[b, h], w, e, "request %d, head %d" % (b, h))
+
+
+@pytest.mark.parametrize("lens,prefix", [
+    ([1], 0), ([31, 32, 33], 0), ([0, 5, -3, 64], 0), ([65, 1, 200], 17), ([0], 64), ([0, 3], 1), ([700, 20], 0),
+    ([2100], 0), ([40, 41] * 20, 300), ([5000], 0), ([7], 2000)])
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(1, 1, 64, 16), (4, 2, 128, 16), (8, 1, 64, 64), (3, 3, 128, 1), (34, 1, 64, 8)])
+def test_decode(lens, prefix, Hq, Hkv, D, page):
+    note("decode lens=%s prefix=%d Hq=%d Hkv=%d D=%d page=%d" % (lens[:6], prefix, Hq, Hkv, D, page))
+    P = 2
+    q, kc, vc, table, ln, pp = decode_inputs(P, lens, prefix, Hq, Hkv, D, page, seed=len(lens) + prefix)
+    o = [poisoned((len(lens), Hq, D)) for _ in range(P)]
+    ws = A.tp_attention_decode(q, kc, vc, o, table, ln, page_size=page, prefix_pages=pp, prefix_len=prefix)
+    first = [t.clone() for t in o]
+    A.tp_attention_decode(q, kc, vc, o, table, ln, page_size=page, prefix_pages=pp, prefix_len=prefix, ws=ws)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(first, o))
+    check_decode(q, kc, vc, o, table, lens, pp, prefix, page, 1 / math.sqrt(D))
+
+
+def test_decode_pages_outside_the_cache_take_no_part():
+    lens, page = [100, 70, 40], 16
+    q, kc, vc, table, ln, pp = decode_inputs(1, lens, 50, 2, 1, 64, page, seed=77)
+    table[0, 2], table[0, 5], table[1, 0], pp[1] = -1, 1 << 30, kc[0].shape[0] // page, -9
+    table[2, :] = -1
+    o = [poisoned((3, 2, 64))]
+    A.tp_attention_decode(q, kc, vc, o, table, ln, page_size=page, prefix_pages=pp, prefix_len=50)
+    torch.cuda.synchronize()
+    check_decode(q, kc, vc, o, table, lens, pp, 50, page, 1 / 8)
+
+
+def test_decode_lengths_past_the_table_are_clamped():
+    q, kc, vc, table, ln, _ = decode_inputs(1, [64, 32], 0, 2, 1, 64, 16, seed=78)
+    o = [poisoned((2, 2, 64))]
+    A.tp_attention_decode(q, kc, vc, o, table[:, :2].contiguous(), i32([1000, 1 << 30]), page_size=16)
+    torch.cuda.synchronize()
+    check_decode(q, kc, vc, o, table[:, :2], [32, 32], None, 0, 16, 1 / 8)
