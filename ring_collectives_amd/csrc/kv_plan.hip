@@ -70,36 +70,36 @@ __global__ __launch_bounds__(kThreads) void kv_plan_kernel(PlanArgs a) {
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int used = *a.used;
     const int page = 1 << a.shift;
-    long long base_n = 0, base_p = 0;
     constexpr int kMax = 0x7fffffff;
     auto sat = [](long long x) { return (int)(x < kMax ? x : kMax); };
     auto pages = [&](long long n) { return (n + page - 1) >> a.shift; };
-    for (int b0 = 0; b0 < a.B; b0 += kThreads) {
-        const int b = b0 + tid;
-        long long n = 0, p = 0;
-        int before = 0, add = 0;
-        if (b < a.B) {
-            before = at_least_0(a.lengths[b]);
-            add = at_least_0(a.new_tokens[b]);
-            n = add;
-            p = pages((long long)before + add) - pages(before);
+    // each thread sums a run of requests, one scan of the threads' sums places
+    // the run, and a second look at its requests writes the running sums
+    const int run = (a.B + kThreads - 1) / kThreads;
+    const int r0 = tid * run < a.B ? tid * run : a.B, r1 = r0 + run < a.B ? r0 + run : a.B;
+    long long n = 0, p = 0, tn, tp;
+#pragma unroll 8
+    for (int b = r0; b < r1; ++b) {
+        const int before = at_least_0(a.lengths[b]), add = at_least_0(a.new_tokens[b]);
+        n += add;
+        p += pages((long long)before + add) - pages(before);
+    }
+    scan2(n, p, tn, tp, part, lane, wave);
+#pragma unroll 8
+    for (int b = r0; b < r1; ++b) {
+        const int before = at_least_0(a.lengths[b]), add = at_least_0(a.new_tokens[b]);
+        cu[b] = sat(n);
+        pg[b] = sat(p);
+        if (blockIdx.x == 0) {
+            a.cu[b] = sat(n);
+            a.after[b] = sat((long long)before + add);
         }
-        long long tn, tp;
-        scan2(n, p, tn, tp, part, lane, wave);
-        if (b < a.B) {
-            cu[b] = sat(base_n + n);
-            pg[b] = sat(base_p + p);
-            if (blockIdx.x == 0) {
-                a.cu[b] = cu[b];
-                a.after[b] = sat((long long)before + add);
-            }
-        }
-        base_n += tn;
-        base_p += tp;
+        n += add;
+        p += pages((long long)before + add) - pages(before);
     }
     if (tid == 0) {
-        cu[a.B] = sat(base_n);
-        pg[a.B] = sat(base_p);
+        cu[a.B] = sat(tn);
+        pg[a.B] = sat(tp);
         if (blockIdx.x == 0) a.cu[a.B] = cu[a.B];
     }
     __syncthreads();

@@ -241,20 +241,24 @@ struct GainArgs {
     int blocks;
 };
 
-// dgain = the workgroups' partial sums, added in a fixed order: 256 / D
-// interleaved sums per value, then those.
+// dgain = the workgroups' partial sums, added in a fixed order: D / 4 lanes
+// hold a gain, 4096 / D such groups sum every 4096 / D-th workgroup's part and
+// their sums are added one after the other.
 template <int D>
-__global__ __launch_bounds__(256) void gain_sum_kernel(GainArgs g) {
-    __shared__ float sum[256];
-    const int rank = blockIdx.x, which = blockIdx.y, d = threadIdx.x % D, u = threadIdx.x / D;
-    float s = 0.0f;
-    for (int b = u; b < g.blocks; b += 256 / D) s += g.part[(((long long)rank * g.blocks + b) * 2 + which) * D + d];
-    sum[threadIdx.x] = s;
+__global__ __launch_bounds__(1024) void gain_sum_kernel(GainArgs g) {
+    constexpr int L = D / 4, kGroups = 1024 / L;
+    __shared__ f32x4 sum[kGroups][L];
+    const int rank = blockIdx.x, which = blockIdx.y, i = threadIdx.x % L, u = threadIdx.x / L;
+    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+    for (int b = u; b < g.blocks; b += kGroups)
+        s += *(const f32x4*)(g.part + (((long long)rank * g.blocks + b) * 2 + which) * D + 4 * i);
+    sum[u][i] = s;
     __syncthreads();
-    if (threadIdx.x < D) {
-        for (int w = 1; w < 256 / D; ++w) s += sum[w * D + d];
-        (which ? g.dgk : g.dgq)[rank][d] = s;
-    }
+    if (u) return;
+#pragma unroll 8
+    for (int w = 1; w < kGroups; ++w) s += sum[w][i];
+    *(f32x4*)((which ? g.dgk : g.dgq)[rank] + 4 * i) = s;
 }
 
 int rope_shape(int P, int T, int Hq, int Hkv, int D, int rot, long long table_rows, long long cache_rows,
@@ -409,8 +413,8 @@ extern "C" int tp_qk_norm_rope_grad(const void* const* dq, const void* const* dk
             w.dgk[r] = dgain_k[r];
         }
         const dim3 grid((unsigned)P, 2);
-        if (D == 128) hipLaunchKernelGGL(gain_sum_kernel<128>, grid, dim3(256), 0, s, w);
-        else hipLaunchKernelGGL(gain_sum_kernel<64>, grid, dim3(256), 0, s, w);
+        if (D == 128) hipLaunchKernelGGL(gain_sum_kernel<128>, grid, dim3(1024), 0, s, w);
+        else hipLaunchKernelGGL(gain_sum_kernel<64>, grid, dim3(1024), 0, s, w);
         if (hipGetLastError() != hipSuccess) return RING_EHIP;
     }
     return RING_OK;
