@@ -17,6 +17,7 @@ CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["ring_api.hip", "ring_kernels.hip", "gemm_rs.hip", "ag_gemm.hip", "tp_mlp.hip", "kv_plan.hip",
            "qk_rope.hip", "attn_prompt.hip", "attn_grad.hip", "attn_decode.hip"]
 LIB = os.path.join(HERE, "libring_collectives.so")
+BINDING = os.path.join(HERE, "_binding.so")
 ARCH = os.environ.get("RING_OFFLOAD_ARCH", "gfx950")
 
 FLAGS = [
@@ -89,7 +90,29 @@ def build(verbose: bool = False) -> str:
         os.remove(tmp)
         raise RuntimeError("build: the library leaves its own symbols undefined: %s" % ", ".join(missing))
     os.replace(tmp, LIB)
+    _build_binding(verbose)
     return LIB
+
+
+def _build_binding(verbose: bool) -> None:
+    """The Python extension of the attention calls (host code), linked to the
+    library next to it."""
+    import sysconfig
+
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+    tmp = BINDING + ".tmp%d" % os.getpid()
+    inc = [sysconfig.get_paths()["include"], os.path.join(ROOT, "include"), *include_paths()]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI), *["-isystem" + p for p in inc],
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, *["-L" + p for p in library_paths()], "-L" + HERE,
+           "-l:libring_collectives.so", "-ltorch_python", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"]
+    rc, kept, _ = _run(cmd, verbose)
+    for ln in kept:
+        print(ln, flush=True)
+    if rc != 0:
+        raise subprocess.CalledProcessError(rc, "g++ (binding)")
+    os.replace(tmp, BINDING)
 
 
 if __name__ == "__main__":
