@@ -151,39 +151,87 @@ __device__ __forceinline__ float sum_halves(float x) {
 
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
+// Inclusive running sum over the wave's lanes (VALU only: four shifts within
+// rows of 16 lanes, then the last lane of rows 0 and 2, and of row 1, added on).
+__device__ __forceinline__ int wave_scan(int x) {
+    x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);
+    x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
+    return x;
+}
+
 // The prompt and tile of work slot `slot`, where prompt b has
 // ceil(len_b * per / rows) tiles, len_b = cu[b + 1] - cu[b] clamped to the
-// `total` rows there are.  Every lane of the wave looks at one prompt at a
-// time.  Returns false past the last tile.
+// `total` rows there are, and the prompt's range of the other tensor's rows
+// likewise (lengths at least 0).  Every lane looks at one prompt, so 64 of
+// them cost one trip to memory.  Returns false past the last tile.
 struct PromptTile {
-    int b, tile, tiles;
+    int tile, tiles;        // of the prompt
+    int lo, n, lo2, n2;     // its rows, and the other tensor's
 };
 __device__ __forceinline__ int clamp_cu(int x, int total) { return x < 0 ? 0 : x > total ? total : x; }
-__device__ inline bool find_tile(const int* cu, int B, int total, int per, int rows, int slot, int lane, PromptTile& t) {
+__device__ __forceinline__ bool find_tile(const int* cu, const int* cu2, int B, int total, int total2, int per, int rows,
+                                          int slot, int lane, PromptTile& t) {
     int before = 0;
     for (int b0 = 0; b0 < B; b0 += 64) {
-        int n = 0;
+        int lo = 0, len = 0, lo2 = 0, len2 = 0;
         if (b0 + lane < B) {
-            const int lo = clamp_cu(cu[b0 + lane], total), hi = clamp_cu(cu[b0 + lane + 1], total);
-            if (hi > lo) n = (int)(((long long)(hi - lo) * per + rows - 1) / rows);
+            const int x0 = cu[b0 + lane], x1 = cu[b0 + lane + 1], y0 = cu2[b0 + lane], y1 = cu2[b0 + lane + 1];
+            lo = clamp_cu(x0, total);
+            len = clamp_cu(x1, total) - lo;
+            lo2 = clamp_cu(y0, total2);
+            len2 = clamp_cu(y1, total2) - lo2;
         }
-        int sum = n;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int y = __shfl_up(sum, d);
-            if (lane >= d) sum += y;
-        }
+        if (len < 0) len = 0;
+        const int n = (int)(((unsigned)len * (unsigned)per + (unsigned)(rows - 1)) / (unsigned)rows);
+        const int sum = wave_scan(n);
         const unsigned long long past = __ballot(before + sum > slot);
         if (past) {
             const int at = __builtin_ctzll(past);
-            t.b = b0 + at;
             t.tiles = __builtin_amdgcn_readlane(n, at);
             t.tile = slot - (before + __builtin_amdgcn_readlane(sum, at) - t.tiles);
+            t.lo = __builtin_amdgcn_readlane(lo, at);
+            t.n = __builtin_amdgcn_readlane(len, at);
+            t.lo2 = __builtin_amdgcn_readlane(lo2, at);
+            const int n2 = __builtin_amdgcn_readlane(len2, at);
+            t.n2 = n2 < 0 ? 0 : n2;
             return true;
         }
         before += __builtin_amdgcn_readlane(sum, 63);
     }
     return false;
+}
+
+// Store the lane's column of a D x 32 block of accumulators, times f, as bf16
+// to its row p: the two halves of the wave trade so that each lane stores 16
+// contiguous bytes.
+template <int D, class Acc>
+__device__ __forceinline__ void store_column(unsigned short* p, const Acc& x, float f, int half, bool live) {
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+#pragma unroll
+    for (int db = 0; db < Rows<D>::DB; ++db)
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {
+            u32x4 y;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                // values 8 j + 4 half + 2 e, + 1 and the same of j + 1: of the
+                // pair the lower half keeps j's and gets the upper's, the
+                // upper half j + 1's
+                const f32x2 lo = {x[db][4 * j + 2 * e] * f, x[db][4 * j + 2 * e + 1] * f};
+                const f32x2 hi = {x[db][4 * j + 4 + 2 * e] * f, x[db][4 * j + 5 + 2 * e] * f};
+                const auto r = __builtin_amdgcn_permlane32_swap(
+                    __builtin_bit_cast(unsigned, __builtin_convertvector(lo, bf16x2)),
+                    __builtin_bit_cast(unsigned, __builtin_convertvector(hi, bf16x2)), false, false);
+                y[e] = r[0];
+                y[2 + e] = r[1];
+            }
+            if (live) *(u32x4*)(p + 32 * db + 8 * (j + half)) = y;
+        }
 }
 
 // Arguments of the packed-prompt kernels (per-rank pointers by value).

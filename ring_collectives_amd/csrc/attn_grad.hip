@@ -35,20 +35,6 @@ struct GradArgs {
     int slots;
 };
 
-typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-
-// Store the lane's column of a D x 32 block of accumulators, times f, as bf16.
-template <int D, class Acc>
-__device__ __forceinline__ void store_column(unsigned short* p, const Acc& x, float f) {
-#pragma unroll
-    for (int db = 0; db < Rows<D>::DB; ++db)
-#pragma unroll
-        for (int v = 0; v < 16; v += 4) {
-            const f32x4 y = {x[db][v] * f, x[db][v + 1] * f, x[db][v + 2] * f, x[db][v + 3] * f};
-            *(bf16x4*)(p + 32 * db + 2 * v) = __builtin_convertvector(y, bf16x4);
-        }
-}
-
 template <int D>
 __global__ __launch_bounds__(256, 2) void attn_dq_kernel(GradArgs a) {
     typedef Rows<D> R;
@@ -61,26 +47,29 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(GradArgs a) {
     unit_slot(a.p.P * a.p.Hkv, a.slots, blockIdx.x, unit, slot);
     const int G = a.p.Hq / a.p.Hkv, rank = unit / a.p.Hkv, kvh = unit % a.p.Hkv;
     PromptTile pt;
-    if (!find_tile(a.p.cu_q, a.p.B, a.p.Tq, G, kRowsWG, slot, lane, pt)) return;
-    const int b = pt.b, tile = pt.tiles - 1 - pt.tile;
-    const int q0 = clamp_cu(a.p.cu_q[b], a.p.Tq), nq = clamp_cu(a.p.cu_q[b + 1], a.p.Tq) - q0;
-    const int k0 = clamp_cu(a.p.cu_k[b], a.p.Tk), k1 = clamp_cu(a.p.cu_k[b + 1], a.p.Tk);
-    const int nk = k1 > k0 ? k1 - k0 : 0;
-    const long long rows = (long long)nq * G;
-    const long long m0 = (long long)tile * kRowsWG + wave * 32;
-    const long long m = m0 + (lane & 31) < rows ? m0 + (lane & 31) : rows - 1;
-    const int qi = (int)(m / G), head = kvh * G + (int)(m % G);
+    if (!find_tile(a.p.cu_q, a.p.cu_k, a.p.B, a.p.Tq, a.p.Tk, G, kRowsWG, slot, lane, pt)) return;
+    const int tile = pt.tiles - 1 - pt.tile;                 // the longest first
+    const int q0 = pt.lo, nq = pt.n, k0 = pt.lo2, nk = pt.n2;
+    // this lane's row; rows past the end repeat the last one and are not stored
+    const unsigned rows = (unsigned)nq * (unsigned)G, m0 = (unsigned)(tile * kRowsWG + wave * 32);
+    const bool live = m0 + (lane & 31) < rows;
+    const unsigned m = live ? m0 + (lane & 31) : rows - 1;
+    const int qi = (int)(m / (unsigned)G), head = kvh * G + (int)(m % (unsigned)G);
+
+    // keys [0, seen) are visible to this lane's query, [0, every) to every row
+    // of the wave, [0, some) to one of them at least, [0, most) to one of the
+    // workgroup's
     const int off = nk - nq;
     int seen = nk, every = nk, some = nk, most = nk;
     if (a.p.causal) {
-        auto upto = [&](long long row) {
-            const long long s = (row < rows ? row : rows - 1) / G + off + 1;
-            return (int)(s < 0 ? 0 : s < nk ? s : nk);
+        auto upto = [&](unsigned row) {
+            const int s = (int)((row < rows ? row : rows - 1) / (unsigned)G) + off + 1;
+            return s < 0 ? 0 : s < nk ? s : nk;
         };
         seen = upto(m);
         every = upto(m0);
         some = upto(m0 + 31);
-        most = upto((long long)tile * kRowsWG + kRowsWG - 1);
+        most = upto((unsigned)(tile * kRowsWG + kRowsWG - 1));
     }
 
     bf16x8 qf[R::KK], gf[R::KK];
@@ -103,7 +92,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(GradArgs a) {
     const long long at = ((long long)rank * a.p.Hq + head) * a.p.Tq + q0 + qi;
     float lse2 = a.lse[rank][(long long)head * a.p.Tq + q0 + qi] * kLog2e;
     if (lse2 == -INFINITY) lse2 = INFINITY;              // no key seen: every weight is 0
-    if (half == 0 && m0 + (lane & 31) < rows) {
+    if (half == 0 && live) {
         a.lse2[at] = lse2;
         a.delta[at] = delta;
     }
@@ -165,8 +154,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(GradArgs a) {
             }
         }
     }
-    if (m0 + (lane & 31) >= rows) return;
-    store_column<D>(a.dq[rank] + (q0 + (long long)qi) * a.dq_stride + (long long)head * D + 4 * half, dq, a.scale);
+    store_column<D>(a.dq[rank] + (q0 + (long long)qi) * a.dq_stride + (long long)head * D, dq, a.scale, half, live);
 }
 
 template <int D>
@@ -181,11 +169,9 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_kernel(GradArgs
     unit_slot(a.p.P * a.p.Hkv, a.slots, blockIdx.x, unit, slot);
     const int G = a.p.Hq / a.p.Hkv, rank = unit / a.p.Hkv, kvh = unit % a.p.Hkv;
     PromptTile pt;
-    if (!find_tile(a.p.cu_k, a.p.B, a.p.Tk, 1, kRowsWG, slot, lane, pt)) return;
-    const int b = pt.b, tile = pt.tile;                   // the first keys are seen by the most queries
-    const int k0 = clamp_cu(a.p.cu_k[b], a.p.Tk), nk = clamp_cu(a.p.cu_k[b + 1], a.p.Tk) - k0;
-    const int q0 = clamp_cu(a.p.cu_q[b], a.p.Tq), q1 = clamp_cu(a.p.cu_q[b + 1], a.p.Tq);
-    const int nq = q1 > q0 ? q1 - q0 : 0, off = nk - nq;
+    if (!find_tile(a.p.cu_k, a.p.cu_q, a.p.B, a.p.Tk, a.p.Tq, 1, kRowsWG, slot, lane, pt)) return;
+    const int tile = pt.tile;                             // the first keys are seen by the most queries
+    const int k0 = pt.lo, nk = pt.n, q0 = pt.lo2, nq = pt.n2, off = nk - nq;
     const int key0 = tile * kRowsWG + wave * 32;          // this wave's first key
     const int key = key0 + (lane & 31), keyc = key < nk ? key : nk - 1;
 
@@ -276,9 +262,8 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_kernel(GradArgs
             }
         }
     }
-    if (key >= nk) return;
-    store_column<D>(a.dk[rank] + (k0 + (long long)key) * a.dk_stride + (long long)kvh * D + 4 * half, dk, a.scale);
-    store_column<D>(a.dv[rank] + (k0 + (long long)key) * a.dv_stride + (long long)kvh * D + 4 * half, dv, 1.0f);
+    store_column<D>(a.dk[rank] + (k0 + (long long)keyc) * a.dk_stride + (long long)kvh * D, dk, a.scale, half, key < nk);
+    store_column<D>(a.dv[rank] + (k0 + (long long)keyc) * a.dv_stride + (long long)kvh * D, dv, 1.0f, half, key < nk);
 }
 
 }  // namespace

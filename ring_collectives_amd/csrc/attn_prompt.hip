@@ -40,16 +40,14 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
     unit_slot(a.p.P * a.p.Hkv, a.slots, blockIdx.x, unit, slot);
     const int G = a.p.Hq / a.p.Hkv, rank = unit / a.p.Hkv, kvh = unit % a.p.Hkv;
     PromptTile pt;
-    if (!find_tile(a.p.cu_q, a.p.B, a.p.Tq, G, kTileRows, slot, lane, pt)) return;
-    const int b = pt.b, tile = pt.tiles - 1 - pt.tile;       // the longest first
-    const int q0 = clamp_cu(a.p.cu_q[b], a.p.Tq), nq = clamp_cu(a.p.cu_q[b + 1], a.p.Tq) - q0;
-    const int k0 = clamp_cu(a.p.cu_k[b], a.p.Tk), k1 = clamp_cu(a.p.cu_k[b + 1], a.p.Tk);
-    const int nk = k1 > k0 ? k1 - k0 : 0;
-    const long long rows = (long long)nq * G;
-    const long long m0 = (long long)tile * kTileRows + wave * 32;
+    if (!find_tile(a.p.cu_q, a.p.cu_k, a.p.B, a.p.Tq, a.p.Tk, G, kTileRows, slot, lane, pt)) return;
+    const int tile = pt.tiles - 1 - pt.tile;                 // the longest first
+    const int q0 = pt.lo, nq = pt.n, k0 = pt.lo2, nk = pt.n2;
     // this lane's row; rows past the end repeat the last one and are not stored
-    const long long m = m0 + (lane & 31) < rows ? m0 + (lane & 31) : rows - 1;
-    const int qi = (int)(m / G), head = kvh * G + (int)(m % G);
+    const unsigned rows = (unsigned)nq * (unsigned)G, m0 = (unsigned)(tile * kTileRows + wave * 32);
+    const bool live = m0 + (lane & 31) < rows;
+    const unsigned m = live ? m0 + (lane & 31) : rows - 1;
+    const int qi = (int)(m / (unsigned)G), head = kvh * G + (int)(m % (unsigned)G);
 
     // keys [0, seen) are visible to this lane's query, [0, every) to every row
     // of the wave, [0, some) to one of them at least, [0, most) to one of the
@@ -57,14 +55,14 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
     const int off = nk - nq;
     int seen = nk, every = nk, some = nk, most = nk;
     if (a.p.causal) {
-        auto upto = [&](long long row) {
-            const long long s = (row < rows ? row : rows - 1) / G + off + 1;
-            return (int)(s < 0 ? 0 : s < nk ? s : nk);
+        auto upto = [&](unsigned row) {
+            const int s = (int)((row < rows ? row : rows - 1) / (unsigned)G) + off + 1;
+            return s < 0 ? 0 : s < nk ? s : nk;
         };
         seen = upto(m);
         every = upto(m0);
         some = upto(m0 + 31);
-        most = upto((long long)tile * kTileRows + kTileRows - 1);
+        most = upto((unsigned)(tile * kTileRows + kTileRows - 1));
     }
 
     bf16x8 qf[R::KK];
@@ -157,19 +155,10 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
         }
     }
 
-    if (m0 + (lane & 31) >= rows) return;
     l = sum_halves(l);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;          // a row that sees no key gives zeros
-    unsigned short* op = a.o[rank] + (q0 + (long long)qi) * a.o_stride + (long long)head * D + 4 * half;
-#pragma unroll
-    for (int db = 0; db < R::DB; ++db)
-#pragma unroll
-        for (int v = 0; v < 16; v += 4) {
-            typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-            const f32x4 y = {o[db][v] * inv, o[db][v + 1] * inv, o[db][v + 2] * inv, o[db][v + 3] * inv};
-            *(bf16x4*)(op + 32 * db + 2 * v) = __builtin_convertvector(y, bf16x4);
-        }
-    if (a.lse[rank] && half == 0)
+    store_column<D>(a.o[rank] + (q0 + (long long)qi) * a.o_stride + (long long)head * D, o, inv, half, live);
+    if (a.lse[rank] && live && half == 0)
         a.lse[rank][(long long)head * a.p.Tq + q0 + qi] = l == 0.0f ? -INFINITY : (mc + __log2f(l)) * kLn2;
 }
 
@@ -215,8 +204,9 @@ bool row_stride_ok(long long stride, int heads, int D) {
     return stride >= (long long)heads * D && stride < kMaxRow && stride % 8 == 0;
 }
 // Tiles of `rows` rows that prompts of `total` tokens, `per` rows each, can
-// make: 0 if there are too many for a launch.
+// make: 0 if there are too many for a launch or for 32-bit row numbers.
 int prompt_slots(int B, int total, int per, int rows, int units) {
+    if ((long long)total * per >= (1LL << 31) - rows) return 0;
     const long long n = (long long)total * per / rows + (B < total ? B : total);
     return n * (units > 8 ? units : 8) < (1LL << 31) ? (int)n : 0;
 }

@@ -64,9 +64,9 @@ __device__ __forceinline__ void scan2(long long& x, long long& y, long long& tx,
 }
 
 __global__ __launch_bounds__(kThreads) void kv_plan_kernel(PlanArgs a) {
-    extern __shared__ int lds[];                 // [B + 1] sums of new tokens, [B + 1] sums of new pages
+    extern __shared__ int lds[];                 // [B + 1] sums of new tokens, [B + 1] of new pages, [B] lengths
     __shared__ long long part[kThreads / 64][2];
-    int *cu = lds, *pg = lds + a.B + 1;
+    int *cu = lds, *pg = lds + a.B + 1, *len = lds + 2 * (a.B + 1);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int used = *a.used;
     const int page = 1 << a.shift;
@@ -90,6 +90,7 @@ __global__ __launch_bounds__(kThreads) void kv_plan_kernel(PlanArgs a) {
         const int before = at_least_0(a.lengths[b]), add = at_least_0(a.new_tokens[b]);
         cu[b] = sat(n);
         pg[b] = sat(p);
+        len[b] = before;
         if (blockIdx.x == 0) {
             a.cu[b] = sat(n);
             a.after[b] = sat((long long)before + add);
@@ -120,7 +121,7 @@ __global__ __launch_bounds__(kThreads) void kv_plan_kernel(PlanArgs a) {
     const int step = gridDim.x * kThreads, first = blockIdx.x * kThreads + tid;
     for (long long i = first; i < need; i += step) {
         const int b = request(pg, (int)i);
-        const long long j = pages(at_least_0(a.lengths[b])) + i - pg[b];
+        const long long j = pages(len[b]) + i - pg[b];
         if (j < a.stride) a.table[(long long)b * a.stride + j] = free_page(i);
     }
     for (long long t = first; t < a.capacity; t += step) {
@@ -128,8 +129,7 @@ __global__ __launch_bounds__(kThreads) void kv_plan_kernel(PlanArgs a) {
         long long slot = -1;
         if (t < total) {
             const int b = request(cu, (int)t);
-            const int before = at_least_0(a.lengths[b]);
-            const long long n = (long long)before + t - cu[b], j = n >> a.shift, have = pages(before);
+            const long long n = (long long)len[b] + t - cu[b], j = n >> a.shift, have = pages(len[b]);
             pos = sat(n + a.prefix);
             if (j < a.stride) {
                 const int p = j >= have ? free_page(pg[b] + j - have) : a.table[(long long)b * a.stride + j];
@@ -171,7 +171,7 @@ extern "C" int kv_plan(const int* lengths, const int* new_tokens, const int* fre
     const int work = capacity > B ? capacity : B;
     int blocks = (work + kThreads - 1) / kThreads;
     if (blocks > 2 * dev_info().cus) blocks = 2 * dev_info().cus;
-    hipLaunchKernelGGL(kv_plan_kernel, dim3((unsigned)blocks), dim3(kThreads), 2 * (size_t)(B + 1) * sizeof(int),
+    hipLaunchKernelGGL(kv_plan_kernel, dim3((unsigned)blocks), dim3(kThreads), (3 * (size_t)B + 2) * sizeof(int),
                        (hipStream_t)stream, a);
     return hipGetLastError() == hipSuccess ? RING_OK : RING_EHIP;
 }
