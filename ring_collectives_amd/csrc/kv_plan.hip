@@ -31,76 +31,74 @@ struct PlanArgs {
 
 __device__ __forceinline__ int at_least_0(int x) { return x < 0 ? 0 : x; }
 
-// Running sums over the workgroup of two values; returns the exclusive ones
-// and leaves the totals in both totals.
-__device__ __forceinline__ void scan2(long long& x, long long& y, long long& tx, long long& ty, long long (*part)[2], int lane,
-                                      int wave) {
-    const long long x0 = x, y0 = y;
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const long long u = __shfl_up(x, d), w = __shfl_up(y, d);
-        if (lane >= d) {
-            x += u;
-            y += w;
-        }
-    }
-    if (lane == 63) {
-        part[wave][0] = x;
-        part[wave][1] = y;
-    }
-    __syncthreads();
-    tx = ty = 0;
-    for (int w = 0; w < kThreads / 64; ++w) {
-        if (w < wave) {
-            x += part[w][0];
-            y += part[w][1];
-        }
-        tx += part[w][0];
-        ty += part[w][1];
-    }
-    __syncthreads();
-    x -= x0;
-    y -= y0;
+// Sums saturate: of non-negative counts in 32 bits, whatever the order, the
+// result is the sum or the largest value.
+__device__ __forceinline__ unsigned add_sat(unsigned x, unsigned y) { return __builtin_elementwise_add_sat(x, y); }
+__device__ __forceinline__ int as_int(unsigned x) { return x < 0x7fffffffu ? (int)x : 0x7fffffff; }
+
+// Inclusive running sum over the wave's lanes, on the VALU.
+__device__ __forceinline__ unsigned scan_sat(unsigned x) {
+    x = add_sat(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, 0x111, 0xf, 0xf, false));
+    x = add_sat(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, 0x112, 0xf, 0xf, false));
+    x = add_sat(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, 0x114, 0xf, 0xf, false));
+    x = add_sat(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, 0x118, 0xf, 0xf, false));
+    x = add_sat(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, 0x142, 0xa, 0xf, false));
+    return add_sat(x, (unsigned)__builtin_amdgcn_update_dpp(0, (int)x, 0x143, 0xc, 0xf, false));
 }
 
 __global__ __launch_bounds__(kThreads) void kv_plan_kernel(PlanArgs a) {
     extern __shared__ int lds[];                 // [B + 1] sums of new tokens, [B + 1] of new pages, [B] lengths
-    __shared__ long long part[kThreads / 64][2];
+    __shared__ unsigned part[kThreads / 64][2];
     int *cu = lds, *pg = lds + a.B + 1, *len = lds + 2 * (a.B + 1);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int used = *a.used;
     const int page = 1 << a.shift;
-    constexpr int kMax = 0x7fffffff;
-    auto sat = [](long long x) { return (int)(x < kMax ? x : kMax); };
     auto pages = [&](long long n) { return (n + page - 1) >> a.shift; };
     // each thread sums a run of requests, one scan of the threads' sums places
-    // the run, and a second look at its requests writes the running sums
+    // the run, and the run's own sums follow from there
     const int run = (a.B + kThreads - 1) / kThreads;
     const int r0 = tid * run < a.B ? tid * run : a.B, r1 = r0 + run < a.B ? r0 + run : a.B;
-    long long n = 0, p = 0, tn, tp;
+    unsigned n = 0, p = 0;
 #pragma unroll 8
     for (int b = r0; b < r1; ++b) {
         const int before = at_least_0(a.lengths[b]), add = at_least_0(a.new_tokens[b]);
-        n += add;
-        p += pages((long long)before + add) - pages(before);
-    }
-    scan2(n, p, tn, tp, part, lane, wave);
-#pragma unroll 8
-    for (int b = r0; b < r1; ++b) {
-        const int before = at_least_0(a.lengths[b]), add = at_least_0(a.new_tokens[b]);
-        cu[b] = sat(n);
-        pg[b] = sat(p);
         len[b] = before;
-        if (blockIdx.x == 0) {
-            a.cu[b] = sat(n);
-            a.after[b] = sat((long long)before + add);
+        cu[b] = add;
+        n = add_sat(n, (unsigned)add);
+        p = add_sat(p, (unsigned)(pages((long long)before + add) - pages(before)));
+    }
+    const unsigned n1 = scan_sat(n), p1 = scan_sat(p);
+    if (lane == 63) {
+        part[wave][0] = n1;
+        part[wave][1] = p1;
+    }
+    __syncthreads();
+    // what lies before this thread's run: the lanes below it and the waves
+    // below its own (saturated, they say at least that the run lies past 2^31)
+    unsigned tn = 0, tp = 0, n0 = (unsigned)__shfl_up((int)n1, 1), p0 = (unsigned)__shfl_up((int)p1, 1);
+    if (lane == 0) n0 = p0 = 0;
+    for (int w = 0; w < kThreads / 64; ++w) {
+        if (w < wave) {
+            n0 = add_sat(n0, part[w][0]);
+            p0 = add_sat(p0, part[w][1]);
         }
-        n += add;
-        p += pages((long long)before + add) - pages(before);
+        tn = add_sat(tn, part[w][0]);
+        tp = add_sat(tp, part[w][1]);
+    }
+    for (int b = r0; b < r1; ++b) {
+        const int before = len[b], add = cu[b];
+        cu[b] = as_int(n0);
+        pg[b] = as_int(p0);
+        if (blockIdx.x == 0) {
+            a.cu[b] = as_int(n0);
+            a.after[b] = as_int((unsigned)before + (unsigned)add);
+        }
+        n0 = add_sat(n0, (unsigned)add);
+        p0 = add_sat(p0, (unsigned)(pages((long long)before + add) - pages(before)));
     }
     if (tid == 0) {
-        cu[a.B] = sat(tn);
-        pg[a.B] = sat(tp);
+        cu[a.B] = as_int(tn);
+        pg[a.B] = as_int(tp);
         if (blockIdx.x == 0) a.cu[a.B] = cu[a.B];
     }
     __syncthreads();
@@ -130,7 +128,7 @@ __global__ __launch_bounds__(kThreads) void kv_plan_kernel(PlanArgs a) {
         if (t < total) {
             const int b = request(cu, (int)t);
             const long long n = (long long)len[b] + t - cu[b], j = n >> a.shift, have = pages(len[b]);
-            pos = sat(n + a.prefix);
+            pos = n + a.prefix < 0x7fffffff ? (int)(n + a.prefix) : 0x7fffffff;
             if (j < a.stride) {
                 const int p = j >= have ? free_page(pg[b] + j - have) : a.table[(long long)b * a.stride + j];
                 if (p >= 0) slot = (long long)p * page + (n & (page - 1));
@@ -140,7 +138,7 @@ __global__ __launch_bounds__(kThreads) void kv_plan_kernel(PlanArgs a) {
         a.slots[t] = slot;
     }
     // not in place: workgroups that start later still read *used
-    if (blockIdx.x == 0 && tid == 0) *a.used_after = sat((long long)used + need);
+    if (blockIdx.x == 0 && tid == 0) *a.used_after = (long long)used + need < 0x7fffffff ? used + need : 0x7fffffff;
 }
 
 }  // namespace
