@@ -83,15 +83,23 @@ template <int D> struct Soft {
     }
 };
 
-// One instruction's rows of a gathered tile: row r of the lane at cache row
-// id (none: id < 0, its LDS bytes keep what they hold).
+// One instruction's rows of a gathered tile: the lane's row r is cache row id.
+// Rows without a key (id < 0) load cache row 0, and blank() makes zeros of
+// what landed.  Both by selects: with a branch per lane around a load, the
+// compiler is free to run the lanes on either side of it apart from each other
+// through the loop that follows, whose steps are the whole wave's.
 template <int D>
 __device__ __forceinline__ void gather(const unsigned short* base, long long stride, int id, int r, int lane,
                                        unsigned short* lds, int at) {
-    if (id >= 0) {
-        const unsigned short* p = base + id * stride + ((lane % Rows<D>::C) ^ Rows<D>::swz(r)) * 8;
-        __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p, lds_at(lds, (unsigned)at), 16, 0, 0);
-    }
+    const unsigned short* p = base + (id < 0 ? 0 : id) * stride + ((lane % Rows<D>::C) ^ Rows<D>::swz(r)) * 8;
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)p, lds_at(lds, (unsigned)at), 16, 0, 0);
+}
+__device__ __forceinline__ void blank(unsigned short* lds, int at, int id, int lane) {
+    u32x4* p = (u32x4*)((char*)lds + at + lane * 16);
+    u32x4 x = *p;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = id < 0 ? 0u : x[e];
+    *p = x;
 }
 
 __device__ __forceinline__ void lds_settled() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
@@ -124,14 +132,16 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a) {
     bool live;
     int part;
     auto load_q = [&](long long row) {
-        const int b = (int)(row / G), head = kvh * G + (int)(row % G);
+        const int b = (int)((unsigned)row / (unsigned)G), head = kvh * G + (int)((unsigned)row % (unsigned)G);
         const unsigned short* qp = a.q[rank] + b * a.q_stride + (long long)head * D + 8 * half;
 #pragma unroll
         for (int kk = 0; kk < R::KK; ++kk) qf[kk] = *(const bf16x8*)(qp + 16 * kk);
     };
-    auto page_row = [&](const int* pages, int key) {      // the cache row of a key, -1 if its page is not one
-        const int p = pages[key >> a.shift];
-        return p >= 0 && p < a.pages ? (int)(((long long)p << a.shift) + (key & ((1 << a.shift) - 1))) : -1;
+    // the cache row of key `key` of n (n > 0), -1 past them or if its page is not one
+    auto page_row = [&](const int* pages, long long key, int n) {
+        const int k = key < n ? (int)key : n - 1, p = pages[k >> a.shift];
+        const int row = (int)(((long long)p << a.shift) + (k & ((1 << a.shift) - 1)));
+        return key < n && p >= 0 && p < a.pages ? row : -1;
     };
 
     if (pre) {
@@ -141,75 +151,81 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a) {
         live = m0 < all;
         m = live ? m0 : all - 1;
         load_q(m);
-        const int n = (a.prefix + kPreKeys - 1) / kPreKeys;
+        const int n = a.pages ? (a.prefix + kPreKeys - 1) / kPreKeys : 0;
         const int j0 = (int)((long long)n * part / a.pre_parts), j1 = (int)((long long)n * (part + 1) / a.pre_parts);
         constexpr int J = kPreKeys / R::RPI / kWaves;
-        int id[J];
-        unsigned long long seen_next = 0;
-        unsigned long long seen = 0;
-        auto look_up = [&](int j) {                       // the rows of tile j this lane loads, and which keys there are
-            const int k0 = j * kPreKeys;
+        // the rows this lane loads of the tile being loaded, and which keys
+        // that tile has; the same of the next one, looked up a tile ahead
+        int id[J], id_next[J];
+        unsigned long long seen = 0, seen_next = 0;
+        auto look_up = [&](int j) {
+            const long long k0 = (long long)j * kPreKeys;
 #pragma unroll
-            for (int i = 0; i < J; ++i) {
-                const int key = k0 + (wave * J + i) * R::RPI + lane / R::C;
-                id[i] = key < a.prefix ? page_row(a.prefix_pages, key) : -1;
-            }
-            const int key = k0 + lane;
-            seen_next = __ballot(key < a.prefix && page_row(a.prefix_pages, key) >= 0);
+            for (int i = 0; i < J; ++i)
+                id_next[i] = page_row(a.prefix_pages, k0 + (wave * J + i) * R::RPI + lane / R::C, a.prefix);
+            seen_next = __ballot(page_row(a.prefix_pages, k0 + lane, a.prefix) >= 0);
         };
-        auto load = [&](int buf) {
+        // restrict for the effect told at the prompts' pass: no wait for the
+        // loads in flight before a tile's transposed reads
+        auto pass = [&](const unsigned short* __restrict__ kc, const unsigned short* __restrict__ vc) __attribute__((always_inline)) {
+            auto load = [&](int buf) {
 #pragma unroll
-            for (int i = 0; i < J; ++i) {
-                const int at = buf * kPreBytes + (wave * J + i) * 1024;
-                if (~seen_next) {                          // rows that no key fills are zeros
-                    const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if (id[i] < 0) {
-                        *(f32x4*)((char*)lds + at + lane * 16) = z;
-                        *(f32x4*)((char*)lds + at + 2 * kPreBytes + lane * 16) = z;
-                    }
-                    lds_settled();
+                for (int i = 0; i < J; ++i) {
+                    const int at = buf * kPreBytes + (wave * J + i) * 1024, r = (wave * J + i) * R::RPI + lane / R::C;
+                    id[i] = id_next[i];
+                    gather<D>(kc, a.kv_stride, id[i], r, lane, lds, at);
+                    gather<D>(vc, a.kv_stride, id[i], r, lane, lds, at + 2 * kPreBytes);
                 }
-                const int r = (wave * J + i) * R::RPI + lane / R::C;
-                gather<D>(kbase, a.kv_stride, id[i], r, lane, lds, at);
-                gather<D>(vbase, a.kv_stride, id[i], r, lane, lds, at + 2 * kPreBytes);
+            };
+            if (j0 < j1) {
+                look_up(j0);
+                load(0);
+                seen = seen_next;
+            }
+            for (int j = j0; j < j1; ++j) {
+                const int buf = (j - j0) & 1;
+                const unsigned long long has = seen;
+                if (j + 1 < j1) look_up(j + 1);
+                wait_vm(0);
+                if (~has) {
+#pragma unroll
+                    for (int i = 0; i < J; ++i) {
+                        blank(lds, buf * kPreBytes + (wave * J + i) * 1024, id[i], lane);
+                        blank(lds, (2 + buf) * kPreBytes + (wave * J + i) * 1024, id[i], lane);
+                    }
+                }
+                lds_barrier();
+                if (j + 1 < j1) {
+                    load(buf ^ 1);
+                    seen = seen_next;
+                }
+                f32x16 s[2];
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb) {
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) s[kb][v] = 0.0f;
+#pragma unroll
+                    for (int kk = 0; kk < R::KK; ++kk)
+                        s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, buf * kPreBytes, kb, kk), qf[kk], s[kb], 0, 0, 0);
+                }
+                if (~has) {
+#pragma unroll
+                    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                        for (int v = 0; v < 16; ++v)
+                            if (!((has >> (kb * 32 + acc_row(v, half))) & 1)) s[kb][v] = -INFINITY;
+                }
+                st.weigh(s, a.c);
+#pragma unroll
+                for (int ks = 0; ks < kPreKeys / 16; ++ks) {
+                    const bf16x8 pf = round8(s[ks / 2], ks % 2);
+#pragma unroll
+                    for (int db = 0; db < R::DB; ++db)
+                        st.o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, (2 + buf) * kPreBytes, db, ks), pf, st.o[db], 0, 0, 0);
+                }
             }
         };
-        if (j0 < j1) {
-            look_up(j0);
-            load(0);
-        }
-        for (int j = j0; j < j1; ++j) {
-            const int buf = (j - j0) & 1;
-            seen = seen_next;
-            if (j + 1 < j1) look_up(j + 1);
-            wait_vm(0);
-            lds_barrier();
-            if (j + 1 < j1) load(buf ^ 1);
-            f32x16 s[2];
-#pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
-#pragma unroll
-                for (int v = 0; v < 16; ++v) s[kb][v] = 0.0f;
-#pragma unroll
-                for (int kk = 0; kk < R::KK; ++kk)
-                    s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, buf * kPreBytes, kb, kk), qf[kk], s[kb], 0, 0, 0);
-            }
-            if (~seen) {
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                    for (int v = 0; v < 16; ++v)
-                        if (!((seen >> (kb * 32 + acc_row(v, half))) & 1)) s[kb][v] = -INFINITY;
-            }
-            st.weigh(s, a.c);
-#pragma unroll
-            for (int ks = 0; ks < kPreKeys / 16; ++ks) {
-                const bf16x8 pf = round8(s[ks / 2], ks % 2);
-#pragma unroll
-                for (int db = 0; db < R::DB; ++db)
-                    st.o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, (2 + buf) * kPreBytes, db, ks), pf, st.o[db], 0, 0, 0);
-            }
-        }
+        pass(kbase, vbase);
         st.l = sum_halves(st.l);
     } else {
         part = a.pre_parts + rest % a.own_parts;
@@ -220,71 +236,83 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a) {
         const long long room = (long long)a.width << a.shift;
         const int len0 = a.lengths[b], len = len0 < 0 ? 0 : len0 < room ? len0 : (int)room;
         const int* pages = a.table + (long long)b * a.width;
-        const int n = (len + kOwnKeys - 1) / kOwnKeys, cuts = a.own_parts * kWaves;
+        const int n = a.pages ? (len + kOwnKeys - 1) / kOwnKeys : 0, cuts = a.own_parts * kWaves;
         const int cut = (part - a.pre_parts) * kWaves + wave;
-        const int j0 = (int)((long long)n * cut / cuts), j1 = (int)((long long)n * (cut + 1) / cuts);
+        const int j0 = __builtin_amdgcn_readfirstlane((int)((long long)n * cut / cuts));
+        const int j1 = __builtin_amdgcn_readfirstlane((int)((long long)n * (cut + 1) / cuts));
         const int ka = wave * 2 * kOwnBytes, va = ka + kOwnBytes;
         constexpr int J = kOwnKeys / R::RPI, kTiles = kIds / kOwnKeys;
-        unsigned seen_next = 0;
-        auto load = [&](const unsigned short* base, int j, int at) {
-            const int* tid = ids[wave] + (j - j0) % kTiles * kOwnKeys;
-            seen_next = (unsigned)__ballot(tid[col] >= 0);
-            const bool whole = seen_next == ~0u;
-#pragma unroll
-            for (int i = 0; i < J; ++i) {
-                const int r = i * R::RPI + lane / R::C, id = tid[r];
-                if (!whole) {
-                    const f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if (id < 0) *(f32x4*)((char*)lds + at + i * 1024 + lane * 16) = z;
-                    lds_settled();
-                }
-                gather<D>(base, a.kv_stride, id, r, lane, lds, at + i * 1024);
-            }
-        };
         auto look_up = [&](int j) {                       // the cache rows of tiles j .. j + kTiles - 1
-            for (int i = lane; i < kIds; i += 64) {
-                const long long key = (long long)j * kOwnKeys + i;
-                ids[wave][i] = key < len ? page_row(pages, (int)key) : -1;
-            }
+#pragma unroll
+            for (int i = 0; i < kIds / 64; ++i)
+                ids[wave][i * 64 + lane] = page_row(pages, (long long)j * kOwnKeys + i * 64 + lane, len);
             lds_settled();
         };
-        for (int c0 = j0; c0 < j1; c0 += kTiles) {
-            const int c1 = c0 + kTiles < j1 ? c0 + kTiles : j1;
-            look_up(c0);
-            load(kbase, c0, ka);
-            load(vbase, c0, va);
-            for (int j = c0; j < c1; ++j) {
-                const unsigned seen = seen_next;
-                // The keys of tile j have landed, its values may be in flight:
-                // J loads, unless rows of it are left out and with them, it
-                // may be, whole loads.
-                wait_vm(~seen ? 0 : J);
-                f32x16 s[1];
+        // the rows this lane loads of tile j, and which keys there are
+        auto rows_of = [&](int j, int (&id)[J]) {
+            const int* tid = ids[wave] + (j - j0) % kTiles * kOwnKeys;
 #pragma unroll
-                for (int v = 0; v < 16; ++v) s[0][v] = 0.0f;
+            for (int i = 0; i < J; ++i) id[i] = tid[i * R::RPI + lane / R::C];
+            return __builtin_amdgcn_readfirstlane((unsigned)__ballot(tid[col] >= 0));
+        };
+        // restrict for the effect told at the prompts' pass: no wait for the
+        // loads in flight before a tile's transposed reads
+        auto pass = [&](const unsigned short* __restrict__ kc, const unsigned short* __restrict__ vc) __attribute__((always_inline)) {
+            auto load = [&](const unsigned short* base, const int (&id)[J], int at) __attribute__((always_inline)) {
 #pragma unroll
-                for (int kk = 0; kk < R::KK; ++kk)
-                    s[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, ka, 0, kk), qf[kk], s[0], 0, 0, 0);
+                for (int i = 0; i < J; ++i) gather<D>(base, a.kv_stride, id[i], i * R::RPI + lane / R::C, lane, lds, at + i * 1024);
+            };
+            auto blank_rows = [&](const int (&id)[J], int at) {
+#pragma unroll
+                for (int i = 0; i < J; ++i) blank(lds, at + i * 1024, id[i], lane);
                 lds_settled();
-                if (j + 1 < c1) load(kbase, j + 1, ka);
-                if (~seen) {
+            };
+            int id[J];
+            for (int c0 = j0; c0 < j1; c0 += kTiles) {
+                const int c1 = c0 + kTiles < j1 ? c0 + kTiles : j1;
+                look_up(c0);
+                unsigned seen = rows_of(c0, id);
+                load(kc, id, ka);
+                load(vc, id, va);
+                for (int j = c0; j < c1; ++j) {
+                    const unsigned has = seen;
+                    int was[J];
 #pragma unroll
-                    for (int v = 0; v < 16; ++v)
-                        if (!((seen >> acc_row(v, half)) & 1)) s[0][v] = -INFINITY;
+                    for (int i = 0; i < J; ++i) was[i] = id[i];
+                    wait_vm(J);                           // the keys of tile j have landed, its values may be in flight
+                    if (~has) blank_rows(was, ka);
+                    f32x16 s[1];
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) s[0][v] = 0.0f;
+#pragma unroll
+                    for (int kk = 0; kk < R::KK; ++kk)
+                        s[0] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, ka, 0, kk), qf[kk], s[0], 0, 0, 0);
+                    lds_settled();
+                    if (j + 1 < c1) {
+                        seen = rows_of(j + 1, id);
+                        load(kc, id, ka);
+                    }
+                    if (~has) {
+#pragma unroll
+                        for (int v = 0; v < 16; ++v)
+                            if (!((has >> acc_row(v, half)) & 1)) s[0][v] = -INFINITY;
+                    }
+                    st.weigh(s, a.c);
+                    wait_vm(j + 1 < c1 ? J : 0);          // its values have; the next keys may be in flight
+                    if (~has) blank_rows(was, va);
+#pragma unroll
+                    for (int ks = 0; ks < 2; ++ks) {
+                        const bf16x8 pf = round8(s[0], ks);
+#pragma unroll
+                        for (int db = 0; db < R::DB; ++db)
+                            st.o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, va, db, ks), pf, st.o[db], 0, 0, 0);
+                    }
+                    lds_settled();
+                    if (j + 1 < c1) load(vc, id, va);
                 }
-                st.weigh(s, a.c);
-                wait_vm(j + 1 < c1 && !~seen_next ? J : 0);   // its values have; the next keys may be in flight
-#pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    const bf16x8 pf = round8(s[0], ks);
-#pragma unroll
-                    for (int db = 0; db < R::DB; ++db)
-                        st.o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, va, db, ks), pf, st.o[db], 0, 0, 0);
-                }
-                lds_settled();
-                if (j + 1 < c1) load(vbase, j + 1, va);
             }
-        }
+        };
+        pass(kbase, vbase);
         // join the four waves in LDS: every wave's share in turn goes through
         // [d][column] floats at the wave's own tiles
         st.l = sum_halves(st.l);
@@ -325,7 +353,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a) {
 
     if (!live) return;
     if (!a.part_o) {                                      // one part in all: the result itself
-        const int b = (int)(m / G), head = kvh * G + (int)(m % G);
+        const int b = (int)((unsigned)m / (unsigned)G), head = kvh * G + (int)((unsigned)m % (unsigned)G);
         const float inv = st.l == 0.0f ? 0.0f : 1.0f / st.l;
         unsigned short* op = a.o[rank] + b * a.o_stride + (long long)head * D + 4 * half;
 #pragma unroll
@@ -363,8 +391,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
     __shared__ f32x4 sum[kGroups][L];
     const int parts = a.pre_parts + a.own_parts, G = a.Hq / a.Hkv;
     const long long all = (long long)a.B * G;
-    const int unit = (int)(blockIdx.x / all);
-    const long long m = blockIdx.x % all, first = (long long)unit * parts * all + m;
+    const int unit = (int)(blockIdx.x / (unsigned)all);
+    const long long m = blockIdx.x % (unsigned)all, first = (long long)unit * parts * all + m;
     const int t = threadIdx.x, i = t % L, g = t / L;
     if (t < 2 * parts) ml[t / 2][t % 2] = a.part_ml[2 * (first + t / 2 * all) + t % 2];
     __syncthreads();
@@ -391,8 +419,8 @@ __global__ __launch_bounds__(256) void attn_join_kernel(DecodeArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) x[e] *= inv;
     typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-    const int rank = unit / a.Hkv, head = unit % a.Hkv * G + (int)(m % G);
-    *(bf16x4*)(a.o[rank] + m / G * a.o_stride + (long long)head * D + 4 * i) = __builtin_convertvector(x, bf16x4);
+    const int rank = unit / a.Hkv, head = unit % a.Hkv * G + (int)((unsigned)m % (unsigned)G);
+    *(bf16x4*)(a.o[rank] + (unsigned)m / (unsigned)G * a.o_stride + (long long)head * D + 4 * i) = __builtin_convertvector(x, bf16x4);
 }
 static_assert(4 * kMaxParts <= 256, "a row's statistics are one load of the workgroup");
 
@@ -436,7 +464,8 @@ size_t decode_ws(int P, int B, int Hq, int Hkv, int D, const Cuts& c) {
 bool decode_shape(int P, int B, int Hq, int Hkv, int D, int width, int page, int prefix) {
     return P >= 1 && P <= RING_MAX_RANKS && B >= 0 && Hq >= 1 && Hkv >= 1 && width >= 0 && prefix >= 0 && page >= 1 &&
            !(page & (page - 1)) && page <= (1 << 20) && Hq % Hkv == 0 && (D == 64 || D == 128) &&
-           (long long)Hq * D < kMaxRow && (long long)width * page < (1LL << 31) && B <= (1 << 20);
+           (long long)Hq * D < kMaxRow && (long long)width * page < (1LL << 31) && B <= (1 << 20) &&
+           (long long)B * Hq < (1LL << 31);
 }
 
 }  // namespace

@@ -98,62 +98,67 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(GradArgs a) {
     }
 
     const unsigned krow = (unsigned)(a.p.k_stride * 2), vrow = (unsigned)(a.p.v_stride * 2);
-    const unsigned short* kp = a.p.k[rank] + (long long)k0 * a.p.k_stride + (long long)kvh * D;
-    const unsigned short* vp = a.p.v[rank] + (long long)k0 * a.p.v_stride + (long long)kvh * D;
+    const unsigned short* kbase = a.p.k[rank] + (long long)k0 * a.p.k_stride + (long long)kvh * D;
+    const unsigned short* vbase = a.p.v[rank] + (long long)k0 * a.p.v_stride + (long long)kvh * D;
     TileLoad<D, kStep, kWaves> kl, vl;
     kl.init(lane, wave, krow);
     vl.init(lane, wave, vrow);
     Frags<D> fr;
     fr.init(lane);
-    auto load = [&](int j, int buf) {
-        kl.issue(kp + (long long)j * kStep * a.p.k_stride, nk - (long long)j * kStep, krow, lds, buf * kTileBytes);
-        vl.issue(vp + (long long)j * kStep * a.p.v_stride, nk - (long long)j * kStep, vrow, lds, (2 + buf) * kTileBytes);
-    };
     f32x16 dq[R::DB];
 #pragma unroll
     for (int db = 0; db < R::DB; ++db)
 #pragma unroll
         for (int v = 0; v < 16; ++v) dq[db][v] = 0.0f;
     const float c = a.p.c;
-    const int tiles = (most + kStep - 1) / kStep;
-    if (tiles) load(0, 0);
-    for (int j = 0; j < tiles; ++j) {
-        const int buf = j & 1;
-        wait_vm(0);
-        lds_barrier();
-        if (j + 1 < tiles) load(j + 1, buf ^ 1);
-        if (j * kStep >= some) continue;
-        const int ka = buf * kTileBytes, va = (2 + buf) * kTileBytes;
+    // restrict for the effect told at the forward pass: no wait for the next
+    // tile's loads before a tile's transposed reads
+    auto pass = [&](const unsigned short* __restrict__ kp, const unsigned short* __restrict__ vp) __attribute__((always_inline)) {
+        auto load = [&](int j, int buf) {
+            kl.issue(kp + (long long)j * kStep * a.p.k_stride, nk - (long long)j * kStep, krow, lds, buf * kTileBytes);
+            vl.issue(vp + (long long)j * kStep * a.p.v_stride, nk - (long long)j * kStep, vrow, lds, (2 + buf) * kTileBytes);
+        };
+        const int tiles = (most + kStep - 1) / kStep;
+        if (tiles) load(0, 0);
+        for (int j = 0; j < tiles; ++j) {
+            const int buf = j & 1;
+            wait_vm(0);
+            lds_barrier();
+            if (j + 1 < tiles) load(j + 1, buf ^ 1);
+            if (j * kStep >= some) continue;
+            const int ka = buf * kTileBytes, va = (2 + buf) * kTileBytes;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-            f32x16 s, dp;
+            for (int kb = 0; kb < 2; ++kb) {
+                f32x16 s, dp;
 #pragma unroll
-            for (int v = 0; v < 16; ++v) s[v] = dp[v] = 0.0f;
+                for (int v = 0; v < 16; ++v) s[v] = dp[v] = 0.0f;
 #pragma unroll
-            for (int kk = 0; kk < R::KK; ++kk) {
-                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, ka, kb, kk), qf[kk], s, 0, 0, 0);
-                dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, va, kb, kk), gf[kk], dp, 0, 0, 0);
-            }
+                for (int kk = 0; kk < R::KK; ++kk) {
+                    s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, ka, kb, kk), qf[kk], s, 0, 0, 0);
+                    dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, va, kb, kk), gf[kk], dp, 0, 0, 0);
+                }
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const float p = exp2_hw(__builtin_fmaf(s[v], c, -lse2));
-                s[v] = p * (dp[v] - delta);
-            }
-            if ((j + 1) * kStep > every) {
+                for (int v = 0; v < 16; ++v) {
+                    const float p = exp2_hw(__builtin_fmaf(s[v], c, -lse2));
+                    s[v] = p * (dp[v] - delta);
+                }
+                if ((j + 1) * kStep > every) {
 #pragma unroll
-                for (int v = 0; v < 16; ++v)
-                    if (j * kStep + kb * 32 + acc_row(v, half) >= seen) s[v] = 0.0f;
-            }
-            // dS is rounded to bf16 for the matrix cores, as P is going forward
+                    for (int v = 0; v < 16; ++v)
+                        if (j * kStep + kb * 32 + acc_row(v, half) >= seen) s[v] = 0.0f;
+                }
+                // dS is rounded to bf16 for the matrix cores, as P is going forward
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                const bf16x8 sf = round8(s, ks);
+                for (int ks = 0; ks < 2; ++ks) {
+                    const bf16x8 sf = round8(s, ks);
 #pragma unroll
-                for (int db = 0; db < R::DB; ++db)
-                    dq[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, ka, db, 2 * kb + ks), sf, dq[db], 0, 0, 0);
+                    for (int db = 0; db < R::DB; ++db)
+                        dq[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, ka, db, 2 * kb + ks), sf, dq[db], 0, 0, 0);
+                }
             }
         }
-    }
+    };
+    pass(kbase, vbase);
     store_column<D>(a.dq[rank] + (q0 + (long long)qi) * a.dq_stride + (long long)head * D, dq, a.scale, half, live);
 }
 
@@ -195,73 +200,78 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_kernel(GradArgs
     gl.init(lane, wave, grow);
     Frags<D> fr;
     fr.init(lane);
-    int lg = 0, lt = t0;                                               // the next tile to load: head of the group, tile
-    auto load = [&](int buf) {
-        const int head = kvh * G + lg;
-        const long long t = q0 + (long long)lt * kStep;
-        const long long left = nq - (long long)lt * kStep;
-        ql.issue(a.p.q[rank] + t * a.p.q_stride + (long long)head * D, left, qrow, lds, buf * kTileBytes);
-        gl.issue(a.go[rank] + t * a.go_stride + (long long)head * D, left, grow, lds, (2 + buf) * kTileBytes);
-        if (wave < 2) {                                                // wave 0: lse, wave 1: delta, one value per lane
-            const float* st = (wave ? a.delta : a.lse2) + ((long long)rank * a.p.Hq + head) * a.p.Tq + t;
-            load_floats(st, left < kStep ? (int)left : kStep, lds, 4 * kTileBytes + (2 * buf + wave) * kStep * 4, lane);
-        }
-        if (++lt == t1) {
-            lt = t0;
-            ++lg;
-        }
-    };
     f32x16 dk[R::DB], dv[R::DB];
 #pragma unroll
     for (int db = 0; db < R::DB; ++db)
 #pragma unroll
         for (int v = 0; v < 16; ++v) dk[db][v] = dv[db][v] = 0.0f;
     const float c = a.p.c;
-    if (total) load(0);
-    int ct = t0;                                                       // the tile being computed
-    for (int it = 0; it < total; ++it) {
-        const int buf = it & 1;
-        wait_vm(0);
-        lds_barrier();
-        if (it + 1 < total) load(buf ^ 1);
-        const int q = ct * kStep;
-        if (++ct == t1) ct = t0;
-        const int qa = buf * kTileBytes, ga = (2 + buf) * kTileBytes;
-        const float* stat = (const float*)((const char*)lds + 4 * kTileBytes + 2 * buf * kStep * 4);
-#pragma unroll
-        for (int qb = 0; qb < kStep / 32; ++qb) {
-            const int qr = q + qb * 32;
-            if (a.p.causal && qr + 31 + off < key0) continue;          // none of these queries sees a key of the wave
-            f32x16 s, dp;
-#pragma unroll
-            for (int v = 0; v < 16; ++v) s[v] = dp[v] = 0.0f;
-#pragma unroll
-            for (int kk = 0; kk < R::KK; ++kk) {
-                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, qa, qb, kk), kf[kk], s, 0, 0, 0);
-                dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, ga, qb, kk), vf[kk], dp, 0, 0, 0);
+    // restrict for the effect told at the forward pass: no wait for the next
+    // tile's loads before a tile's transposed reads
+    auto pass = [&](const unsigned short* __restrict__ qp, const unsigned short* __restrict__ gp) __attribute__((always_inline)) {
+        int lg = 0, lt = t0;                                               // the next tile to load: head of the group, tile
+        auto load = [&](int buf) {
+            const int head = kvh * G + lg;
+            const long long t = q0 + (long long)lt * kStep;
+            const long long left = nq - (long long)lt * kStep;
+            ql.issue(qp + t * a.p.q_stride + (long long)head * D, left, qrow, lds, buf * kTileBytes);
+            gl.issue(gp + t * a.go_stride + (long long)head * D, left, grow, lds, (2 + buf) * kTileBytes);
+            if (wave < 2) {                                                // wave 0: lse, wave 1: delta, one value per lane
+                const float* st = (wave ? a.delta : a.lse2) + ((long long)rank * a.p.Hq + head) * a.p.Tq + t;
+                load_floats(st, left < kStep ? (int)left : kStep, lds, 4 * kTileBytes + (2 * buf + wave) * kStep * 4, lane);
             }
-#pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                const int r = qb * 32 + acc_row(v, half);
-                s[v] = exp2_hw(__builtin_fmaf(s[v], c, -stat[r]));
-                dp[v] = s[v] * (dp[v] - stat[kStep + r]);
+            if (++lt == t1) {
+                lt = t0;
+                ++lg;
             }
-            if (a.p.causal && qr + off < key0 + 31) {
+        };
+        if (total) load(0);
+        int ct = t0;                                                       // the tile being computed
+        for (int it = 0; it < total; ++it) {
+            const int buf = it & 1;
+            wait_vm(0);
+            lds_barrier();
+            if (it + 1 < total) load(buf ^ 1);
+            const int q = ct * kStep;
+            if (++ct == t1) ct = t0;
+            const int qa = buf * kTileBytes, ga = (2 + buf) * kTileBytes;
+            const float* stat = (const float*)((const char*)lds + 4 * kTileBytes + 2 * buf * kStep * 4);
 #pragma unroll
-                for (int v = 0; v < 16; ++v)
-                    if (qr + acc_row(v, half) + off < key) s[v] = dp[v] = 0.0f;
-            }
+            for (int qb = 0; qb < kStep / 32; ++qb) {
+                const int qr = q + qb * 32;
+                if (a.p.causal && qr + 31 + off < key0) continue;          // none of these queries sees a key of the wave
+                f32x16 s, dp;
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                const bf16x8 pf = round8(s, ks), sf = round8(dp, ks);
+                for (int v = 0; v < 16; ++v) s[v] = dp[v] = 0.0f;
 #pragma unroll
-                for (int db = 0; db < R::DB; ++db) {
-                    dv[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, ga, db, 2 * qb + ks), pf, dv[db], 0, 0, 0);
-                    dk[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, qa, db, 2 * qb + ks), sf, dk[db], 0, 0, 0);
+                for (int kk = 0; kk < R::KK; ++kk) {
+                    s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, qa, qb, kk), kf[kk], s, 0, 0, 0);
+                    dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, ga, qb, kk), vf[kk], dp, 0, 0, 0);
+                }
+#pragma unroll
+                for (int v = 0; v < 16; ++v) {
+                    const int r = qb * 32 + acc_row(v, half);
+                    s[v] = exp2_hw(__builtin_fmaf(s[v], c, -stat[r]));
+                    dp[v] = s[v] * (dp[v] - stat[kStep + r]);
+                }
+                if (a.p.causal && qr + off < key0 + 31) {
+#pragma unroll
+                    for (int v = 0; v < 16; ++v)
+                        if (qr + acc_row(v, half) + off < key) s[v] = dp[v] = 0.0f;
+                }
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    const bf16x8 pf = round8(s, ks), sf = round8(dp, ks);
+#pragma unroll
+                    for (int db = 0; db < R::DB; ++db) {
+                        dv[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, ga, db, 2 * qb + ks), pf, dv[db], 0, 0, 0);
+                        dk[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, qa, db, 2 * qb + ks), sf, dk[db], 0, 0, 0);
+                    }
                 }
             }
         }
-    }
+    };
+    pass(a.p.q[rank], a.go[rank]);
     store_column<D>(a.dk[rank] + (k0 + (long long)keyc) * a.dk_stride + (long long)kvh * D, dk, a.scale, half, key < nk);
     store_column<D>(a.dv[rank] + (k0 + (long long)keyc) * a.dv_stride + (long long)kvh * D, dv, 1.0f, half, key < nk);
 }

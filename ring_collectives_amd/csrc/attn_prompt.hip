@@ -72,18 +72,13 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
         for (int kk = 0; kk < R::KK; ++kk) qf[kk] = *(const bf16x8*)(qp + 16 * kk);
     }
     const unsigned krow = (unsigned)(a.p.k_stride * 2), vrow = (unsigned)(a.p.v_stride * 2);
-    const unsigned short* kp = a.p.k[rank] + (long long)k0 * a.p.k_stride + (long long)kvh * D;
-    const unsigned short* vp = a.p.v[rank] + (long long)k0 * a.p.v_stride + (long long)kvh * D;
+    const unsigned short* kbase = a.p.k[rank] + (long long)k0 * a.p.k_stride + (long long)kvh * D;
+    const unsigned short* vbase = a.p.v[rank] + (long long)k0 * a.p.v_stride + (long long)kvh * D;
     TileLoad<D, kTileKeys, kWaves> kl, vl;
     kl.init(lane, wave, krow);
     vl.init(lane, wave, vrow);
     Frags<D> fr;
     fr.init(lane);
-    auto load = [&](int j, int buf) {
-        kl.issue(kp + (long long)j * kTileKeys * a.p.k_stride, nk - (long long)j * kTileKeys, krow, lds, buf * kTileBytes);
-        vl.issue(vp + (long long)j * kTileKeys * a.p.v_stride, nk - (long long)j * kTileKeys, vrow, lds, (2 + buf) * kTileBytes);
-    };
-
     f32x16 o[R::DB];
 #pragma unroll
     for (int db = 0; db < R::DB; ++db)
@@ -92,68 +87,79 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
     float mc = -INFINITY, l = 0.0f;       // running maximum times c (both halves), this half's share of the sum
     const float c = a.p.c;
 
-    const int tiles = (most + kTileKeys - 1) / kTileKeys;
-    if (tiles) load(0, 0);
-    for (int j = 0; j < tiles; ++j) {
-        const int buf = j & 1;
-        wait_vm(0);                       // tile j has landed
-        lds_barrier();                    // everyone's has; the buffers of tile j - 1 are free
-        if (j + 1 < tiles) load(j + 1, buf ^ 1);
-        if (j * kTileKeys >= some) continue;    // nothing here for this wave's rows
-        const int ka = buf * kTileBytes, va = (2 + buf) * kTileBytes;
-        f32x16 s[2];
+    // The pass is a function of restrict pointers for one effect: its LDS reads
+    // are then known not to alias what it loads from, and the compiler leaves
+    // out the wait for every load in flight, the next tile's, that it otherwise
+    // puts before each tile's first transposed read.
+    auto pass = [&](const unsigned short* __restrict__ kp, const unsigned short* __restrict__ vp) __attribute__((always_inline)) {
+        auto load = [&](int j, int buf) {
+            kl.issue(kp + (long long)j * kTileKeys * a.p.k_stride, nk - (long long)j * kTileKeys, krow, lds, buf * kTileBytes);
+            vl.issue(vp + (long long)j * kTileKeys * a.p.v_stride, nk - (long long)j * kTileKeys, vrow, lds, (2 + buf) * kTileBytes);
+        };
+        const int tiles = (most + kTileKeys - 1) / kTileKeys;
+        if (tiles) load(0, 0);
+        for (int j = 0; j < tiles; ++j) {
+            const int buf = j & 1;
+            wait_vm(0);                       // tile j has landed
+            lds_barrier();                    // everyone's has; the buffers of tile j - 1 are free
+            if (j + 1 < tiles) load(j + 1, buf ^ 1);
+            if (j * kTileKeys >= some) continue;    // nothing here for this wave's rows
+            const int ka = buf * kTileBytes, va = (2 + buf) * kTileBytes;
+            f32x16 s[2];
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
+            for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
-            for (int v = 0; v < 16; ++v) s[kb][v] = 0.0f;
+                for (int v = 0; v < 16; ++v) s[kb][v] = 0.0f;
 #pragma unroll
-            for (int kk = 0; kk < R::KK; ++kk)
-                s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, ka, kb, kk), qf[kk], s[kb], 0, 0, 0);
-        }
-        if ((j + 1) * kTileKeys > every) {
+                for (int kk = 0; kk < R::KK; ++kk)
+                    s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, ka, kb, kk), qf[kk], s[kb], 0, 0, 0);
+            }
+            if ((j + 1) * kTileKeys > every) {
+#pragma unroll
+                for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v)
+                        if (j * kTileKeys + kb * 32 + acc_row(v, half) >= seen) s[kb][v] = -INFINITY;
+            }
+            float mx = s[0][0];
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-                for (int v = 0; v < 16; ++v)
-                    if (j * kTileKeys + kb * 32 + acc_row(v, half) >= seen) s[kb][v] = -INFINITY;
-        }
-        float mx = s[0][0];
+                for (int v = 0; v < 16; ++v) mx = fmaxf(mx, s[kb][v]);
+            mx = max_halves(mx) * c;
+            // The maximum only keeps the exponents in range: it moves when some
+            // row's grows by more than 2^8, which P in bf16 and its fp32 sums hold
+            // as exactly as values up to 1.
+            if (__any(mx > mc + 8.0f)) {
+                const float mn = fmaxf(mc, mx);
+                const float alpha = mn == -INFINITY ? 1.0f : exp2_hw(mc - mn);
+                mc = mn;
+                l *= alpha;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
+                for (int db = 0; db < R::DB; ++db)
 #pragma unroll
-            for (int v = 0; v < 16; ++v) mx = fmaxf(mx, s[kb][v]);
-        mx = max_halves(mx) * c;
-        // The maximum only keeps the exponents in range: it moves when some
-        // row's grows by more than 2^8, which P in bf16 and its fp32 sums hold
-        // as exactly as values up to 1.
-        if (__any(mx > mc + 8.0f)) {
-            const float mn = fmaxf(mc, mx);
-            const float alpha = mn == -INFINITY ? 1.0f : exp2_hw(mc - mn);
-            mc = mn;
-            l *= alpha;
-#pragma unroll
-            for (int db = 0; db < R::DB; ++db)
-#pragma unroll
-                for (int v = 0; v < 16; ++v) o[db][v] *= alpha;
-        }
-        const float sub = mc == -INFINITY ? 0.0f : mc;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                s[kb][v] = exp2_hw(__builtin_fmaf(s[kb][v], c, -sub));
-                l += s[kb][v];
+                    for (int v = 0; v < 16; ++v) o[db][v] *= alpha;
             }
-        // P is rounded to bf16 for the matrix cores (relative error 2^-9 of
-        // each weight; l sums the unrounded ones in fp32).
+            const float sub = mc == -INFINITY ? 0.0f : mc;
 #pragma unroll
-        for (int ks = 0; ks < kTileKeys / 16; ++ks) {
-            const bf16x8 pf = round8(s[ks / 2], ks % 2);
+            for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-            for (int db = 0; db < R::DB; ++db)
-                o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, va, db, ks), pf, o[db], 0, 0, 0);
+                for (int v = 0; v < 16; ++v) {
+                    s[kb][v] = exp2_hw(__builtin_fmaf(s[kb][v], c, -sub));
+                    l += s[kb][v];
+                }
+            // P is rounded to bf16 for the matrix cores (relative error 2^-9 of
+            // each weight; l sums the unrounded ones in fp32).
+#pragma unroll
+            for (int ks = 0; ks < kTileKeys / 16; ++ks) {
+                const bf16x8 pf = round8(s[ks / 2], ks % 2);
+#pragma unroll
+                for (int db = 0; db < R::DB; ++db)
+                    o[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, va, db, ks), pf, o[db], 0, 0, 0);
+            }
         }
-    }
+    };
+    pass(kbase, vbase);
 
     l = sum_halves(l);
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;          // a row that sees no key gives zeros
