@@ -7,8 +7,13 @@
 // four waves takes 128 rows of one (rank, key head): row i G + g is query i of
 // the prompt and query head g of the G that share the key head, so the group
 // reads every key tile once.  Each wave keeps 32 of the rows (its Q fragments
-// and the accumulators of O^T) in registers; key and value tiles of 64 rows go
-// through two LDS buffers each, the next tile loading while one is computed.
+// and the accumulators of O^T) in registers; key and value tiles go through two
+// LDS buffers each, the next tile loading while one is computed.
+//
+// Tiles of 64 keys and two workgroups on a compute unit, one computing its
+// weights while the other multiplies; for D = 128, where many short prompts
+// make many workgroups that spend much of their time in their first loads and
+// last stores, tiles of 32 keys and three (kShort).
 #include "attn_core.h"
 #include "attn_internal.h"
 
@@ -18,8 +23,13 @@ namespace ringc {
 namespace {
 
 constexpr int kTileRows = 128;     // rows (query, head of the group) of a workgroup
-constexpr int kTileKeys = 64;      // keys of a tile
 constexpr int kWaves = 4;
+// D = 128 takes tiles of 32 keys below this many keys a prompt on average, with
+// more than four workgroups a compute unit: 8192 tokens on 4 ranks of 8 heads
+// on 2 in prompts of 64 / 256 / 683 / 2048 keys take 33 / 47 / 73 / 166 us with
+// 32 and 42 / 50 / 77 / 164 us with 64; one prompt of 1000, 31 and 24 us.
+constexpr int kShort = 1024;
+constexpr int kAhead = 4;        // row fragments asked for ahead of their MFMA
 
 struct FwdArgs {
     PromptArgs p;
@@ -29,8 +39,8 @@ struct FwdArgs {
     int slots;
 };
 
-template <int D>
-__global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
+template <int D, int kTileKeys>
+__global__ __launch_bounds__(256, kTileKeys == 32 ? 3 : 2) void attn_fwd_kernel(FwdArgs a) {
     typedef Rows<D> R;
     constexpr int kTileBytes = kTileKeys * R::RB;
     __shared__ __align__(4096) unsigned short lds[4 * kTileBytes / 2];   // K 0, K 1, V 0, V 1
@@ -84,7 +94,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
     for (int db = 0; db < R::DB; ++db)
 #pragma unroll
         for (int v = 0; v < 16; ++v) o[db][v] = 0.0f;
-    float mc = -INFINITY, l = 0.0f;       // running maximum times c (both halves), this half's share of the sum
+    float mc = -INFINITY;                 // running maximum times c (of both halves of the column)
+    float lp[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // this half's share of the sum, in four parts
     const float c = a.p.c;
 
     // The pass is a function of restrict pointers for one effect: its LDS reads
@@ -105,25 +116,37 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
             if (j + 1 < tiles) load(j + 1, buf ^ 1);
             if (j * kTileKeys >= some) continue;    // nothing here for this wave's rows
             const int ka = buf * kTileBytes, va = (2 + buf) * kTileBytes;
-            f32x16 s[2];
+            f32x16 s[kTileKeys / 32];
+            // row reads kAhead MFMAs early; left alone, the compiler puts each
+            // next to its use and waits out the LDS latency every time
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb) {
+            for (int kb = 0; kb < kTileKeys / 32; ++kb)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) s[kb][v] = 0.0f;
 #pragma unroll
-                for (int kk = 0; kk < R::KK; ++kk)
+            for (int kk = 0; kk < R::KK; ++kk)
+#pragma unroll
+                for (int kb = 0; kb < kTileKeys / 32; ++kb)
                     s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, ka, kb, kk), qf[kk], s[kb], 0, 0, 0);
+            __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+            for (int i = 0; i < kTileKeys / 32 * R::KK - kAhead; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
             }
+            __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+            __builtin_amdgcn_sched_barrier(0);
             if ((j + 1) * kTileKeys > every) {
 #pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
+                for (int kb = 0; kb < kTileKeys / 32; ++kb)
 #pragma unroll
                     for (int v = 0; v < 16; ++v)
                         if (j * kTileKeys + kb * 32 + acc_row(v, half) >= seen) s[kb][v] = -INFINITY;
             }
             float mx = s[0][0];
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
+            for (int kb = 0; kb < kTileKeys / 32; ++kb)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) mx = fmaxf(mx, s[kb][v]);
             mx = max_halves(mx) * c;
@@ -134,7 +157,8 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
                 const float mn = fmaxf(mc, mx);
                 const float alpha = mn == -INFINITY ? 1.0f : exp2_hw(mc - mn);
                 mc = mn;
-                l *= alpha;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) lp[i] *= alpha;
 #pragma unroll
                 for (int db = 0; db < R::DB; ++db)
 #pragma unroll
@@ -142,11 +166,11 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
             }
             const float sub = mc == -INFINITY ? 0.0f : mc;
 #pragma unroll
-            for (int kb = 0; kb < 2; ++kb)
+            for (int kb = 0; kb < kTileKeys / 32; ++kb)
 #pragma unroll
                 for (int v = 0; v < 16; ++v) {
                     s[kb][v] = exp2_hw(__builtin_fmaf(s[kb][v], c, -sub));
-                    l += s[kb][v];
+                    lp[v % 4] += s[kb][v];
                 }
             // P is rounded to bf16 for the matrix cores (relative error 2^-9 of
             // each weight; l sums the unrounded ones in fp32).
@@ -160,8 +184,58 @@ __global__ __launch_bounds__(256, 2) void attn_fwd_kernel(FwdArgs a) {
         }
     };
     pass(kbase, vbase);
+    float l = sum_halves((lp[0] + lp[1]) + (lp[2] + lp[3]));
 
-    l = sum_halves(l);
+    // The product of a weight that the mask made 0 with a value that is not
+    // finite is NaN, in rows that do not see the value.  So where a result of a
+    // causal call is not finite the wave makes its rows again, key by key, each
+    // key added only to the rows that see it.
+    if (a.p.causal) {
+        float z = 0.0f * l;
+#pragma unroll
+        for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+            for (int v = 0; v < 16; ++v) z = __builtin_fmaf(o[db][v], 0.0f, z);
+        if (__any(z != 0.0f)) {
+            mc = -INFINITY;
+            l = 0.0f;
+#pragma unroll
+            for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+                for (int v = 0; v < 16; ++v) o[db][v] = 0.0f;
+            for (int key = 0; key < some; ++key) {
+                const unsigned short* kr = kbase + (long long)key * a.p.k_stride + 8 * half;
+                const unsigned short* vr = vbase + (long long)key * a.p.v_stride + 4 * half;
+                float s = 0.0f;
+#pragma unroll
+                for (int kk = 0; kk < R::KK; ++kk) {
+                    const bf16x8 x = *(const bf16x8*)(kr + 16 * kk);
+                    bf16x8 y = qf[kk];
+                    asm volatile("" : "+v"(y));          // converted here, not once for all keys
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s = __builtin_fmaf((float)y[e], (float)x[e], s);
+                    __builtin_amdgcn_sched_barrier(0);   // few registers, not speed
+                }
+                const bool sees = key < seen;
+                s = sees ? sum_halves(s) * c : -INFINITY;
+                const float mn = fmaxf(mc, s), sub = mn == -INFINITY ? 0.0f : mn;
+                const float alpha = mn == mc ? 1.0f : exp2_hw(mc - mn), w = exp2_hw(s - sub);
+                mc = mn;
+                l = l * alpha + w;
+#pragma unroll
+                for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+                    for (int v = 0; v < 16; v += 4) {
+                        typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+                        const bf16x4 x = *(const bf16x4*)(vr + 32 * db + 2 * v);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            o[db][v + e] = sees ? __builtin_fmaf(w, (float)x[e], o[db][v + e] * alpha) : o[db][v + e];
+                        __builtin_amdgcn_sched_barrier(0);
+                    }
+            }
+        }
+    }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;          // a row that sees no key gives zeros
     store_column<D>(a.o[rank] + (q0 + (long long)qi) * a.o_stride + (long long)head * D, o, inv, half, live);
     if (a.lse[rank] && live && half == 0)
@@ -247,9 +321,12 @@ extern "C" int tp_attention(const void* const* q, const void* const* k, const vo
     a.slots = prompt_slots(B, Tq, Hq / Hkv, kTileRows, units);
     if (!a.slots) return RING_EUNSUPPORTED;
     const dim3 grid((unsigned)a.slots * (unsigned)units);
-    if (D == 128)
-        hipLaunchKernelGGL(attn_fwd_kernel<128>, grid, dim3(256), 0, (hipStream_t)stream, a);
+    hipStream_t st = (hipStream_t)stream;
+    if (D == 64)
+        hipLaunchKernelGGL((attn_fwd_kernel<64, 64>), grid, dim3(256), 0, st, a);
+    else if (Tk / B < kShort && (long long)a.slots * units > 4LL * dev_info().cus)
+        hipLaunchKernelGGL((attn_fwd_kernel<128, 32>), grid, dim3(256), 0, st, a);
     else
-        hipLaunchKernelGGL(attn_fwd_kernel<64>, grid, dim3(256), 0, (hipStream_t)stream, a);
+        hipLaunchKernelGGL((attn_fwd_kernel<128, 64>), grid, dim3(256), 0, st, a);
     return hipGetLastError() == hipSuccess ? RING_OK : RING_EHIP;
 }

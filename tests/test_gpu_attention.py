@@ -281,6 +281,29 @@ def test_attention_rows_of_other_prompts_take_no_part():
     assert o[0][:50].isnan().all()                       # a prompt of NaN is NaN
 
 
+@pytest.mark.parametrize("at,bad", [(70, float("nan")), (40, float("inf")), (199, float("-inf")), (0, float("nan"))])
+@pytest.mark.parametrize("Hq,Hkv,D", [(1, 1, 64), (4, 1, 128)])
+def test_attention_keys_and_values_that_a_causal_query_does_not_see(at, bad, Hq, Hkv, D):
+    """A key and value that are not finite reach only the queries from their
+    own place on; the others, of the same tiles too, are as without them."""
+    lq = [200]
+    q, k, v = attn_inputs(1, lq, lq, Hq, Hkv, D, seed=at)
+    o, lse = ([poisoned((200, Hq, D))], [poisoned((Hq, 200), torch.float32)])
+    v[0][at, 0, 5] = bad
+    A.tp_attention(q, k, v, o, cu(lq), cu(lq), lse=lse)
+    torch.cuda.synchronize()
+    if at:
+        part = slice(0, at)
+        check_attention([q[0][part]], [k[0][part]], [v[0][part]], [o[0][part]], [lse[0][:, part]], [at], [at], True, D ** -0.5)
+    assert not o[0][at:, :, 5].isfinite().any() and o[0][at:, :, 6].isfinite().all()
+    k[0][at, 0, 3] = float("nan")
+    A.tp_attention(q, k, v, o, cu(lq), cu(lq), lse=lse)
+    torch.cuda.synchronize()
+    if at:
+        check_attention([q[0][part]], [k[0][part]], [v[0][part]], [o[0][part]], [lse[0][:, part]], [at], [at], True, D ** -0.5)
+    assert o[0][at:].isnan().all()
+
+
 def test_attention_offsets_outside_the_tensors_are_not_followed():
     q, k, v = attn_inputs(1, [60], [60], 2, 1, 64, seed=9)
     o, lse = [torch.zeros(60, 2, 64, dtype=BF, device="cuda")], [torch.zeros(2, 60, device="cuda")]
