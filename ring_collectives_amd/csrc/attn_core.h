@@ -205,33 +205,35 @@ __device__ __forceinline__ bool find_tile(const int* cu, const int* cu2, int B, 
     return false;
 }
 
-// Store the lane's column of a D x 32 block of accumulators, times f, as bf16
-// to its row p: the two halves of the wave trade so that each lane stores 16
+// Store the lane's column of a 32 x 32 block of accumulators, times f, as bf16
+// to p on: the two halves of the wave trade so that each lane stores 16
 // contiguous bytes.
-template <int D, class Acc>
-__device__ __forceinline__ void store_column(unsigned short* p, const Acc& x, float f, int half, bool live) {
+__device__ __forceinline__ void store_block(unsigned short* p, const f32x16& x, float f, int half, bool live) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     typedef float f32x2 __attribute__((ext_vector_type(2)));
 #pragma unroll
-    for (int db = 0; db < Rows<D>::DB; ++db)
+    for (int j = 0; j < 4; j += 2) {
+        u32x4 y;
 #pragma unroll
-        for (int j = 0; j < 4; j += 2) {
-            u32x4 y;
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                // values 8 j + 4 half + 2 e, + 1 and the same of j + 1: of the
-                // pair the lower half keeps j's and gets the upper's, the
-                // upper half j + 1's
-                const f32x2 lo = {x[db][4 * j + 2 * e] * f, x[db][4 * j + 2 * e + 1] * f};
-                const f32x2 hi = {x[db][4 * j + 4 + 2 * e] * f, x[db][4 * j + 5 + 2 * e] * f};
-                const auto r = __builtin_amdgcn_permlane32_swap(
-                    __builtin_bit_cast(unsigned, __builtin_convertvector(lo, bf16x2)),
-                    __builtin_bit_cast(unsigned, __builtin_convertvector(hi, bf16x2)), false, false);
-                y[e] = r[0];
-                y[2 + e] = r[1];
-            }
-            if (live) *(u32x4*)(p + 32 * db + 8 * (j + half)) = y;
+        for (int e = 0; e < 2; ++e) {
+            // values 8 j + 4 half + 2 e, + 1 and the same of j + 1: of the pair
+            // the lower half keeps j's and gets the upper's, the upper half
+            // j + 1's
+            const f32x2 lo = {x[4 * j + 2 * e] * f, x[4 * j + 2 * e + 1] * f};
+            const f32x2 hi = {x[4 * j + 4 + 2 * e] * f, x[4 * j + 5 + 2 * e] * f};
+            const auto r = __builtin_amdgcn_permlane32_swap(
+                __builtin_bit_cast(unsigned, __builtin_convertvector(lo, bf16x2)),
+                __builtin_bit_cast(unsigned, __builtin_convertvector(hi, bf16x2)), false, false);
+            y[e] = r[0];
+            y[2 + e] = r[1];
         }
+        if (live) *(u32x4*)(p + 8 * (j + half)) = y;
+    }
+}
+template <int D, class Acc>
+__device__ __forceinline__ void store_column(unsigned short* p, const Acc& x, float f, int half, bool live) {
+#pragma unroll
+    for (int db = 0; db < Rows<D>::DB; ++db) store_block(p + 32 * db, x[db], f, half, live);
 }
 
 // Arguments of the packed-prompt kernels (per-rank pointers by value).

@@ -20,6 +20,7 @@ namespace {
 constexpr int kRowsWG = 128;   // query rows, or keys, of a workgroup
 constexpr int kStep = 64;      // keys, or queries, of a tile
 constexpr int kWaves = 4;
+constexpr int kAhead = 4;       // row fragments asked for ahead of their MFMA
 
 struct GradArgs {
     PromptArgs p;
@@ -130,6 +131,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(GradArgs a) {
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
                 f32x16 s, dp;
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int v = 0; v < 16; ++v) s[v] = dp[v] = 0.0f;
 #pragma unroll
@@ -137,6 +139,14 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(GradArgs a) {
                     s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, ka, kb, kk), qf[kk], s, 0, 0, 0);
                     dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, va, kb, kk), gf[kk], dp, 0, 0, 0);
                 }
+                __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+                for (int i = 0; i < 2 * R::KK - kAhead; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                }
+                __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int v = 0; v < 16; ++v) {
                     const float p = exp2_hw(__builtin_fmaf(s[v], c, -lse2));
@@ -241,6 +251,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_kernel(GradArgs
                 const int qr = q + qb * 32;
                 if (a.p.causal && qr + 31 + off < key0) continue;          // none of these queries sees a key of the wave
                 f32x16 s, dp;
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int v = 0; v < 16; ++v) s[v] = dp[v] = 0.0f;
 #pragma unroll
@@ -248,6 +259,14 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_kernel(GradArgs
                     s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, qa, qb, kk), kf[kk], s, 0, 0, 0);
                     dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, ga, qb, kk), vf[kk], dp, 0, 0, 0);
                 }
+                __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+                for (int i = 0; i < 2 * R::KK - kAhead; ++i) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                }
+                __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int v = 0; v < 16; ++v) {
                     const int r = qb * 32 + acc_row(v, half);
@@ -259,14 +278,21 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_kernel(GradArgs
                     for (int v = 0; v < 16; ++v)
                         if (qr + acc_row(v, half) + off < key) s[v] = dp[v] = 0.0f;
                 }
+                // columns of dO and Q in turn, kAhead ahead of their MFMA
+                bf16x8 col[kAhead];
+                auto column = [&](int i) {
+                    col[i % kAhead] = fr.cols(lds, i % 2 ? qa : ga, i / 2 % R::DB, 2 * qb + i / (2 * R::DB));
+                };
 #pragma unroll
-                for (int ks = 0; ks < 2; ++ks) {
-                    const bf16x8 pf = round8(s, ks), sf = round8(dp, ks);
+                for (int i = 0; i < kAhead; ++i) column(i);
+                const bf16x8 pf[2] = {round8(s, 0), round8(s, 1)}, sf[2] = {round8(dp, 0), round8(dp, 1)};
 #pragma unroll
-                    for (int db = 0; db < R::DB; ++db) {
-                        dv[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, ga, db, 2 * qb + ks), pf, dv[db], 0, 0, 0);
-                        dk[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, qa, db, 2 * qb + ks), sf, dk[db], 0, 0, 0);
-                    }
+                for (int i = 0; i < 4 * R::DB; ++i) {
+                    const bf16x8 x = col[i % kAhead];
+                    if (i + kAhead < 4 * R::DB) column(i + kAhead);
+                    f32x16& acc = i % 2 ? dk[i / 2 % R::DB] : dv[i / 2 % R::DB];
+                    acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, i % 2 ? sf[i / (2 * R::DB)] : pf[i / (2 * R::DB)], acc, 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
                 }
             }
         }
@@ -274,6 +300,142 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_kernel(GradArgs
     pass(a.p.q[rank], a.go[rank]);
     store_column<D>(a.dk[rank] + (k0 + (long long)keyc) * a.dk_stride + (long long)kvh * D, dk, a.scale, half, key < nk);
     store_column<D>(a.dv[rank] + (k0 + (long long)keyc) * a.dv_stride + (long long)kvh * D, dv, 1.0f, half, key < nk);
+}
+
+// dK and dV where there are few keys for the device's compute units: a
+// workgroup takes 32 keys, and its waves each a quarter of the (head of the
+// group, 32 queries) items, every wave with LDS of its own and no barrier
+// before the end, where the four sums are added in LDS, in the waves' order.
+// Four times the workgroups, and a quarter of the steps one after the other,
+// for four times the loads of Q and dO.
+template <int D>
+__global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_few_kernel(GradArgs a) {
+    typedef Rows<D> R;
+    constexpr int kRows = 32, kPart = kRows * R::RB;     // queries of an item, bytes of its Q (or dO) tile
+    constexpr int kStat = 64 * 4;                        // a load instruction of floats fills 64, the upper 32 with zeros
+    // per wave: stages of Q and dO; then, per wave and stage, lse and delta
+    __shared__ __align__(4096) unsigned short lds[kWaves * (4 * kPart + 4 * kStat) / 2];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int half = lane >> 5, col = lane & 31;
+    int unit, slot;
+    unit_slot(a.p.P * a.p.Hkv, a.slots, blockIdx.x, unit, slot);
+    const int G = a.p.Hq / a.p.Hkv, rank = unit / a.p.Hkv, kvh = unit % a.p.Hkv;
+    PromptTile pt;
+    if (!find_tile(a.p.cu_k, a.p.cu_q, a.p.B, a.p.Tk, a.p.Tq, 1, kRows, slot, lane, pt)) return;
+    const int k0 = pt.lo, nk = pt.n, q0 = pt.lo2, nq = pt.n2, off = nk - nq;
+    const int key0 = pt.tile * kRows, key = key0 + col, keyc = key < nk ? key : nk - 1;
+    bf16x8 kf[R::KK], vf[R::KK];
+    {
+        const unsigned short* kp = a.p.k[rank] + (k0 + (long long)keyc) * a.p.k_stride + (long long)kvh * D + 8 * half;
+        const unsigned short* vp = a.p.v[rank] + (k0 + (long long)keyc) * a.p.v_stride + (long long)kvh * D + 8 * half;
+#pragma unroll
+        for (int kk = 0; kk < R::KK; ++kk) {
+            kf[kk] = *(const bf16x8*)(kp + 16 * kk);
+            vf[kk] = *(const bf16x8*)(vp + 16 * kk);
+        }
+    }
+    const int first = a.p.causal ? key0 - off : 0;
+    const int t0 = first > 0 ? first / kRows : 0, t1 = (nq + kRows - 1) / kRows;
+    const int per = t1 > t0 ? t1 - t0 : 0, total = per * G;
+    const unsigned qrow = (unsigned)(a.p.q_stride * 2), grow = (unsigned)(a.go_stride * 2);
+    TileLoad<D, kRows, 1> ql, gl;
+    ql.init(lane, 0, qrow);
+    gl.init(lane, 0, grow);
+    Frags<D> fr;
+    fr.init(lane);
+    f32x16 dk[R::DB], dv[R::DB];
+#pragma unroll
+    for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) dk[db][v] = dv[db][v] = 0.0f;
+    const float c = a.p.c;
+    const int base = wave * 4 * kPart, stats = kWaves * 4 * kPart + wave * 4 * kStat;
+    constexpr int kLoads = 2 * decltype(ql)::J + 2;
+    // restrict for the effect told at the forward pass
+    auto pass = [&](const unsigned short* __restrict__ qp, const unsigned short* __restrict__ gp) __attribute__((always_inline)) {
+        auto load = [&](int it, int buf) {
+            const int head = kvh * G + it / per, t = t0 + it % per;
+            const long long row = q0 + (long long)t * kRows, left = nq - (long long)t * kRows;
+            ql.issue(qp + row * a.p.q_stride + (long long)head * D, left, qrow, lds, base + 2 * buf * kPart);
+            gl.issue(gp + row * a.go_stride + (long long)head * D, left, grow, lds, base + (2 * buf + 1) * kPart);
+            const long long st = ((long long)rank * a.p.Hq + head) * a.p.Tq + row;
+            const int n = left < kRows ? (int)left : kRows;
+            load_floats(a.lse2 + st, n, lds, stats + 2 * buf * kStat, lane);
+            load_floats(a.delta + st, n, lds, stats + (2 * buf + 1) * kStat, lane);
+        };
+        if (wave < total) load(wave, 0);
+        int buf = 0;
+        for (int it = wave; it < total; it += kWaves, buf ^= 1) {
+            const bool more = it + kWaves < total;
+            if (more) load(it + kWaves, buf ^ 1);
+            wait_vm(more ? kLoads : 0);                   // this item has landed
+            const int qa = base + 2 * buf * kPart, ga = qa + kPart, q = (t0 + it % per) * kRows;
+            const float* stat = (const float*)((const char*)lds + stats + 2 * buf * kStat);
+            f32x16 s, dp;
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int v = 0; v < 16; ++v) s[v] = dp[v] = 0.0f;
+#pragma unroll
+            for (int kk = 0; kk < R::KK; ++kk) {
+                s = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, qa, 0, kk), kf[kk], s, 0, 0, 0);
+                dp = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.rows(lds, ga, 0, kk), vf[kk], dp, 0, 0, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x100, kAhead, 0);
+#pragma unroll
+            for (int i = 0; i < 2 * R::KK - kAhead; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, kAhead, 0);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int v = 0; v < 16; ++v) {
+                const int r = acc_row(v, half);
+                s[v] = exp2_hw(__builtin_fmaf(s[v], c, -stat[r]));
+                dp[v] = s[v] * (dp[v] - stat[kStat / 4 + r]);
+            }
+            if (a.p.causal && q + off < key0 + 31) {
+#pragma unroll
+                for (int v = 0; v < 16; ++v)
+                    if (q + acc_row(v, half) + off < key) s[v] = dp[v] = 0.0f;
+            }
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                const bf16x8 pf = round8(s, ks), sf = round8(dp, ks);
+#pragma unroll
+                for (int db = 0; db < R::DB; ++db) {
+                    dv[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, ga, db, ks), pf, dv[db], 0, 0, 0);
+                    dk[db] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fr.cols(lds, qa, db, ks), sf, dk[db], 0, 0, 0);
+                }
+            }
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // this stage's reads are done before it loads again
+        }
+    };
+    pass(a.p.q[rank], a.go[rank]);
+
+    // the waves' sums: blocks of 32 x 32 floats, dK's then dV's, in each wave's tiles
+    static_assert(2 * R::DB * 4096 <= 4 * kPart, "a wave's sums fit its tiles");
+    float* mine = (float*)((char*)lds + base);
+#pragma unroll
+    for (int b = 0; b < 2 * R::DB; ++b)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) mine[b * 1024 + acc_row(v, half) * 32 + col] = b < R::DB ? dk[b][v] : dv[b - R::DB][v];
+    __syncthreads();
+    const long long row = k0 + (long long)keyc;
+#pragma unroll
+    for (int i = 0; i < 2 * R::DB / kWaves; ++i) {
+        const int b = i * kWaves + wave, db = b % R::DB;
+        f32x16 x;
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+            x[v] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+                x[v] += ((const float*)((const char*)lds + w * 4 * kPart))[b * 1024 + acc_row(v, half) * 32 + col];
+        }
+        unsigned short* p = b < R::DB ? a.dk[rank] + row * a.dk_stride : a.dv[rank] + row * a.dv_stride;
+        store_block(p + (long long)kvh * D + 32 * db, x, b < R::DB ? a.scale : 1.0f, half, key < nk);
+    }
 }
 
 }  // namespace
@@ -343,8 +505,20 @@ extern "C" int tp_attention_grad(const void* const* dout, const void* const* q, 
     if (Tk) {
         a.slots = prompt_slots(B, Tk, 1, kRowsWG, units);
         if (!a.slots) return RING_EUNSUPPORTED;
+        // Few keys: at most one workgroup of 128 keys for every second compute
+        // unit, or, in long prompts, whose first keys' workgroups run longest,
+        // for every one.  4 ranks of 8 heads of 128 on 2, dQ included, 128 and
+        // 32 keys a workgroup: one prompt of 1024 / 2048 / 4096 / 8192 tokens
+        // 160 / 315 / 691 / 1821 us and 82 / 172 / 572 / 2134; 5 prompts of 80,
+        // 31 and 21; 8 of 512, 121 and 138.
+        const long long groups = (long long)a.slots * units, cus = dev_info().cus;
+        const bool few = 2 * groups <= cus || (groups <= cus + units && Tk / B >= 1024);
+        if (few) a.slots = prompt_slots(B, Tk, 1, 32, units);
+        if (!a.slots) return RING_EUNSUPPORTED;
         const dim3 grid((unsigned)a.slots * (unsigned)units);
-        if (D == 128) hipLaunchKernelGGL(attn_dkv_kernel<128>, grid, dim3(256), 0, s, a);
+        if (few && D == 128) hipLaunchKernelGGL(attn_dkv_few_kernel<128>, grid, dim3(256), 0, s, a);
+        else if (few) hipLaunchKernelGGL(attn_dkv_few_kernel<64>, grid, dim3(256), 0, s, a);
+        else if (D == 128) hipLaunchKernelGGL(attn_dkv_kernel<128>, grid, dim3(256), 0, s, a);
         else hipLaunchKernelGGL(attn_dkv_kernel<64>, grid, dim3(256), 0, s, a);
         if (hipGetLastError() != hipSuccess) return RING_EHIP;
     }

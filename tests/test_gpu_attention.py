@@ -220,7 +220,8 @@ def check_attention(q, k, v, o, lse, lq, lk, causal, scale, ranks=None):
 
 
 # (query lengths, key lengths or None for the same)
-LENS = [([1], None), ([31], None), ([32], None), ([33], None), ([64], None), ([65], None), ([127], None), ([129], None),
+MANY = [150, 61, 200] * 14                               # enough workgroups for every compute unit
+LENS = [([1], None), (MANY, None), ([31], None), ([32], None), ([33], None), ([64], None), ([65], None), ([127], None), ([129], None),
         ([300], None), ([0], None), ([5, 0, 1, 64, 0, 130, 2], None), ([1] * 70, None), ([3, 2] * 65, None),
         ([1, 1, 7], [300, 1, 129]),                      # fewer queries than keys: a prompt's last part
         ([70, 9, 4], [5, 0, 4])]                         # more queries than keys: causal rows that see none
