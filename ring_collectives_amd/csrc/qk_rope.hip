@@ -12,8 +12,8 @@
 // the rotation's partner values come from the lane rot / 16 further on.  Going
 // forward a wave has one such group of rows, so a step of few tokens runs wide
 // (a wave per token, its rows one group after the other, took 6.8 us for 32
-// tokens of 12 heads on 4 ranks); going back it has a token's rows, one group
-// after the other, since it sums the gains' gradients in registers.
+// tokens of 12 heads on 4 ranks; this 4.5); going back it keeps one group of
+// rows for many tokens, since it sums the gains' gradients in registers.
 #include "ring_device.h"
 #include "tp_attention.h"
 
@@ -140,15 +140,15 @@ __global__ __launch_bounds__(256) void qk_rope_kernel(RopeArgs a, int groups) {
     }
 }
 
-constexpr int kGradBlocks = 256;       // workgroups per rank that leave a partial sum of the gains' gradients
+constexpr int kGradBlocks = 1024;      // workgroups per rank that leave a partial sum of the gains' gradients, at most
 
 struct RopeGradArgs {
-    RopeArgs f;                        // q, k, v: the gradients read; kc: unused
+    RopeArgs f;                        // q, k, v: the gradients read; kc, vc: unused
     void* dx[RING_MAX_RANKS];
     float* part;                       // [P][blocks][2][D]
     Status* status;
     WsSpan data;
-    int blocks;
+    int blocks, groups;
 };
 
 template <int D, class X>
@@ -156,66 +156,64 @@ __global__ __launch_bounds__(256) void qk_rope_grad_kernel(RopeGradArgs g) {
     constexpr int W = D / 8, HW = 64 / W;
     __shared__ float sum[4][HW][2][D];
     const RopeArgs& a = g.f;
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int sub = lane / W, i = lane % W;
     const int H = a.Hq + 2 * a.Hkv, rank = blockIdx.y;
     if (blockIdx.x == 0 && rank == 0 && threadIdx.x == 0) ws_add_data(g.status, g.data);
     const bool norm = a.gq[rank] != nullptr;
-    f32x8 gq, gk, sq, sk;
+    // a wave keeps to one group of head rows, of every step-th token, so a lane
+    // sums one gain's gradient
+    const int w = blockIdx.x * 4 + wave, step = g.blocks * 4 / g.groups;
+    const int h = w % g.groups * HW + sub, t0 = w / g.groups < step ? w / g.groups : a.T;
+    const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv, there = h < H;
+    const int hh = there ? h : H - 1;
+    const unsigned short* dz0 = is_q ? a.q[rank] + (long long)h * D
+                              : is_k ? a.k[rank] + (long long)(h - a.Hq) * D
+                                     : a.v[rank] + (long long)(hh - a.Hq - a.Hkv) * D;
+    const int heads = is_q ? a.Hq : a.Hkv;
+    f32x8 gain, s8;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sq[e] = sk[e] = 0.0f;
-    if (norm) {
-        gq = load8(a.gq[rank] + 8 * i);
-        gk = load8(a.gk[rank] + 8 * i);
+    for (int e = 0; e < 8; ++e) {
+        s8[e] = 0.0f;
+        gain[e] = 1.0f;
     }
-    for (long long t = (long long)blockIdx.x * 4 + wave; t < a.T; t += (long long)gridDim.x * 4) {
-        Turn r = make_turn<D>(a.cs, a.pos, a.table_rows, a.rot, (int)t, lane);
+    if (norm && (is_q || is_k)) gain = load8((is_q ? a.gq : a.gk)[rank] + 8 * i);
+    for (int t = t0; t < a.T; t += step) {
+        const f32x8 dz = load8(dz0 + (long long)t * heads * D + 8 * i);
+        f32x8 y;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = 0.0f;
+        if (norm && (is_q || is_k)) y = load8((const X*)a.qkv[rank] + t * a.stride + h * D + 8 * i);
+        Turn r = make_turn<D>(a.cs, a.pos, a.table_rows, a.rot, t, lane);
 #pragma unroll
         for (int e = 0; e < 8; ++e) r.b[e] = -r.b[e];          // the other way
-        const long long p = a.pos[t];
-        const bool known = p >= 0 && p < a.table_rows;
-        const X* x = (const X*)a.qkv[rank] + t * a.stride;
-        X* dx = (X*)g.dx[rank] + t * (long long)H * D;
-        for (int h0 = 0; h0 < H; h0 += HW) {
-            const int h = h0 + sub;
-            const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv;
-            f32x8 y, dz;
+        f32x8 d = turn(r, dz);
+        if (norm) {
+            const long long p = a.pos[t];
+            const bool known = p >= 0 && p < a.table_rows;
+            float s = 0.0f, c = 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = dz[e] = 0.0f;
-            if (h < H) {
-                const unsigned short* dp = is_q ? a.q[rank] + (t * a.Hq + h) * D
-                                         : is_k ? a.k[rank] + (t * a.Hkv + h - a.Hq) * D
-                                                : a.v[rank] + (t * a.Hkv + h - a.Hq - a.Hkv) * D;
-                dz = load8(dp + 8 * i);
-                if (norm && (is_q || is_k)) y = load8(x + h * D + 8 * i);
+            for (int e = 0; e < 8; ++e) s += y[e] * y[e];
+            const float inv = 1.0f / sqrtf(row_sum<W>(s) * (1.0f / D) + a.eps);
+            f32x8 n;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                n[e] = y[e] * inv;
+                s8[e] += known ? d[e] * n[e] : 0.0f;
+                d[e] *= gain[e];
+                c += d[e] * n[e];
             }
-            f32x8 d = turn(r, dz);
-            if (norm) {
-                float s = 0.0f, c = 0.0f;
+            c = row_sum<W>(c) * (1.0f / D);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s += y[e] * y[e];
-                const float inv = 1.0f / sqrtf(row_sum<W>(s) * (1.0f / D) + a.eps);
-                f32x8 n;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    n[e] = y[e] * inv;
-                    if (known && is_q) sq[e] += d[e] * n[e];
-                    if (known && is_k) sk[e] += d[e] * n[e];
-                    d[e] *= is_q ? gq[e] : gk[e];
-                    c += d[e] * n[e];
-                }
-                c = row_sum<W>(c) * (1.0f / D);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) d[e] = (d[e] - n[e] * c) * inv;
-            }
-            if (h < H) store8(dx + h * D + 8 * i, is_q || is_k ? d : dz);
+            for (int e = 0; e < 8; ++e) d[e] = (d[e] - n[e] * c) * inv;
         }
+        if (there) store8((X*)g.dx[rank] + ((long long)t * H + h) * D + 8 * i, is_q || is_k ? d : dz);
     }
     if (!norm) return;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-        sum[wave][sub][0][8 * i + e] = sq[e];
-        sum[wave][sub][1][8 * i + e] = sk[e];
+        sum[wave][sub][0][8 * i + e] = is_q ? s8[e] : 0.0f;
+        sum[wave][sub][1][8 * i + e] = is_k ? s8[e] : 0.0f;
     }
     __syncthreads();
     for (int j = threadIdx.x; j < 2 * D; j += 256) {
@@ -366,14 +364,19 @@ extern "C" int tp_qk_norm_rope_grad(const void* const* dq, const void* const* dk
     if (gain_q && (!all16((const void* const*)dgain_q, P) || !all16((const void* const*)dgain_k, P))) return RING_EINVAL;
     if (!ws || ((uintptr_t)ws & 255) || ws_bytes < tp_qk_norm_rope_grad_workspace_bytes(P, D)) return RING_EWORKSPACE;
     hipStream_t s = (hipStream_t)stream;
-    int blocks = (T + 3) / 4;
-    const int most = (4 * dev_info().cus + P - 1) / P;
-    if (blocks > most) blocks = most;
+    // Four workgroups a compute unit in all, every group of head rows at least
+    // one wave: at most 2^21 / 512 = 4096 groups, so kGradBlocks always do.
+    g.groups = (Hq + 2 * Hkv + 512 / D - 1) / (512 / D);
+    const long long items = (long long)T * g.groups;
+    long long blocks = (4 * dev_info().cus + P - 1) / P;
+    if (blocks > (items + 3) / 4) blocks = (items + 3) / 4;
+    if (blocks < (g.groups + 3) / 4) blocks = (g.groups + 3) / 4;
     if (blocks > kGradBlocks) blocks = kGradBlocks;
+    if (!T) blocks = 0;
     g.part = (float*)((char*)ws + kStatusBytes);
     g.status = (Status*)ws;
     g.data = WsSpan{kStatusBytes, kStatusBytes + (unsigned long long)P * blocks * 2 * D * sizeof(float)};
-    g.blocks = blocks;
+    g.blocks = (int)blocks;
     if (T) {
         for (int r = 0; r < P; ++r) {
             g.f.q[r] = (unsigned short*)const_cast<void*>(dq[r]);
@@ -400,7 +403,7 @@ extern "C" int tp_qk_norm_rope_grad(const void* const* dq, const void* const* dk
     if (gain_q) {
         GainArgs w;
         w.part = g.part;
-        w.blocks = blocks;
+        w.blocks = (int)blocks;
         for (int r = 0; r < P; ++r) {
             w.dgq[r] = dgain_q[r];
             w.dgk[r] = dgain_k[r];
