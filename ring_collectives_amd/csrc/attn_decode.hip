@@ -313,8 +313,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a) {
             }
         };
         pass(kbase, vbase);
-        // join the four waves in LDS: every wave's share in turn goes through
-        // [d][column] floats at the wave's own tiles
+        // the four waves' results, as [d][column] floats in each wave's own tiles
         st.l = sum_halves(st.l);
         if (half == 0) {
             wave_ml[wave][col][0] = st.mc;
@@ -327,7 +326,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a) {
 #pragma unroll
             for (int v = 0; v < 16; ++v) mine[(32 * db + acc_row(v, half)) * 32 + col] = st.o[db][v];
         __syncthreads();
-        if (wave) return;
+        if (wave >= R::DB) return;
         float mx = -INFINITY, l = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) mx = fmaxf(mx, wave_ml[w][col][0]);
@@ -339,41 +338,38 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a) {
         }
         st.mc = mx;
         st.l = l;
+        // wave db joins block db of the values, in st.o[0]
 #pragma unroll
-        for (int db = 0; db < R::DB; ++db)
+        for (int v = 0; v < 16; ++v) {
+            float x = 0.0f;
 #pragma unroll
-            for (int v = 0; v < 16; ++v) {
-                float x = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w)
-                    x += f[w] * ((const float*)((const char*)lds + w * 2 * kOwnBytes))[(32 * db + acc_row(v, half)) * 32 + col];
-                st.o[db][v] = x;
-            }
+            for (int w = 0; w < kWaves; ++w)
+                x += f[w] * ((const float*)((const char*)lds + w * 2 * kOwnBytes))[(32 * wave + acc_row(v, half)) * 32 + col];
+            st.o[0][v] = x;
+        }
     }
 
-    if (!live) return;
+    // a prefix wave holds all blocks of its rows, an own-key wave block `wave`
+    const int db0 = pre ? 0 : wave;
     if (!a.part_o) {                                      // one part in all: the result itself
         const int b = (int)((unsigned)m / (unsigned)G), head = kvh * G + (int)((unsigned)m % (unsigned)G);
+        unsigned short* op = a.o[rank] + b * a.o_stride + (long long)head * D + 32 * db0;
         const float inv = st.l == 0.0f ? 0.0f : 1.0f / st.l;
-        unsigned short* op = a.o[rank] + b * a.o_stride + (long long)head * D + 4 * half;
 #pragma unroll
-        for (int db = 0; db < R::DB; ++db)
-#pragma unroll
-            for (int v = 0; v < 16; v += 4) {
-                typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
-                const f32x4 y = {st.o[db][v] * inv, st.o[db][v + 1] * inv, st.o[db][v + 2] * inv, st.o[db][v + 3] * inv};
-                *(bf16x4*)(op + 32 * db + 2 * v) = __builtin_convertvector(y, bf16x4);
-            }
+        for (int i = 0; i < R::DB; ++i)
+            if (pre || i == 0) store_block(op + 32 * i, st.o[i], inv, half, live);
         return;
     }
+    if (!live) return;
     const long long at = ((long long)unit * parts + part) * all + m;
-    float* po = a.part_o + at * D + 4 * half;
+    float* po = a.part_o + at * D + 32 * db0 + 4 * half;
 #pragma unroll
-    for (int db = 0; db < R::DB; ++db)
+    for (int i = 0; i < R::DB; ++i)
+        if (pre || i == 0)
 #pragma unroll
-        for (int v = 0; v < 16; v += 4)
-            *(f32x4*)(po + 32 * db + 2 * v) = f32x4{st.o[db][v], st.o[db][v + 1], st.o[db][v + 2], st.o[db][v + 3]};
-    if (half == 0) {
+            for (int v = 0; v < 16; v += 4)
+                *(f32x4*)(po + 32 * i + 2 * v) = f32x4{st.o[i][v], st.o[i][v + 1], st.o[i][v + 2], st.o[i][v + 3]};
+    if (half == 0 && db0 == 0) {
         a.part_ml[2 * at] = st.mc;
         a.part_ml[2 * at + 1] = st.l;
     }
