@@ -38,8 +38,24 @@ def _at(stream):
     return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(dev), dev
 
 
-def _scale(scale, D: int) -> float:
-    return float(scale) if scale is not None else D ** -0.5 if D else 0.0
+def _shape(t, dims: int, what: str):
+    """The shape that a default is computed from; _binding checks the rest."""
+    if not isinstance(t, torch.Tensor) or t.dim() != dims:
+        raise ValueError("%s must be a tensor of %d dimensions" % (what, dims))
+    return t.shape
+
+
+def _lead(ts, dims: int, what: str):
+    if not len(ts):
+        raise ValueError("1..%d rank buffers, got 0" % N.MAX_RANKS)
+    return _shape(ts[0], dims, what)
+
+
+def _scale(scale, q) -> float:
+    if scale is not None:
+        return float(scale)
+    D = _lead(q, 3, "q")[2]
+    return D ** -0.5 if D else 0.0
 
 
 def _new_ws(nbytes: int, device, stream) -> torch.Tensor:
@@ -76,7 +92,7 @@ def tp_qk_norm_rope_grad(dq, dk, dv, qkv, gain_q, gain_k, cos_sin, pos, dqkv, dg
     """dqkv[r] <- the gradient of tp_qk_norm_rope's rows (their type), and
     dgain_q[r], dgain_k[r] <- the gains', from dq, dk, dv (bf16)."""
     if ws is None:
-        ws = _new_ws(N.lib().tp_qk_norm_rope_grad_workspace_bytes(len(dq), dq[0].shape[-1]), dq[0].device, stream)
+        ws = _new_ws(N.lib().tp_qk_norm_rope_grad_workspace_bytes(len(dq), _lead(dq, 3, "dq")[2]), dq[0].device, stream)
     N.check(_binding().tp_qk_norm_rope_grad(dq, dk, dv, qkv, gain_q, gain_k, cos_sin, pos, dqkv, dgain_q, dgain_k, eps, ws,
                                             *_at(stream)), "tp_qk_norm_rope_grad")
     return ws
@@ -89,7 +105,7 @@ def tp_attention(q, k, v, o, cu_q, cu_k, lse=None, causal: bool = True, scale=No
     its last query with its last key.  bf16, fp32 sums; rows may be slices of a
     packed row.  lse[r] (Hq, Tq fp32) <- the rows' log sum exp.  scale: 1 /
     sqrt(D) unless given."""
-    N.check(_binding().tp_attention(q, k, v, o, cu_q, cu_k, lse, int(bool(causal)), _scale(scale, q[0].shape[-1]),
+    N.check(_binding().tp_attention(q, k, v, o, cu_q, cu_k, lse, int(bool(causal)), _scale(scale, q),
                                     *_at(stream)), "tp_attention")
 
 
@@ -97,10 +113,10 @@ def tp_attention_grad(do, q, k, v, o, lse, dq, dk, dv, cu_q, cu_k, causal: bool 
     """dq[r], dk[r], dv[r] <- the gradient of tp_attention for do[r], the
     gradient of o[r], from its inputs and outputs (the same bits every time)."""
     if ws is None:
-        Tq, Hq = q[0].shape[:2]
+        Tq, Hq, _ = _lead(q, 3, "q")
         ws = _new_ws(N.lib().tp_attention_grad_workspace_bytes(len(q), Tq, Hq), q[0].device, stream)
     N.check(_binding().tp_attention_grad(q, k, v, o, cu_q, cu_k, lse, do, dq, dk, dv, int(bool(causal)),
-                                         _scale(scale, q[0].shape[-1]), ws, *_at(stream)), "tp_attention_grad")
+                                         _scale(scale, q), ws, *_at(stream)), "tp_attention_grad")
     return ws
 
 
@@ -111,9 +127,10 @@ def tp_attention_decode(q, k_cache, v_cache, o, block_table, lengths, page_size:
     rows of prefix_pages, shared by all requests and read once, and the first
     lengths[b] rows of block_table[b] (B, W int32)."""
     if ws is None:
-        B, Hq, D = q[0].shape
-        ws = _new_ws(N.lib().tp_attention_decode_workspace_bytes(len(q), B, Hq, k_cache[0].shape[1], D, block_table.shape[1],
-                                                                 page_size, prefix_len), q[0].device, stream)
+        B, Hq, D = _lead(q, 3, "q")
+        Hkv, W = _lead(k_cache, 3, "k_cache")[1], _shape(block_table, 2, "block_table")[1]
+        ws = _new_ws(N.lib().tp_attention_decode_workspace_bytes(len(q), B, Hq, Hkv, D, W, page_size, prefix_len),
+                     q[0].device, stream)
     N.check(_binding().tp_attention_decode(q, k_cache, v_cache, o, block_table, lengths, page_size, prefix_pages, prefix_len,
-                                           _scale(scale, q[0].shape[-1]), ws, *_at(stream)), "tp_attention_decode")
+                                           _scale(scale, q), ws, *_at(stream)), "tp_attention_decode")
     return ws
