@@ -5,7 +5,7 @@
 //
 // Two passes, each summing its results in registers in a fixed order: one per
 // 128 query rows over the keys (dQ; it also leaves lse and delta of its rows
-// in the workspace), one per 128 keys over the queries of every head of the
+// in the workspace; in shares of the keys as the forward pass), one per 128 keys over the queries of every head of the
 // group (dK, dV).  S and dP are computed in both, seven products in all where
 // five would do, but no result is added up through memory: no atomics, whose
 // order would change the results, and no fp32 copy of dQ.
@@ -36,12 +36,13 @@ struct GradArgs {
     int slots;
 };
 
-template <int D>
-__global__ __launch_bounds__(256, 2) void attn_dq_kernel(GradArgs a) {
+template <int D, int kShares>
+__global__ __launch_bounds__(256 * kShares, 2) void attn_dq_kernel(GradArgs a) {
     typedef Rows<D> R;
     constexpr int kTileBytes = kStep * R::RB;
-    __shared__ __align__(4096) unsigned short lds[4 * kTileBytes / 2];   // K 0, K 1, V 0, V 1
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    __shared__ __align__(4096) unsigned short lds[kShares * 4 * kTileBytes / 2];   // of each share: K 0, K 1, V 0, V 1
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kWaves;
+    const int share = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / kWaves;
     const int half = lane >> 5;
     if (blockIdx.x == 0 && threadIdx.x == 0) ws_add_data(a.status, a.data);
     int unit, slot;
@@ -93,7 +94,7 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(GradArgs a) {
     const long long at = ((long long)rank * a.p.Hq + head) * a.p.Tq + q0 + qi;
     float lse2 = a.lse[rank][(long long)head * a.p.Tq + q0 + qi] * kLog2e;
     if (lse2 == -INFINITY) lse2 = INFINITY;              // no key seen: every weight is 0
-    if (half == 0 && live) {
+    if (half == 0 && live && share == 0) {
         a.lse2[at] = lse2;
         a.delta[at] = delta;
     }
@@ -116,18 +117,19 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(GradArgs a) {
     // tile's loads before a tile's transposed reads
     auto pass = [&](const unsigned short* __restrict__ kp, const unsigned short* __restrict__ vp) __attribute__((always_inline)) {
         auto load = [&](int j, int buf) {
-            kl.issue(kp + (long long)j * kStep * a.p.k_stride, nk - (long long)j * kStep, krow, lds, buf * kTileBytes);
-            vl.issue(vp + (long long)j * kStep * a.p.v_stride, nk - (long long)j * kStep, vrow, lds, (2 + buf) * kTileBytes);
+            const int at = (share * 4 + buf) * kTileBytes;
+            kl.issue(kp + (long long)j * kStep * a.p.k_stride, nk - (long long)j * kStep, krow, lds, at);
+            vl.issue(vp + (long long)j * kStep * a.p.v_stride, nk - (long long)j * kStep, vrow, lds, at + 2 * kTileBytes);
         };
         const int tiles = (most + kStep - 1) / kStep;
-        if (tiles) load(0, 0);
-        for (int j = 0; j < tiles; ++j) {
-            const int buf = j & 1;
+        if (share < tiles) load(share, 0);
+        for (int i = 0; i * kShares < tiles; ++i) {
+            const int j = i * kShares + share, buf = i & 1;
             wait_vm(0);
             lds_barrier();
-            if (j + 1 < tiles) load(j + 1, buf ^ 1);
+            if (j + kShares < tiles) load(j + kShares, buf ^ 1);
             if (j * kStep >= some) continue;
-            const int ka = buf * kTileBytes, va = (2 + buf) * kTileBytes;
+            const int ka = (share * 4 + buf) * kTileBytes, va = ka + 2 * kTileBytes;
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb) {
                 f32x16 s, dp;
@@ -169,6 +171,30 @@ __global__ __launch_bounds__(256, 2) void attn_dq_kernel(GradArgs a) {
         }
     };
     pass(kbase, vbase);
+    // the shares' sums, added in their order
+    if constexpr (kShares > 1) {
+        constexpr int kRegs = 16 * R::DB;
+        static_assert(kRegs * 4 * 64 * kWaves <= (int)sizeof(lds), "one share's sums");
+        float* x = (float*)lds + wave * kRegs * 64 + lane;
+#pragma unroll
+        for (int u = 1; u < kShares; ++u) {
+            lds_barrier();                    // the tiles, or the share before, have been read
+            if (share == u) {
+#pragma unroll
+                for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) x[(db * 16 + v) * 64] = dq[db][v];
+            }
+            lds_barrier();
+            if (share == 0) {
+#pragma unroll
+                for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) dq[db][v] += x[(db * 16 + v) * 64];
+            }
+        }
+        if (share) return;
+    }
     store_column<D>(a.dq[rank] + (q0 + (long long)qi) * a.dq_stride + (long long)head * D, dq, a.scale, half, live);
 }
 
@@ -498,8 +524,16 @@ extern "C" int tp_attention_grad(const void* const* dout, const void* const* q, 
         a.slots = prompt_slots(B, Tq, Hq / Hkv, kRowsWG, units);
         if (!a.slots || (Tk && !prompt_slots(B, Tk, 1, kRowsWG, units))) return RING_EUNSUPPORTED;
         const dim3 grid((unsigned)a.slots * (unsigned)units);
-        if (D == 128) hipLaunchKernelGGL(attn_dq_kernel<128>, grid, dim3(256), 0, s, a);
-        else hipLaunchKernelGGL(attn_dq_kernel<64>, grid, dim3(256), 0, s, a);
+        // Two shares where long prompts make few workgroups (keys a prompt on
+        // average).  Both passes, one share / two: one prompt of 1000 / 2000 /
+        // 6000 on a rank of 8 heads of 128 on 2 79 / 142 / 410 us and 76 / 134 /
+        // 378, on 2 ranks of 4 heads of 64 on 2 39 / 69 / 204 and 36 / 61 / 176;
+        // three of 1000 on 4 ranks 187 and 197; nine of 333 33 and 36.
+        const bool shares = Tk / B >= 768 && 2LL * a.slots * units <= 3LL * dev_info().cus;
+        if (shares && D == 128) hipLaunchKernelGGL((attn_dq_kernel<128, 2>), grid, dim3(512), 0, s, a);
+        else if (shares) hipLaunchKernelGGL((attn_dq_kernel<64, 2>), grid, dim3(512), 0, s, a);
+        else if (D == 128) hipLaunchKernelGGL((attn_dq_kernel<128, 1>), grid, dim3(256), 0, s, a);
+        else hipLaunchKernelGGL((attn_dq_kernel<64, 1>), grid, dim3(256), 0, s, a);
         if (hipGetLastError() != hipSuccess) return RING_EHIP;
     }
     if (Tk) {
@@ -507,7 +541,7 @@ extern "C" int tp_attention_grad(const void* const* dout, const void* const* q, 
         if (!a.slots) return RING_EUNSUPPORTED;
         // Few keys: at most one workgroup of 128 keys for every second compute
         // unit, or, in long prompts, whose first keys' workgroups run longest,
-        // for every one.  4 ranks of 8 heads of 128 on 2, dQ included, 128 and
+        // for every one.  4 ranks of 8 heads of 128 on 2, dQ (in one share) included, 128 and
         // 32 keys a workgroup: one prompt of 1024 / 2048 / 4096 / 8192 tokens
         // 160 / 315 / 691 / 1821 us and 82 / 172 / 572 / 2134; 5 prompts of 80,
         // 31 and 21; 8 of 512, 121 and 138.

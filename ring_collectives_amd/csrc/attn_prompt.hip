@@ -29,6 +29,13 @@ constexpr int kWaves = 4;
 // on 2 in prompts of 64 / 256 / 683 / 2048 keys take 33 / 47 / 73 / 166 us with
 // 32 and 42 / 50 / 77 / 164 us with 64; one prompt of 1000, 31 and 24 us.
 constexpr int kShort = 1024;
+// Long prompts that make few workgroups are bound by the tiles that one goes
+// through after another: their workgroups have two or four shares of four
+// waves, each with its own buffers and every second or fourth tile, whose sums
+// are joined in LDS.  D = 64, one share / two / four: one prompt of 1000 on 4
+// ranks of 4 heads 18 / 15 / 15 us, 2000 32 / 25 / 23, 6000 on 2 ranks 85 / 66 /
+// 57; nine of 333 12.4 / 12.9 / 19.  D = 128, one / two: one prompt of 1000 on a
+// rank of 8 heads on 2 22 / 20, 3000 54 / 45, 6000 113 / 94; ten of 600 23 / 26.
 constexpr int kAhead = 4;        // row fragments asked for ahead of their MFMA
 
 struct FwdArgs {
@@ -39,12 +46,13 @@ struct FwdArgs {
     int slots;
 };
 
-template <int D, int kTileKeys>
-__global__ __launch_bounds__(256, kTileKeys == 32 ? 3 : 2) void attn_fwd_kernel(FwdArgs a) {
+template <int D, int kTileKeys, int kShares>
+__global__ __launch_bounds__(256 * kShares, kTileKeys == 32 ? 3 : 2) void attn_fwd_kernel(FwdArgs a) {
     typedef Rows<D> R;
     constexpr int kTileBytes = kTileKeys * R::RB;
-    __shared__ __align__(4096) unsigned short lds[4 * kTileBytes / 2];   // K 0, K 1, V 0, V 1
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    __shared__ __align__(4096) unsigned short lds[kShares * 4 * kTileBytes / 2];   // of each share: K 0, K 1, V 0, V 1
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % kWaves;
+    const int share = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / kWaves;
     const int half = lane >> 5;
     int unit, slot;
     unit_slot(a.p.P * a.p.Hkv, a.slots, blockIdx.x, unit, slot);
@@ -104,18 +112,19 @@ __global__ __launch_bounds__(256, kTileKeys == 32 ? 3 : 2) void attn_fwd_kernel(
     // puts before each tile's first transposed read.
     auto pass = [&](const unsigned short* __restrict__ kp, const unsigned short* __restrict__ vp) __attribute__((always_inline)) {
         auto load = [&](int j, int buf) {
-            kl.issue(kp + (long long)j * kTileKeys * a.p.k_stride, nk - (long long)j * kTileKeys, krow, lds, buf * kTileBytes);
-            vl.issue(vp + (long long)j * kTileKeys * a.p.v_stride, nk - (long long)j * kTileKeys, vrow, lds, (2 + buf) * kTileBytes);
+            const int at = (share * 4 + buf) * kTileBytes;
+            kl.issue(kp + (long long)j * kTileKeys * a.p.k_stride, nk - (long long)j * kTileKeys, krow, lds, at);
+            vl.issue(vp + (long long)j * kTileKeys * a.p.v_stride, nk - (long long)j * kTileKeys, vrow, lds, at + 2 * kTileBytes);
         };
         const int tiles = (most + kTileKeys - 1) / kTileKeys;
-        if (tiles) load(0, 0);
-        for (int j = 0; j < tiles; ++j) {
-            const int buf = j & 1;
+        if (share < tiles) load(share, 0);
+        for (int i = 0; i * kShares < tiles; ++i) {
+            const int j = i * kShares + share, buf = i & 1;
             wait_vm(0);                       // tile j has landed
-            lds_barrier();                    // everyone's has; the buffers of tile j - 1 are free
-            if (j + 1 < tiles) load(j + 1, buf ^ 1);
+            lds_barrier();                    // everyone's has; the buffers of the turn before are free
+            if (j + kShares < tiles) load(j + kShares, buf ^ 1);
             if (j * kTileKeys >= some) continue;    // nothing here for this wave's rows
-            const int ka = buf * kTileBytes, va = (2 + buf) * kTileBytes;
+            const int ka = (share * 4 + buf) * kTileBytes, va = ka + 2 * kTileBytes;
             f32x16 s[kTileKeys / 32];
             // row reads kAhead MFMAs early; left alone, the compiler puts each
             // next to its use and waits out the LDS latency every time
@@ -185,6 +194,37 @@ __global__ __launch_bounds__(256, kTileKeys == 32 ? 3 : 2) void attn_fwd_kernel(
     };
     pass(kbase, vbase);
     float l = sum_halves((lp[0] + lp[1]) + (lp[2] + lp[3]));
+
+    // the shares' sums, brought to one maximum, to the first share
+    if constexpr (kShares > 1) {
+        constexpr int kRegs = 16 * R::DB + 2;
+        static_assert(kRegs * 4 * 64 * kWaves <= (int)sizeof(lds), "one share's sums");
+        float* x = (float*)lds + wave * kRegs * 64 + lane;
+#pragma unroll
+        for (int u = 1; u < kShares; ++u) {
+            lds_barrier();                    // the tiles, or the share before, have been read
+            if (share == u) {
+#pragma unroll
+                for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) x[(db * 16 + v) * 64] = o[db][v];
+                x[(kRegs - 2) * 64] = l;
+                x[(kRegs - 1) * 64] = mc;
+            }
+            lds_barrier();
+            if (share == 0) {
+                const float lu = x[(kRegs - 2) * 64], mu = x[(kRegs - 1) * 64], mn = fmaxf(mc, mu);
+                const float f = mc == mn ? 1.0f : exp2_hw(mc - mn), fu = mu == mn ? 1.0f : exp2_hw(mu - mn);
+                mc = mn;
+                l = l * f + lu * fu;
+#pragma unroll
+                for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+                    for (int v = 0; v < 16; ++v) o[db][v] = __builtin_fmaf(x[(db * 16 + v) * 64], fu, o[db][v] * f);
+            }
+        }
+        if (share) return;
+    }
 
     // The product of a weight that the mask made 0 with a value that is not
     // finite is NaN, in rows that do not see the value.  So where a result of a
@@ -322,11 +362,20 @@ extern "C" int tp_attention(const void* const* q, const void* const* k, const vo
     if (!a.slots) return RING_EUNSUPPORTED;
     const dim3 grid((unsigned)a.slots * (unsigned)units);
     hipStream_t st = (hipStream_t)stream;
-    if (D == 64)
-        hipLaunchKernelGGL((attn_fwd_kernel<64, 64>), grid, dim3(256), 0, st, a);
-    else if (Tk / B < kShort && (long long)a.slots * units > 4LL * dev_info().cus)
-        hipLaunchKernelGGL((attn_fwd_kernel<128, 32>), grid, dim3(256), 0, st, a);
-    else
-        hipLaunchKernelGGL((attn_fwd_kernel<128, 64>), grid, dim3(256), 0, st, a);
+    const long long groups = (long long)a.slots * units, cus = dev_info().cus, keys = Tk / B;
+    if (D == 64) {
+        if (keys >= 2048 && 2 * groups <= 3 * cus)
+            hipLaunchKernelGGL((attn_fwd_kernel<64, 64, 4>), grid, dim3(1024), 0, st, a);
+        else if (keys >= 256 && groups * 256 <= cus * (keys < 1024 ? keys : 1024))
+            hipLaunchKernelGGL((attn_fwd_kernel<64, 64, 2>), grid, dim3(512), 0, st, a);
+        else
+            hipLaunchKernelGGL((attn_fwd_kernel<64, 64, 1>), grid, dim3(256), 0, st, a);
+    } else if (keys >= 512 && 2 * groups <= 3 * cus) {
+        hipLaunchKernelGGL((attn_fwd_kernel<128, 64, 2>), grid, dim3(512), 0, st, a);
+    } else if (keys < kShort && groups > 4 * cus) {
+        hipLaunchKernelGGL((attn_fwd_kernel<128, 32, 1>), grid, dim3(256), 0, st, a);
+    } else {
+        hipLaunchKernelGGL((attn_fwd_kernel<128, 64, 1>), grid, dim3(256), 0, st, a);
+    }
     return hipGetLastError() == hipSuccess ? RING_OK : RING_EHIP;
 }
