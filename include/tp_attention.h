@@ -127,7 +127,8 @@ size_t tp_qk_norm_rope_grad_workspace_bytes(int P, int D);
  * fp32, the softmax weights rounded to bf16 for the second product.
  * Offsets are clamped to [0, Tq] and [0, Tk], and one below its prompt's start
  * makes the prompt empty; rows that no prompt covers are not written.
- * scale > 0.
+ * scale > 0.  A key or value that is not finite reaches only the queries that
+ * see it.
  */
 int tp_attention(const void *const *q, const void *const *k, const void *const *v, void *const *o, float *const *lse,
                  const int *cu_q, const int *cu_k, int P, int B, int Tq, int Tk, int Hq, int Hkv, int D,
@@ -139,8 +140,11 @@ int tp_attention(const void *const *q, const void *const *k, const void *const *
  * and outputs: dq[r] (Tq rows), dk[r], dv[r] (Tk rows), bf16, with fp32 sums
  * in a fixed order (the same bits every time).  P and dS = P (dP - sum(dout
  * o)) are computed again from q, k, v and lse in fp32 and rounded to bf16 for
- * the products that they enter.  A query that sees no key gives dq = 0 and
- * adds nothing; a key that no query sees gives dk = dv = 0.
+ * the products that they enter; sum(dout o) is taken in fp32 from o as it was
+ * rounded.  A query that sees no key gives dq = 0 and adds nothing; a key that
+ * no query sees gives dk = dv = 0.  Inputs that are not finite may make NaN of
+ * any gradient of their prompt (of their rank and group of heads), and of no
+ * other.
  */
 int tp_attention_grad(const void *const *dout, const void *const *q, const void *const *k, const void *const *v,
                       const void *const *o, const float *const *lse, void *const *dq, void *const *dk, void *const *dv,
@@ -160,7 +164,8 @@ size_t tp_attention_grad_workspace_bytes(int P, int Tq, int Hq);
  * row among them, if it is to be seen).  o[r] = softmax(scale q k^T) v over
  * both; the prefix is read once for all requests.
  * Lengths are clamped to [0, table_stride * page_size]; keys whose page lies
- * outside [0, pages) take no part; a request without keys gives o = 0.
+ * outside [0, pages) take no part; a request without keys gives o = 0.  Rows
+ * of the cache that are no key of a request never reach its result.
  * pages * page_size and table_stride * page_size stay below 2^31.
  * scale > 0.  The workspace's size depends on the device's compute units.
  */

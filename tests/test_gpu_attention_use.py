@@ -359,3 +359,33 @@ def test_layer_training_step():
     # bf16 q, k, v, o, P, dS and gradients of them: some 2^-8 each, random signs
     for got, w in zip(d + [gq, gk], want):
         assert (got.cpu().double() - w).norm() < 0.02 * w.norm()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [[50, 45, 70], [300, 45, 1000]])
+def test_gradient_of_other_prompts_keeps_clear_of_a_prompt_of_nan(D, lens):
+    """Inputs that are not finite stay within their prompt, and within their
+    group of heads, going back."""
+    n = sum(lens)
+    q, k, v = attn_inputs(1, lens, lens, 4, 2, D, seed=D + n)
+    do = [torch.randn(n, 4, D, device="cuda").to(BF)]
+    c, mid = cu(lens), slice(lens[0], lens[0] + lens[1])
+
+    def grads():
+        o, lse = [poisoned((n, 4, D))], [poisoned((4, n), torch.float32)]
+        A.tp_attention(q, k, v, o, c, c, lse=lse)
+        d = [[poisoned(tuple(t[0].shape))] for t in (q, k, v)]
+        A.tp_attention_grad(do, q, k, v, o, lse, *d, c, c)
+        torch.cuda.synchronize()
+        return [t[0] for t in d]
+
+    want = grads()
+    v[0][mid, 1] = float("inf")                              # key head 1: query heads 2, 3
+    k[0][mid.start + 3, 1, 0] = float("nan")
+    q[0][mid.stop - 1, 3, 1] = float("nan")
+    for got, w in zip(grads(), want):
+        h = got.shape[1] // 2
+        rest = torch.ones(n, dtype=torch.bool, device="cuda")
+        rest[mid] = False
+        assert torch.equal(got[rest], w[rest]) and torch.equal(got[:, :h], w[:, :h])
+        assert torch.isfinite(w).all()
