@@ -67,7 +67,7 @@ struct Turn {
     bool turns;
 };
 template <int D>
-__device__ __forceinline__ Turn make_turn(const float* cs, const int* pos, long long table_rows, int rot, int t, int lane) {
+__device__ __forceinline__ Turn make_turn(const float* cs, long long p, long long table_rows, int rot, int lane) {
     Turn r;
     const int i = lane % (D / 8), w = rot / 16;          // lanes [0, w) hold the pairs' first values, [w, 2 w) the second
     r.turns = i < 2 * w;
@@ -77,7 +77,6 @@ __device__ __forceinline__ Turn make_turn(const float* cs, const int* pos, long 
         r.a[e] = 1.0f;
         r.b[e] = 0.0f;
     }
-    const long long p = pos[t];
     if (p < 0 || p >= table_rows) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) r.a[e] = __builtin_nanf("");
@@ -102,41 +101,64 @@ template <int D, class X>
 __global__ __launch_bounds__(256) void qk_rope_kernel(RopeArgs a, int groups) {
     constexpr int W = D / 8, HW = 64 / W;          // lanes of a head row, head rows of a wave
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int i = lane % W, H = a.Hq + 2 * a.Hkv;
-    // item: rank, then token, then group of HW head rows
-    const unsigned it = blockIdx.x * 4 + wave, per = (unsigned)a.T * groups;
-    const int rank = (int)(it / per);
-    if (rank >= a.P) return;
-    const int t = (int)(it % per / (unsigned)groups), h = (int)(it % (unsigned)groups) * HW + lane / W;
-    const bool is_q = h < a.Hq, is_k = !is_q && h < a.Hq + a.Hkv, is_v = !is_q && !is_k && h < H;
-    f32x8 y;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = 0.0f;
-    if (h < H) y = load8((const X*)a.qkv[rank] + t * a.stride + h * D + 8 * i);
-    const long long slot = a.slots ? a.slots[t] : -1;
-    const bool cached = slot >= 0 && slot < a.cache_rows;
-    const Turn r = make_turn<D>(a.cs, a.pos, a.table_rows, a.rot, t, lane);
+    const int i = lane % W, rank = blockIdx.y;
+    // All the arguments in one trip to the kernel's argument memory: left
+    // alone, the compiler reads each where it is first used, one after the
+    // other (8192 tokens of 12 heads on 4 ranks took 71 us so, and take 63:
+    // 5.4 TB/s).
+    auto gx = (Global<const X>)a.qkv[rank];
+    auto ggq = (Global<const float>)a.gq[rank], ggk = (Global<const float>)a.gk[rank], gcs = (Global<const float>)a.cs;
+    auto gqo = (Global<unsigned short>)a.q[rank], gko = (Global<unsigned short>)a.k[rank], gvo = (Global<unsigned short>)a.v[rank];
+    auto gkc = (Global<unsigned short>)a.kc[rank], gvc = (Global<unsigned short>)a.vc[rank];
+    auto gpos = (Global<const int>)a.pos;
+    auto gslots = (Global<const long long>)a.slots;
+    long long stride = a.stride, table_rows = a.table_rows, cache_rows = a.cache_rows;
+    int T = a.T, Hq = a.Hq, Hkv = a.Hkv, rot = a.rot;
+    float eps = a.eps;
+    asm volatile("" : "+s"(gx), "+s"(ggq), "+s"(ggk), "+s"(gcs), "+s"(gqo), "+s"(gko), "+s"(gvo), "+s"(gkc), "+s"(gvc),
+                      "+s"(gpos), "+s"(gslots), "+s"(stride), "+s"(table_rows), "+s"(cache_rows), "+s"(T), "+s"(Hq),
+                      "+s"(Hkv), "+s"(rot), "+s"(eps), "+s"(groups));
+    const X* x = (const X*)gx;
+    const float *gq = (const float*)ggq, *gk = (const float*)ggk, *cs = (const float*)gcs;
+    unsigned short *qo = (unsigned short*)gqo, *ko = (unsigned short*)gko, *vo = (unsigned short*)gvo;
+    unsigned short *kc = (unsigned short*)gkc, *vc = (unsigned short*)gvc;
+    const int* pos = (const int*)gpos;
+    const long long* slots = (const long long*)gslots;
+    // item of the rank: token, then group of HW head rows
+    const unsigned it = blockIdx.x * 4 + wave;
+    const int t = (int)(it / (unsigned)groups), h = (int)(it % (unsigned)groups) * HW + lane / W;
+    const int H = Hq + 2 * Hkv;
+    if (t >= T) return;
+    const bool is_q = h < Hq, is_k = !is_q && h < Hq + Hkv, is_v = !is_q && !is_k && h < H;
+    // the position first, which the table's row waits for; a lane past the
+    // heads reads the last one
+    const int p = pos[t];
+    const long long slot = slots ? slots[t] : -1;
+    const bool cached = slot >= 0 && slot < cache_rows;
+    const f32x8 y = load8(x + t * stride + (h < H ? h : H - 1) * D + 8 * i);
+    f32x8 g = y;
+    if (gq) g = load8((is_q ? gq : gk) + 8 * i);
+    const Turn r = make_turn<D>(cs, p, table_rows, rot, lane);
     f32x8 z = y;
-    if (a.gq[rank]) {
-        const f32x8 g = load8((is_q ? a.gq : a.gk)[rank] + 8 * i);
+    if (gq) {
         float s = 0.0f;
 #pragma unroll
         for (int e = 0; e < 8; ++e) s += y[e] * y[e];
-        const float inv = 1.0f / sqrtf(row_sum<W>(s) * (1.0f / D) + a.eps);
+        const float inv = 1.0f / sqrtf(row_sum<W>(s) * (1.0f / D) + eps);
 #pragma unroll
         for (int e = 0; e < 8; ++e) z[e] = y[e] * inv * g[e];
     }
     z = turn(r, z);
     if (is_q) {
-        store8(a.q[rank] + ((long long)t * a.Hq + h) * D + 8 * i, z);
+        store8(qo + ((long long)t * Hq + h) * D + 8 * i, z);
     } else if (is_k) {
-        const int g = h - a.Hq;
-        if (a.k[rank]) store8(a.k[rank] + ((long long)t * a.Hkv + g) * D + 8 * i, z);
-        if (cached) store8(a.kc[rank] + (slot * a.Hkv + g) * D + 8 * i, z);
+        const int g = h - Hq;
+        if (ko) store8(ko + ((long long)t * Hkv + g) * D + 8 * i, z);
+        if (cached) store8(kc + (slot * Hkv + g) * D + 8 * i, z);
     } else if (is_v) {
-        const int g = h - a.Hq - a.Hkv;
-        if (a.v[rank]) store8(a.v[rank] + ((long long)t * a.Hkv + g) * D + 8 * i, y);
-        if (cached) store8(a.vc[rank] + (slot * a.Hkv + g) * D + 8 * i, y);
+        const int g = h - Hq - Hkv;
+        if (vo) store8(vo + ((long long)t * Hkv + g) * D + 8 * i, y);
+        if (cached) store8(vc + (slot * Hkv + g) * D + 8 * i, y);
     }
 }
 
@@ -184,12 +206,12 @@ __global__ __launch_bounds__(256) void qk_rope_grad_kernel(RopeGradArgs g) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[e] = 0.0f;
         if (norm && (is_q || is_k)) y = load8((const X*)a.qkv[rank] + t * a.stride + h * D + 8 * i);
-        Turn r = make_turn<D>(a.cs, a.pos, a.table_rows, a.rot, t, lane);
+        const int p = a.pos[t];
+        Turn r = make_turn<D>(a.cs, p, a.table_rows, a.rot, lane);
 #pragma unroll
         for (int e = 0; e < 8; ++e) r.b[e] = -r.b[e];          // the other way
         f32x8 d = turn(r, dz);
         if (norm) {
-            const long long p = a.pos[t];
             const bool known = p >= 0 && p < a.table_rows;
             float s = 0.0f, c = 0.0f;
 #pragma unroll
@@ -324,9 +346,9 @@ extern "C" int tp_qk_norm_rope(const void* const* qkv, const float* const* gain_
     a.Hkv = Hkv;
     a.eps = eps;
     const int groups = (Hq + 2 * Hkv + 512 / D - 1) / (512 / D);
-    const long long items = (long long)P * T * groups;
+    const long long items = (long long)T * groups;
     if (items >= (1LL << 31)) return RING_EUNSUPPORTED;
-    const dim3 grid((unsigned)((items + 3) / 4));
+    const dim3 grid((unsigned)((items + 3) / 4), (unsigned)P);
     hipStream_t s = (hipStream_t)stream;
     if (dtype == RING_F32) {
         if (D == 128) hipLaunchKernelGGL((qk_rope_kernel<128, float>), grid, dim3(256), 0, s, a, groups);
