@@ -46,10 +46,18 @@ __global__ __launch_bounds__(256 * kShares, 2) void attn_dq_kernel(GradArgs a) {
     const int half = lane >> 5;
     if (blockIdx.x == 0 && threadIdx.x == 0) ws_add_data(a.status, a.data);
     int unit, slot;
-    unit_slot(a.p.P * a.p.Hkv, a.slots, blockIdx.x, unit, slot);
-    const int G = a.p.Hq / a.p.Hkv, rank = unit / a.p.Hkv, kvh = unit % a.p.Hkv;
+    const PromptSizes sz = read_sizes(a.p, a.slots);
+    unit_slot(sz.P * sz.Hkv, sz.slots, blockIdx.x, unit, slot);
+    const int G = sz.Hq / sz.Hkv, rank = unit / sz.Hkv, kvh = unit % sz.Hkv;
+    auto gq = (Global<const unsigned short>)a.p.q[rank], gk = (Global<const unsigned short>)a.p.k[rank];
+    auto gv = (Global<const unsigned short>)a.p.v[rank], gout = (Global<const unsigned short>)a.o[rank];
+    auto ggo = (Global<const unsigned short>)a.go[rank];
+    auto glse = (Global<const float>)a.lse[rank];
+    auto gdq = (Global<unsigned short>)a.dq[rank];
+    auto glse2 = (Global<float>)a.lse2, gdelta = (Global<float>)a.delta;
+    asm volatile("" : "+s"(gq), "+s"(gk), "+s"(gv), "+s"(gout), "+s"(ggo), "+s"(glse), "+s"(gdq), "+s"(glse2), "+s"(gdelta));
     PromptTile pt;
-    if (!find_tile(a.p.cu_q, a.p.cu_k, a.p.B, a.p.Tq, a.p.Tk, G, kRowsWG, slot, lane, pt)) return;
+    if (!find_tile(sz.cu_q, sz.cu_k, sz.B, sz.Tq, sz.Tk, G, kRowsWG, slot, lane, pt)) return;
     const int tile = pt.tiles - 1 - pt.tile;                 // the longest first
     const int q0 = pt.lo, nq = pt.n, k0 = pt.lo2, nk = pt.n2;
     // this lane's row; rows past the end repeat the last one and are not stored
@@ -63,7 +71,7 @@ __global__ __launch_bounds__(256 * kShares, 2) void attn_dq_kernel(GradArgs a) {
     // workgroup's
     const int off = nk - nq;
     int seen = nk, every = nk, some = nk, most = nk;
-    if (a.p.causal) {
+    if (sz.causal) {
         auto upto = [&](unsigned row) {
             const int s = (int)((row < rows ? row : rows - 1) / (unsigned)G) + off + 1;
             return s < 0 ? 0 : s < nk ? s : nk;
@@ -78,9 +86,9 @@ __global__ __launch_bounds__(256 * kShares, 2) void attn_dq_kernel(GradArgs a) {
     float delta = 0.0f;
     {
         const long long t = q0 + (long long)qi;
-        const unsigned short* qp = a.p.q[rank] + t * a.p.q_stride + (long long)head * D + 8 * half;
-        const unsigned short* op = a.o[rank] + t * a.o_stride + (long long)head * D + 8 * half;
-        const unsigned short* gp = a.go[rank] + t * a.go_stride + (long long)head * D + 8 * half;
+        const unsigned short* qp = (const unsigned short*)gq + t * sz.q_stride + (long long)head * D + 8 * half;
+        const unsigned short* op = (const unsigned short*)gout + t * a.o_stride + (long long)head * D + 8 * half;
+        const unsigned short* gp = (const unsigned short*)ggo + t * a.go_stride + (long long)head * D + 8 * half;
 #pragma unroll
         for (int kk = 0; kk < R::KK; ++kk) {
             qf[kk] = *(const bf16x8*)(qp + 16 * kk);
@@ -91,17 +99,17 @@ __global__ __launch_bounds__(256 * kShares, 2) void attn_dq_kernel(GradArgs a) {
         }
         delta = sum_halves(delta);
     }
-    const long long at = ((long long)rank * a.p.Hq + head) * a.p.Tq + q0 + qi;
-    float lse2 = a.lse[rank][(long long)head * a.p.Tq + q0 + qi] * kLog2e;
+    const long long at = ((long long)rank * sz.Hq + head) * sz.Tq + q0 + qi;
+    float lse2 = glse[(long long)head * sz.Tq + q0 + qi] * kLog2e;
     if (lse2 == -INFINITY) lse2 = INFINITY;              // no key seen: every weight is 0
     if (half == 0 && live && share == 0) {
-        a.lse2[at] = lse2;
-        a.delta[at] = delta;
+        glse2[at] = lse2;
+        gdelta[at] = delta;
     }
 
-    const unsigned krow = (unsigned)(a.p.k_stride * 2), vrow = (unsigned)(a.p.v_stride * 2);
-    const unsigned short* kbase = a.p.k[rank] + (long long)k0 * a.p.k_stride + (long long)kvh * D;
-    const unsigned short* vbase = a.p.v[rank] + (long long)k0 * a.p.v_stride + (long long)kvh * D;
+    const unsigned krow = (unsigned)(sz.k_stride * 2), vrow = (unsigned)(sz.v_stride * 2);
+    const unsigned short* kbase = (const unsigned short*)gk + (long long)k0 * sz.k_stride + (long long)kvh * D;
+    const unsigned short* vbase = (const unsigned short*)gv + (long long)k0 * sz.v_stride + (long long)kvh * D;
     TileLoad<D, kStep, kWaves> kl, vl;
     kl.init(lane, wave, krow);
     vl.init(lane, wave, vrow);
@@ -112,14 +120,14 @@ __global__ __launch_bounds__(256 * kShares, 2) void attn_dq_kernel(GradArgs a) {
     for (int db = 0; db < R::DB; ++db)
 #pragma unroll
         for (int v = 0; v < 16; ++v) dq[db][v] = 0.0f;
-    const float c = a.p.c;
+    const float c = sz.c;
     // restrict for the effect told at the forward pass: no wait for the next
     // tile's loads before a tile's transposed reads
     auto pass = [&](const unsigned short* __restrict__ kp, const unsigned short* __restrict__ vp) __attribute__((always_inline)) {
         auto load = [&](int j, int buf) {
             const int at = (share * 4 + buf) * kTileBytes;
-            kl.issue(kp + (long long)j * kStep * a.p.k_stride, nk - (long long)j * kStep, krow, lds, at);
-            vl.issue(vp + (long long)j * kStep * a.p.v_stride, nk - (long long)j * kStep, vrow, lds, at + 2 * kTileBytes);
+            kl.issue(kp + (long long)j * kStep * sz.k_stride, nk - (long long)j * kStep, krow, lds, at);
+            vl.issue(vp + (long long)j * kStep * sz.v_stride, nk - (long long)j * kStep, vrow, lds, at + 2 * kTileBytes);
         };
         const int tiles = (most + kStep - 1) / kStep;
         if (share < tiles) load(share, 0);
@@ -195,7 +203,7 @@ __global__ __launch_bounds__(256 * kShares, 2) void attn_dq_kernel(GradArgs a) {
         }
         if (share) return;
     }
-    store_column<D>(a.dq[rank] + (q0 + (long long)qi) * a.dq_stride + (long long)head * D, dq, a.scale, half, live);
+    store_column<D>((unsigned short*)gdq + (q0 + (long long)qi) * a.dq_stride + (long long)head * D, dq, a.scale, half, live);
 }
 
 template <int D>
@@ -207,10 +215,15 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_kernel(GradArgs
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5;
     int unit, slot;
-    unit_slot(a.p.P * a.p.Hkv, a.slots, blockIdx.x, unit, slot);
-    const int G = a.p.Hq / a.p.Hkv, rank = unit / a.p.Hkv, kvh = unit % a.p.Hkv;
+    const PromptSizes sz = read_sizes(a.p, a.slots);
+    unit_slot(sz.P * sz.Hkv, sz.slots, blockIdx.x, unit, slot);
+    const int G = sz.Hq / sz.Hkv, rank = unit / sz.Hkv, kvh = unit % sz.Hkv;
+    auto gq = (Global<const unsigned short>)a.p.q[rank], gk = (Global<const unsigned short>)a.p.k[rank];
+    auto gv = (Global<const unsigned short>)a.p.v[rank], ggo = (Global<const unsigned short>)a.go[rank];
+    auto gdk = (Global<unsigned short>)a.dk[rank], gdv = (Global<unsigned short>)a.dv[rank];
+    asm volatile("" : "+s"(gq), "+s"(gk), "+s"(gv), "+s"(ggo), "+s"(gdk), "+s"(gdv));
     PromptTile pt;
-    if (!find_tile(a.p.cu_k, a.p.cu_q, a.p.B, a.p.Tk, a.p.Tq, 1, kRowsWG, slot, lane, pt)) return;
+    if (!find_tile(sz.cu_k, sz.cu_q, sz.B, sz.Tk, sz.Tq, 1, kRowsWG, slot, lane, pt)) return;
     const int tile = pt.tile;                             // the first keys are seen by the most queries
     const int k0 = pt.lo, nk = pt.n, q0 = pt.lo2, nq = pt.n2, off = nk - nq;
     const int key0 = tile * kRowsWG + wave * 32;          // this wave's first key
@@ -218,8 +231,8 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_kernel(GradArgs
 
     bf16x8 kf[R::KK], vf[R::KK];
     {
-        const unsigned short* kp = a.p.k[rank] + (k0 + (long long)keyc) * a.p.k_stride + (long long)kvh * D + 8 * half;
-        const unsigned short* vp = a.p.v[rank] + (k0 + (long long)keyc) * a.p.v_stride + (long long)kvh * D + 8 * half;
+        const unsigned short* kp = (const unsigned short*)gk + (k0 + (long long)keyc) * sz.k_stride + (long long)kvh * D + 8 * half;
+        const unsigned short* vp = (const unsigned short*)gv + (k0 + (long long)keyc) * sz.v_stride + (long long)kvh * D + 8 * half;
 #pragma unroll
         for (int kk = 0; kk < R::KK; ++kk) {
             kf[kk] = *(const bf16x8*)(kp + 16 * kk);
@@ -227,10 +240,10 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_kernel(GradArgs
         }
     }
     // query i sees key j when i >= j - off
-    const int first = a.p.causal ? tile * kRowsWG - off : 0;          // first query that sees a key of the workgroup
+    const int first = sz.causal ? tile * kRowsWG - off : 0;          // first query that sees a key of the workgroup
     const int t0 = first > 0 ? first / kStep : 0, t1 = (nq + kStep - 1) / kStep;
     const int per = t1 > t0 ? t1 - t0 : 0, total = per * G;            // tiles of a head, of the group
-    const unsigned qrow = (unsigned)(a.p.q_stride * 2), grow = (unsigned)(a.go_stride * 2);
+    const unsigned qrow = (unsigned)(sz.q_stride * 2), grow = (unsigned)(a.go_stride * 2);
     TileLoad<D, kStep, kWaves> ql, gl;
     ql.init(lane, wave, qrow);
     gl.init(lane, wave, grow);
@@ -241,7 +254,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_kernel(GradArgs
     for (int db = 0; db < R::DB; ++db)
 #pragma unroll
         for (int v = 0; v < 16; ++v) dk[db][v] = dv[db][v] = 0.0f;
-    const float c = a.p.c;
+    const float c = sz.c;
     // restrict for the effect told at the forward pass: no wait for the next
     // tile's loads before a tile's transposed reads
     auto pass = [&](const unsigned short* __restrict__ qp, const unsigned short* __restrict__ gp) __attribute__((always_inline)) {
@@ -250,10 +263,10 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_kernel(GradArgs
             const int head = kvh * G + lg;
             const long long t = q0 + (long long)lt * kStep;
             const long long left = nq - (long long)lt * kStep;
-            ql.issue(qp + t * a.p.q_stride + (long long)head * D, left, qrow, lds, buf * kTileBytes);
+            ql.issue(qp + t * sz.q_stride + (long long)head * D, left, qrow, lds, buf * kTileBytes);
             gl.issue(gp + t * a.go_stride + (long long)head * D, left, grow, lds, (2 + buf) * kTileBytes);
             if (wave < 2) {                                                // wave 0: lse, wave 1: delta, one value per lane
-                const float* st = (wave ? a.delta : a.lse2) + ((long long)rank * a.p.Hq + head) * a.p.Tq + t;
+                const float* st = (wave ? a.delta : a.lse2) + ((long long)rank * sz.Hq + head) * sz.Tq + t;
                 load_floats(st, left < kStep ? (int)left : kStep, lds, 4 * kTileBytes + (2 * buf + wave) * kStep * 4, lane);
             }
             if (++lt == t1) {
@@ -275,7 +288,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_kernel(GradArgs
 #pragma unroll
             for (int qb = 0; qb < kStep / 32; ++qb) {
                 const int qr = q + qb * 32;
-                if (a.p.causal && qr + 31 + off < key0) continue;          // none of these queries sees a key of the wave
+                if (sz.causal && qr + 31 + off < key0) continue;          // none of these queries sees a key of the wave
                 f32x16 s, dp;
                 __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
@@ -299,7 +312,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_kernel(GradArgs
                     s[v] = exp2_hw(__builtin_fmaf(s[v], c, -stat[r]));
                     dp[v] = s[v] * (dp[v] - stat[kStep + r]);
                 }
-                if (a.p.causal && qr + off < key0 + 31) {
+                if (sz.causal && qr + off < key0 + 31) {
 #pragma unroll
                     for (int v = 0; v < 16; ++v)
                         if (qr + acc_row(v, half) + off < key) s[v] = dp[v] = 0.0f;
@@ -323,9 +336,9 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_kernel(GradArgs
             }
         }
     };
-    pass(a.p.q[rank], a.go[rank]);
-    store_column<D>(a.dk[rank] + (k0 + (long long)keyc) * a.dk_stride + (long long)kvh * D, dk, a.scale, half, key < nk);
-    store_column<D>(a.dv[rank] + (k0 + (long long)keyc) * a.dv_stride + (long long)kvh * D, dv, 1.0f, half, key < nk);
+    pass((const unsigned short*)gq, (const unsigned short*)ggo);
+    store_column<D>((unsigned short*)gdk + (k0 + (long long)keyc) * a.dk_stride + (long long)kvh * D, dk, a.scale, half, key < nk);
+    store_column<D>((unsigned short*)gdv + (k0 + (long long)keyc) * a.dv_stride + (long long)kvh * D, dv, 1.0f, half, key < nk);
 }
 
 // dK and dV where there are few keys for the device's compute units: a
@@ -344,26 +357,31 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_few_kernel(Grad
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int half = lane >> 5, col = lane & 31;
     int unit, slot;
-    unit_slot(a.p.P * a.p.Hkv, a.slots, blockIdx.x, unit, slot);
-    const int G = a.p.Hq / a.p.Hkv, rank = unit / a.p.Hkv, kvh = unit % a.p.Hkv;
+    const PromptSizes sz = read_sizes(a.p, a.slots);
+    unit_slot(sz.P * sz.Hkv, sz.slots, blockIdx.x, unit, slot);
+    const int G = sz.Hq / sz.Hkv, rank = unit / sz.Hkv, kvh = unit % sz.Hkv;
+    auto gq = (Global<const unsigned short>)a.p.q[rank], gk = (Global<const unsigned short>)a.p.k[rank];
+    auto gv = (Global<const unsigned short>)a.p.v[rank], ggo = (Global<const unsigned short>)a.go[rank];
+    auto gdk = (Global<unsigned short>)a.dk[rank], gdv = (Global<unsigned short>)a.dv[rank];
+    asm volatile("" : "+s"(gq), "+s"(gk), "+s"(gv), "+s"(ggo), "+s"(gdk), "+s"(gdv));
     PromptTile pt;
-    if (!find_tile(a.p.cu_k, a.p.cu_q, a.p.B, a.p.Tk, a.p.Tq, 1, kRows, slot, lane, pt)) return;
+    if (!find_tile(sz.cu_k, sz.cu_q, sz.B, sz.Tk, sz.Tq, 1, kRows, slot, lane, pt)) return;
     const int k0 = pt.lo, nk = pt.n, q0 = pt.lo2, nq = pt.n2, off = nk - nq;
     const int key0 = pt.tile * kRows, key = key0 + col, keyc = key < nk ? key : nk - 1;
     bf16x8 kf[R::KK], vf[R::KK];
     {
-        const unsigned short* kp = a.p.k[rank] + (k0 + (long long)keyc) * a.p.k_stride + (long long)kvh * D + 8 * half;
-        const unsigned short* vp = a.p.v[rank] + (k0 + (long long)keyc) * a.p.v_stride + (long long)kvh * D + 8 * half;
+        const unsigned short* kp = (const unsigned short*)gk + (k0 + (long long)keyc) * sz.k_stride + (long long)kvh * D + 8 * half;
+        const unsigned short* vp = (const unsigned short*)gv + (k0 + (long long)keyc) * sz.v_stride + (long long)kvh * D + 8 * half;
 #pragma unroll
         for (int kk = 0; kk < R::KK; ++kk) {
             kf[kk] = *(const bf16x8*)(kp + 16 * kk);
             vf[kk] = *(const bf16x8*)(vp + 16 * kk);
         }
     }
-    const int first = a.p.causal ? key0 - off : 0;
+    const int first = sz.causal ? key0 - off : 0;
     const int t0 = first > 0 ? first / kRows : 0, t1 = (nq + kRows - 1) / kRows;
     const int per = t1 > t0 ? t1 - t0 : 0, total = per * G;
-    const unsigned qrow = (unsigned)(a.p.q_stride * 2), grow = (unsigned)(a.go_stride * 2);
+    const unsigned qrow = (unsigned)(sz.q_stride * 2), grow = (unsigned)(a.go_stride * 2);
     TileLoad<D, kRows, 1> ql, gl;
     ql.init(lane, 0, qrow);
     gl.init(lane, 0, grow);
@@ -374,7 +392,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_few_kernel(Grad
     for (int db = 0; db < R::DB; ++db)
 #pragma unroll
         for (int v = 0; v < 16; ++v) dk[db][v] = dv[db][v] = 0.0f;
-    const float c = a.p.c;
+    const float c = sz.c;
     const int base = wave * 4 * kPart, stats = kWaves * 4 * kPart + wave * 4 * kStat;
     constexpr int kLoads = 2 * decltype(ql)::J + 2;
     // restrict for the effect told at the forward pass
@@ -382,9 +400,9 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_few_kernel(Grad
         auto load = [&](int it, int buf) {
             const int head = kvh * G + it / per, t = t0 + it % per;
             const long long row = q0 + (long long)t * kRows, left = nq - (long long)t * kRows;
-            ql.issue(qp + row * a.p.q_stride + (long long)head * D, left, qrow, lds, base + 2 * buf * kPart);
+            ql.issue(qp + row * sz.q_stride + (long long)head * D, left, qrow, lds, base + 2 * buf * kPart);
             gl.issue(gp + row * a.go_stride + (long long)head * D, left, grow, lds, base + (2 * buf + 1) * kPart);
-            const long long st = ((long long)rank * a.p.Hq + head) * a.p.Tq + row;
+            const long long st = ((long long)rank * sz.Hq + head) * sz.Tq + row;
             const int n = left < kRows ? (int)left : kRows;
             load_floats(a.lse2 + st, n, lds, stats + 2 * buf * kStat, lane);
             load_floats(a.delta + st, n, lds, stats + (2 * buf + 1) * kStat, lane);
@@ -420,7 +438,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_few_kernel(Grad
                 s[v] = exp2_hw(__builtin_fmaf(s[v], c, -stat[r]));
                 dp[v] = s[v] * (dp[v] - stat[kStat / 4 + r]);
             }
-            if (a.p.causal && q + off < key0 + 31) {
+            if (sz.causal && q + off < key0 + 31) {
 #pragma unroll
                 for (int v = 0; v < 16; ++v)
                     if (q + acc_row(v, half) + off < key) s[v] = dp[v] = 0.0f;
@@ -437,7 +455,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_few_kernel(Grad
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");   // this stage's reads are done before it loads again
         }
     };
-    pass(a.p.q[rank], a.go[rank]);
+    pass((const unsigned short*)gq, (const unsigned short*)ggo);
 
     // the waves' sums: blocks of 32 x 32 floats, dK's then dV's, in each wave's tiles
     static_assert(2 * R::DB * 4096 <= 4 * kPart, "a wave's sums fit its tiles");
@@ -459,7 +477,7 @@ __global__ __launch_bounds__(256, D == 64 ? 2 : 1) void attn_dkv_few_kernel(Grad
             for (int w = 0; w < kWaves; ++w)
                 x[v] += ((const float*)((const char*)lds + w * 4 * kPart))[b * 1024 + acc_row(v, half) * 32 + col];
         }
-        unsigned short* p = b < R::DB ? a.dk[rank] + row * a.dk_stride : a.dv[rank] + row * a.dv_stride;
+        unsigned short* p = b < R::DB ? (unsigned short*)gdk + row * a.dk_stride : (unsigned short*)gdv + row * a.dv_stride;
         store_block(p + (long long)kvh * D + 32 * db, x, b < R::DB ? a.scale : 1.0f, half, key < nk);
     }
 }

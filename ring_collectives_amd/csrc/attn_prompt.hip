@@ -55,10 +55,17 @@ __global__ __launch_bounds__(256 * kShares, kTileKeys == 32 ? 3 : 2) void attn_f
     const int share = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) / kWaves;
     const int half = lane >> 5;
     int unit, slot;
-    unit_slot(a.p.P * a.p.Hkv, a.slots, blockIdx.x, unit, slot);
-    const int G = a.p.Hq / a.p.Hkv, rank = unit / a.p.Hkv, kvh = unit % a.p.Hkv;
+    const PromptSizes sz = read_sizes(a.p, a.slots);
+    unit_slot(sz.P * sz.Hkv, sz.slots, blockIdx.x, unit, slot);
+    const int G = sz.Hq / sz.Hkv, rank = unit / sz.Hkv, kvh = unit % sz.Hkv;
+    auto gq = (Global<const unsigned short>)a.p.q[rank], gk = (Global<const unsigned short>)a.p.k[rank];
+    auto gv = (Global<const unsigned short>)a.p.v[rank];
+    auto go = (Global<unsigned short>)a.o[rank];
+    auto glse = (Global<float>)a.lse[rank];
+    long long o_stride = a.o_stride;
+    asm volatile("" : "+s"(gq), "+s"(gk), "+s"(gv), "+s"(go), "+s"(glse), "+s"(o_stride));     // the rank's, in one trip
     PromptTile pt;
-    if (!find_tile(a.p.cu_q, a.p.cu_k, a.p.B, a.p.Tq, a.p.Tk, G, kTileRows, slot, lane, pt)) return;
+    if (!find_tile(sz.cu_q, sz.cu_k, sz.B, sz.Tq, sz.Tk, G, kTileRows, slot, lane, pt)) return;
     const int tile = pt.tiles - 1 - pt.tile;                 // the longest first
     const int q0 = pt.lo, nq = pt.n, k0 = pt.lo2, nk = pt.n2;
     // this lane's row; rows past the end repeat the last one and are not stored
@@ -72,7 +79,7 @@ __global__ __launch_bounds__(256 * kShares, kTileKeys == 32 ? 3 : 2) void attn_f
     // workgroup's
     const int off = nk - nq;
     int seen = nk, every = nk, some = nk, most = nk;
-    if (a.p.causal) {
+    if (sz.causal) {
         auto upto = [&](unsigned row) {
             const int s = (int)((row < rows ? row : rows - 1) / (unsigned)G) + off + 1;
             return s < 0 ? 0 : s < nk ? s : nk;
@@ -85,13 +92,13 @@ __global__ __launch_bounds__(256 * kShares, kTileKeys == 32 ? 3 : 2) void attn_f
 
     bf16x8 qf[R::KK];
     {
-        const unsigned short* qp = a.p.q[rank] + (q0 + (long long)qi) * a.p.q_stride + (long long)head * D + 8 * half;
+        const unsigned short* qp = (const unsigned short*)gq + (q0 + (long long)qi) * sz.q_stride + (long long)head * D + 8 * half;
 #pragma unroll
         for (int kk = 0; kk < R::KK; ++kk) qf[kk] = *(const bf16x8*)(qp + 16 * kk);
     }
-    const unsigned krow = (unsigned)(a.p.k_stride * 2), vrow = (unsigned)(a.p.v_stride * 2);
-    const unsigned short* kbase = a.p.k[rank] + (long long)k0 * a.p.k_stride + (long long)kvh * D;
-    const unsigned short* vbase = a.p.v[rank] + (long long)k0 * a.p.v_stride + (long long)kvh * D;
+    const unsigned krow = (unsigned)(sz.k_stride * 2), vrow = (unsigned)(sz.v_stride * 2);
+    const unsigned short* kbase = (const unsigned short*)gk + (long long)k0 * sz.k_stride + (long long)kvh * D;
+    const unsigned short* vbase = (const unsigned short*)gv + (long long)k0 * sz.v_stride + (long long)kvh * D;
     TileLoad<D, kTileKeys, kWaves> kl, vl;
     kl.init(lane, wave, krow);
     vl.init(lane, wave, vrow);
@@ -104,7 +111,7 @@ __global__ __launch_bounds__(256 * kShares, kTileKeys == 32 ? 3 : 2) void attn_f
         for (int v = 0; v < 16; ++v) o[db][v] = 0.0f;
     float mc = -INFINITY;                 // running maximum times c (of both halves of the column)
     float lp[4] = {0.0f, 0.0f, 0.0f, 0.0f};   // this half's share of the sum, in four parts
-    const float c = a.p.c;
+    const float c = sz.c;
 
     // The pass is a function of restrict pointers for one effect: its LDS reads
     // are then known not to alias what it loads from, and the compiler leaves
@@ -113,8 +120,8 @@ __global__ __launch_bounds__(256 * kShares, kTileKeys == 32 ? 3 : 2) void attn_f
     auto pass = [&](const unsigned short* __restrict__ kp, const unsigned short* __restrict__ vp) __attribute__((always_inline)) {
         auto load = [&](int j, int buf) {
             const int at = (share * 4 + buf) * kTileBytes;
-            kl.issue(kp + (long long)j * kTileKeys * a.p.k_stride, nk - (long long)j * kTileKeys, krow, lds, at);
-            vl.issue(vp + (long long)j * kTileKeys * a.p.v_stride, nk - (long long)j * kTileKeys, vrow, lds, at + 2 * kTileBytes);
+            kl.issue(kp + (long long)j * kTileKeys * sz.k_stride, nk - (long long)j * kTileKeys, krow, lds, at);
+            vl.issue(vp + (long long)j * kTileKeys * sz.v_stride, nk - (long long)j * kTileKeys, vrow, lds, at + 2 * kTileBytes);
         };
         const int tiles = (most + kTileKeys - 1) / kTileKeys;
         if (share < tiles) load(share, 0);
@@ -230,7 +237,7 @@ __global__ __launch_bounds__(256 * kShares, kTileKeys == 32 ? 3 : 2) void attn_f
     // finite is NaN, in rows that do not see the value.  So where a result of a
     // causal call is not finite the wave makes its rows again, key by key, each
     // key added only to the rows that see it.
-    if (a.p.causal) {
+    if (sz.causal) {
         float z = 0.0f * l;
 #pragma unroll
         for (int db = 0; db < R::DB; ++db)
@@ -244,8 +251,8 @@ __global__ __launch_bounds__(256 * kShares, kTileKeys == 32 ? 3 : 2) void attn_f
 #pragma unroll
                 for (int v = 0; v < 16; ++v) o[db][v] = 0.0f;
             for (int key = 0; key < some; ++key) {
-                const unsigned short* kr = kbase + (long long)key * a.p.k_stride + 8 * half;
-                const unsigned short* vr = vbase + (long long)key * a.p.v_stride + 4 * half;
+                const unsigned short* kr = kbase + (long long)key * sz.k_stride + 8 * half;
+                const unsigned short* vr = vbase + (long long)key * sz.v_stride + 4 * half;
                 float s = 0.0f;
 #pragma unroll
                 for (int kk = 0; kk < R::KK; ++kk) {
@@ -277,9 +284,9 @@ __global__ __launch_bounds__(256 * kShares, kTileKeys == 32 ? 3 : 2) void attn_f
         }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;          // a row that sees no key gives zeros
-    store_column<D>(a.o[rank] + (q0 + (long long)qi) * a.o_stride + (long long)head * D, o, inv, half, live);
-    if (a.lse[rank] && live && half == 0)
-        a.lse[rank][(long long)head * a.p.Tq + q0 + qi] = l == 0.0f ? -INFINITY : (mc + __log2f(l)) * kLn2;
+    store_column<D>((unsigned short*)go + (q0 + (long long)qi) * o_stride + (long long)head * D, o, inv, half, live);
+    if (glse && live && half == 0)
+        glse[(long long)head * sz.Tq + q0 + qi] = l == 0.0f ? -INFINITY : (mc + __log2f(l)) * kLn2;
 }
 
 }  // namespace
