@@ -162,7 +162,16 @@ __global__ __launch_bounds__(256) void qk_rope_kernel(RopeArgs a, int groups) {
     }
 }
 
-constexpr int kGradBlocks = 1024;      // workgroups per rank that leave a partial sum of the gains' gradients, at most
+// Workgroups a compute unit, as many as fit by registers: each has one token's
+// loads in flight, so it takes them all (4097 tokens of 24 heads of 64 on 4
+// ranks, with 2 / 3 / 4 / 5 / 6: 55 / 46 / 43 / 40 / 39 us; with 8, whose last
+// two wait, 47).
+constexpr int kGradPerCu = 6;
+constexpr int kGradLeast = 1024;       // and room for as many parts per rank, which every group of head rows may need
+int grad_blocks_most(int P) {
+    const int n = (kGradPerCu * dev_info().cus + P - 1) / P;
+    return n > kGradLeast ? n : kGradLeast;
+}
 
 struct RopeGradArgs {
     RopeArgs f;                        // q, k, v: the gradients read; kc, vc: unused
@@ -174,7 +183,7 @@ struct RopeGradArgs {
 };
 
 template <int D, class X>
-__global__ __launch_bounds__(256) void qk_rope_grad_kernel(RopeGradArgs g) {
+__global__ __launch_bounds__(256, kGradPerCu) void qk_rope_grad_kernel(RopeGradArgs g) {
     constexpr int W = D / 8, HW = 64 / W;
     __shared__ float sum[4][HW][2][D];
     const RopeArgs& a = g.f;
@@ -362,7 +371,7 @@ extern "C" int tp_qk_norm_rope(const void* const* qkv, const float* const* gain_
 
 extern "C" size_t tp_qk_norm_rope_grad_workspace_bytes(int P, int D) {
     if (P < 1 || P > RING_MAX_RANKS || (D != 64 && D != 128)) return 0;
-    return kStatusBytes + (size_t)P * kGradBlocks * 2 * D * sizeof(float);
+    return kStatusBytes + (size_t)P * grad_blocks_most(P) * 2 * D * sizeof(float);
 }
 
 extern "C" int tp_qk_norm_rope_grad(const void* const* dq, const void* const* dk, const void* const* dv,
@@ -386,14 +395,14 @@ extern "C" int tp_qk_norm_rope_grad(const void* const* dq, const void* const* dk
     if (gain_q && (!all16((const void* const*)dgain_q, P) || !all16((const void* const*)dgain_k, P))) return RING_EINVAL;
     if (!ws || ((uintptr_t)ws & 255) || ws_bytes < tp_qk_norm_rope_grad_workspace_bytes(P, D)) return RING_EWORKSPACE;
     hipStream_t s = (hipStream_t)stream;
-    // Four workgroups a compute unit in all, every group of head rows at least
-    // one wave: at most 2^21 / 512 = 4096 groups, so kGradBlocks always do.
+    // kGradPerCu workgroups a compute unit in all, every group of head rows at
+    // least one wave: at most 2^21 / 512 = 4096 groups, so kGradLeast do.
     g.groups = (Hq + 2 * Hkv + 512 / D - 1) / (512 / D);
     const long long items = (long long)T * g.groups;
-    long long blocks = (4 * dev_info().cus + P - 1) / P;
+    long long blocks = (kGradPerCu * dev_info().cus + P - 1) / P;
     if (blocks > (items + 3) / 4) blocks = (items + 3) / 4;
     if (blocks < (g.groups + 3) / 4) blocks = (g.groups + 3) / 4;
-    if (blocks > kGradBlocks) blocks = kGradBlocks;
+    if (blocks > grad_blocks_most(P)) blocks = grad_blocks_most(P);
     if (!T) blocks = 0;
     g.part = (float*)((char*)ws + kStatusBytes);
     g.status = (Status*)ws;
