@@ -205,28 +205,35 @@ __device__ __forceinline__ bool find_tile(const int* cu, const int* cu2, int B, 
     return false;
 }
 
-// Store the lane's column of a 32 x 32 block of accumulators, times f, as bf16
-// to p on: the two halves of the wave trade so that each lane stores 16
-// contiguous bytes.
-__device__ __forceinline__ void store_block(unsigned short* p, const f32x16& x, float f, int half, bool live) {
+// Accumulators 4 j .. 4 j + 7 (j even) of the lane's column of a 32 x 32 block,
+// times f, as bf16: the two halves of the wave trade, so that each lane has 8
+// contiguous values, 8 (j + half) and on.
+__device__ __forceinline__ u32x4 round_chunk(const f32x16& x, int j, float f) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
     typedef float f32x2 __attribute__((ext_vector_type(2)));
+    u32x4 y;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        // values 8 j + 4 half + 2 e, + 1 and the same of j + 1: of the pair
+        // the lower half keeps j's and gets the upper's, the upper half
+        // j + 1's
+        const f32x2 lo = {x[4 * j + 2 * e] * f, x[4 * j + 2 * e + 1] * f};
+        const f32x2 hi = {x[4 * j + 4 + 2 * e] * f, x[4 * j + 5 + 2 * e] * f};
+        const auto r = __builtin_amdgcn_permlane32_swap(
+            __builtin_bit_cast(unsigned, __builtin_convertvector(lo, bf16x2)),
+            __builtin_bit_cast(unsigned, __builtin_convertvector(hi, bf16x2)), false, false);
+        y[e] = r[0];
+        y[2 + e] = r[1];
+    }
+    return y;
+}
+
+// Store the lane's column of a 32 x 32 block of accumulators, times f, as bf16
+// to p on, 16 bytes a lane.
+__device__ __forceinline__ void store_block(unsigned short* p, const f32x16& x, float f, int half, bool live) {
 #pragma unroll
     for (int j = 0; j < 4; j += 2) {
-        u32x4 y;
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            // values 8 j + 4 half + 2 e, + 1 and the same of j + 1: of the pair
-            // the lower half keeps j's and gets the upper's, the upper half
-            // j + 1's
-            const f32x2 lo = {x[4 * j + 2 * e] * f, x[4 * j + 2 * e + 1] * f};
-            const f32x2 hi = {x[4 * j + 4 + 2 * e] * f, x[4 * j + 5 + 2 * e] * f};
-            const auto r = __builtin_amdgcn_permlane32_swap(
-                __builtin_bit_cast(unsigned, __builtin_convertvector(lo, bf16x2)),
-                __builtin_bit_cast(unsigned, __builtin_convertvector(hi, bf16x2)), false, false);
-            y[e] = r[0];
-            y[2 + e] = r[1];
-        }
+        const u32x4 y = round_chunk(x, j, f);
         if (live) *(u32x4*)(p + 8 * (j + half)) = y;
     }
 }
@@ -234,6 +241,32 @@ template <int D, class Acc>
 __device__ __forceinline__ void store_column(unsigned short* p, const Acc& x, float f, int half, bool live) {
 #pragma unroll
     for (int db = 0; db < Rows<D>::DB; ++db) store_block(p + 32 * db, x[db], f, half, live);
+}
+
+// The same by whole rows: the wave's 32 columns go through its own 32 rows of
+// LDS at byte `at`, and each store instruction writes full rows of memory,
+// where store_column's writes 32 bytes of each of 32 rows.  Full lines need not
+// wait in the L2s to be filled, so they are stored nontemporally.  off: the
+// element offset from p of this lane's column's row, n: the rows there are.
+template <int D, class Acc>
+__device__ __forceinline__ void store_rows(unsigned short* p, const Acc& x, float f, unsigned off, int n, unsigned short* lds,
+                                           int at, int lane) {
+    typedef Rows<D> R;
+    const int half = lane >> 5, r = lane & 31;
+    char* w = (char*)lds + at;
+#pragma unroll
+    for (int db = 0; db < R::DB; ++db)
+#pragma unroll
+        for (int j = 0; j < 4; j += 2)
+            *(u32x4*)(w + r * R::RB + (((4 * db + j + half) ^ R::swz(r)) * 16)) = round_chunk(x[db], j, f);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < 32 / R::RPI; ++i) {
+        const int t = i * R::RPI + lane / R::C, c = lane % R::C;
+        const u32x4 y = *(const u32x4*)(w + t * R::RB + ((c ^ R::swz(t)) * 16));
+        const unsigned to = (unsigned)__shfl((int)off, t);
+        if (t < n) __builtin_nontemporal_store(y, (u32x4*)(p + to + 8 * c));
+    }
 }
 
 // Arguments of the packed-prompt kernels (per-rank pointers by value).

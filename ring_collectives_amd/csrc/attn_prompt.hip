@@ -284,7 +284,22 @@ __global__ __launch_bounds__(256 * kShares, kTileKeys == 32 ? 3 : 2) void attn_f
         }
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;          // a row that sees no key gives zeros
-    store_column<D>((unsigned short*)go + (q0 + (long long)qi) * o_stride + (long long)head * D, o, inv, half, live);
+    // D = 128 stores whole rows through the tiles' LDS (128 prompts of 64 on 4
+    // ranks of 8 heads 34 to 32.5 us, nine of 333 27 to 25); D = 64, whose rows
+    // are half a line wide and whose registers the rows' places would cost a
+    // wave, does not (18 to 20 us)
+    if constexpr (D == 128) {
+        lds_barrier();                                       // every wave has read the tiles
+        unsigned row = m;
+        asm volatile("" : "+v"(row));                        // its place is computed here, not before the pass
+        const unsigned first = m0 / (unsigned)G;
+        const unsigned at = (row / (unsigned)G - first) * (unsigned)o_stride + row % (unsigned)G * (unsigned)D;
+        const int n = rows > m0 ? (rows - m0 < 32 ? (int)(rows - m0) : 32) : 0;
+        store_rows<D>((unsigned short*)go + (q0 + (long long)first) * o_stride + (long long)kvh * G * D, o, inv, at, n, lds,
+                      wave * 32 * R::RB, lane);
+    } else {
+        store_column<D>((unsigned short*)go + (q0 + (long long)qi) * o_stride + (long long)head * D, o, inv, half, live);
+    }
     if (glse && live && half == 0)
         glse[(long long)head * sz.Tq + q0 + qi] = l == 0.0f ? -INFINITY : (mc + __log2f(l)) * kLn2;
 }
