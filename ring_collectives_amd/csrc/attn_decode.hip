@@ -14,6 +14,10 @@
 //     rows in flight in turn, and the four results join in LDS.
 // The cache rows read bound it: the ranges are cut so that every compute unit
 // has two workgroups' loads in flight, whatever the number of requests.
+//
+// 4 ranks of 8 heads of 128 on 2: 4 requests of up to 60000 keys 153 us, 5.35
+// TB/s; 64 requests of up to 700 behind 8192 shared ones 53 us, 3.1 TB/s, the
+// join 6 of them.
 #include "attn_core.h"
 #include "attn_internal.h"
 

@@ -5,10 +5,21 @@
 //
 // Two passes, each summing its results in registers in a fixed order: one per
 // 128 query rows over the keys (dQ; it also leaves lse and delta of its rows
-// in the workspace; in shares of the keys as the forward pass), one per 128 keys over the queries of every head of the
-// group (dK, dV).  S and dP are computed in both, seven products in all where
-// five would do, but no result is added up through memory: no atomics, whose
-// order would change the results, and no fp32 copy of dQ.
+// in the workspace; in shares of the keys as the forward pass), one per 128
+// keys over the queries of every head of the group (dK, dV).  S and dP are
+// computed in both, seven products in all where five would do, but no result
+// is added up through memory: no atomics, whose order would change the
+// results, and no fp32 copy of dQ.
+//
+// delta is summed in fp32 from O as it was rounded to bf16, which costs the
+// gradients up to 2e-3 of relative error in prompts of some 60 tokens and 0.6 to
+// 1e-3 in ones of hundreds, beside the 1.6e-3 each of their own rounding and of
+// dS's.  From sum(P dP) it would be known only after the pass that uses it.
+//
+// 8192 tokens on 4 ranks of 8 heads of 128 on 2: dQ 724 us, its matrix cores 62%
+// busy at 1.8 GHz, the card's power limit; dK and dV 1230 us, 40% at 2.15 GHz,
+// one wave per SIMD (128 registers of sums and 64 of K and V in each), whose
+// products wait for its own weights.
 #include "attn_core.h"
 #include "attn_internal.h"
 
@@ -559,10 +570,10 @@ extern "C" int tp_attention_grad(const void* const* dout, const void* const* q, 
         if (!a.slots) return RING_EUNSUPPORTED;
         // Few keys: at most one workgroup of 128 keys for every second compute
         // unit, or, in long prompts, whose first keys' workgroups run longest,
-        // for every one.  4 ranks of 8 heads of 128 on 2, dQ (in one share) included, 128 and
-        // 32 keys a workgroup: one prompt of 1024 / 2048 / 4096 / 8192 tokens
-        // 160 / 315 / 691 / 1821 us and 82 / 172 / 572 / 2134; 5 prompts of 80,
-        // 31 and 21; 8 of 512, 121 and 138.
+        // for every one.  4 ranks of 8 heads of 128 on 2, dQ (in one share)
+        // included, 128 and 32 keys a workgroup: one prompt of 1024 / 2048 /
+        // 4096 / 8192 tokens 160 / 315 / 691 / 1821 us and 82 / 172 / 572 / 2134;
+        // 5 prompts of 80, 31 and 21; 8 of 512, 121 and 138.
         const long long groups = (long long)a.slots * units, cus = dev_info().cus;
         const bool few = 2 * groups <= cus || (groups <= cus + units && Tk / B >= 1024);
         if (few) a.slots = prompt_slots(B, Tk, 1, 32, units);

@@ -12,8 +12,12 @@
 // the rotation's partner values come from the lane rot / 16 further on.  Going
 // forward a wave has one such group of rows, so a step of few tokens runs wide
 // (a wave per token, its rows one group after the other, took 6.8 us for 32
-// tokens of 12 heads on 4 ranks; this 4.5); going back it keeps one group of
+// tokens of 12 heads on 4 ranks; this 3.7); going back it keeps one group of
 // rows for many tokens, since it sums the gains' gradients in registers.
+//
+// 8192 tokens of 12 heads of 128 on 4 ranks, fp32 rows, with the cache write:
+// 61.5 us, 5.5 TB/s.  Back, 4097 tokens of 24 heads of 64 in bf16 on 4 ranks:
+// 26 us, 5.2 TB/s, and 4.9 for the sum of the gains' parts in a second launch.
 #include "ring_device.h"
 #include "tp_attention.h"
 
