@@ -15,6 +15,7 @@
 #pragma once
 
 #include "gemm_core.h"
+#include "global_ptr.h"
 
 namespace ringc {
 

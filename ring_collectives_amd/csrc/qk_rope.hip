@@ -18,6 +18,7 @@
 // 8192 tokens of 12 heads of 128 on 4 ranks, fp32 rows, with the cache write:
 // 61.5 us, 5.5 TB/s.  Back, 4097 tokens of 24 heads of 64 in bf16 on 4 ranks:
 // 26 us, 5.2 TB/s, and 4.9 for the sum of the gains' parts in a second launch.
+#include "global_ptr.h"
 #include "ring_device.h"
 #include "tp_attention.h"
 

@@ -70,10 +70,6 @@ template <int POL> __device__ __forceinline__ void st2(unsigned short x, rsrc_t 
     __builtin_amdgcn_raw_buffer_store_b16(x, v, off, 0, POL);
 }
 
-// A pointer into global memory, said so: of one that asm has hidden the origin
-// of, the compiler would otherwise make flat accesses.
-template <class T> using Global = __attribute__((address_space(1))) T*;
-
 // ---------------------------------------------------------------- flags
 // A flag is one int in HBM, kFlagStride ints apart from the next.  It goes
 // from 0 to 1 when its producer has finished a tile, and back to 0 when its
