@@ -320,7 +320,7 @@ bool fill_prompt_args(PromptArgs& p, const void* const* q, const void* const* k,
         p.q[r] = (const unsigned short*)q[r];
         p.k[r] = (const unsigned short*)k[r];
         p.v[r] = (const unsigned short*)v[r];
-        if (!q[r] || (Tk && (!k[r] || !v[r]))) return false;
+        if ((Tq && !q[r]) || (Tk && (!k[r] || !v[r]))) return false;     // what has no element may have no address
         if (((uintptr_t)q[r] | (uintptr_t)k[r] | (uintptr_t)v[r]) & 15) return false;
     }
     p.cu_q = cu_q;
