@@ -94,11 +94,37 @@ def build(verbose: bool = False) -> str:
     return LIB
 
 
+def _binding_lacks() -> str:
+    """What this machine lacks to build the Python extension, if anything."""
+    import importlib.util
+    import shutil
+    import sysconfig
+    if shutil.which("g++") is None:
+        return "g++"
+    if importlib.util.find_spec("torch") is None:
+        return "torch"
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        return "Python.h"
+    from torch.utils.cpp_extension import include_paths
+    if not any(os.path.exists(os.path.join(p, "torch", "csrc", "Dtype.h")) for p in include_paths()):
+        return "torch's headers"
+    return ""
+
+
 def _build_binding(verbose: bool) -> None:
     """The Python extension of the attention calls (host code), linked to the
-    library next to it."""
+    library next to it.  The C library does without it: where what it is built
+    from is not installed it is left out, and one built for an older library
+    goes."""
     import sysconfig
 
+    lacks = _binding_lacks()
+    if lacks:
+        if os.path.exists(BINDING):
+            os.remove(BINDING)
+        print("build: no %s here, so %s is left out: the C library is whole, the attention calls from Python need it"
+              % (lacks, os.path.basename(BINDING)), flush=True)
+        return
     import torch
     from torch.utils.cpp_extension import include_paths, library_paths
     tmp = BINDING + ".tmp%d" % os.getpid()
