@@ -310,10 +310,10 @@ bool all16(const void* const* p, int P) {
 }
 
 int rope_inputs(RopeArgs& a, const void* const* qkv, const float* const* gain_q, const float* const* gain_k,
-                const float* cos_sin, const int* pos, int P, int rot) {
+                const float* cos_sin, const int* pos, int P, int rot, long long table_rows) {
     if (!qkv || !all16(qkv, P) || !gain_q != !gain_k || !pos || ((uintptr_t)pos & 3)) return RING_EINVAL;
     if (gain_q && (!all16((const void* const*)gain_q, P) || !all16((const void* const*)gain_k, P))) return RING_EINVAL;
-    if ((rot && !cos_sin) || ((uintptr_t)cos_sin & 15)) return RING_EINVAL;
+    if ((rot && table_rows && !cos_sin) || ((uintptr_t)cos_sin & 15)) return RING_EINVAL;
     for (int r = 0; r < P; ++r) {
         a.qkv[r] = qkv[r];
         a.gq[r] = gain_q ? gain_q[r] : nullptr;
@@ -338,13 +338,14 @@ extern "C" int tp_qk_norm_rope(const void* const* qkv, const float* const* gain_
                                float eps, int dtype, void* stream) {
     int rc = rope_shape(P, T, Hq, Hkv, D, rot, table_rows, cache_rows, qkv_stride, eps, dtype);
     if (rc != RING_OK) return rc;
-    if (!k != !v || !k_cache != !v_cache || !k_cache != !slots || ((uintptr_t)slots & 7)) return RING_EINVAL;
+    // what has no element may have no address: slots of no token, a cache of no row
+    if (!k != !v || !k_cache != !v_cache || (T && !k_cache != !slots) || ((uintptr_t)slots & 7)) return RING_EINVAL;
     if (T == 0) return RING_OK;
     RopeArgs a;
-    rc = rope_inputs(a, qkv, gain_q, gain_k, cos_sin, pos, P, rot);
+    rc = rope_inputs(a, qkv, gain_q, gain_k, cos_sin, pos, P, rot, table_rows);
     if (rc != RING_OK) return rc;
     if (!q || !all16(q, P) || (k && (!all16(k, P) || !all16(v, P))) ||
-        (k_cache && (!all16(k_cache, P) || !all16(v_cache, P))))
+        (k_cache && cache_rows && (!all16(k_cache, P) || !all16(v_cache, P))))
         return RING_EINVAL;
     for (int r = 0; r < P; ++r) {
         a.q[r] = (unsigned short*)q[r];
@@ -392,7 +393,7 @@ extern "C" int tp_qk_norm_rope_grad(const void* const* dq, const void* const* dk
     if (gain_q && (!dgain_q || !dgain_k)) return RING_EINVAL;
     RopeGradArgs g;
     if (T) {
-        rc = rope_inputs(g.f, qkv, gain_q, gain_k, cos_sin, pos, P, rot);
+        rc = rope_inputs(g.f, qkv, gain_q, gain_k, cos_sin, pos, P, rot, table_rows);
         if (rc != RING_OK) return rc;
         if (!dq || !dk || !dv || !dqkv || !all16(dq, P) || !all16(dk, P) || !all16(dv, P) || !all16(dqkv, P))
             return RING_EINVAL;
