@@ -66,7 +66,8 @@ extern "C" {
  * used_after and lengths_after must not be used's, lengths' or new_tokens'
  * memory (RING_EINVAL): a caller that goes step by step keeps two of each.
  * Tokens past `capacity` are left out.  1 <= B <= KV_PLAN_MAX_REQUESTS, else
- * RING_EUNSUPPORTED (B = 0: RING_OK, nothing written).
+ * RING_EUNSUPPORTED.  B = 0 is RING_OK without a launch, and writes nothing:
+ * a caller that swaps used and used_after does not swap them then.
  */
 int kv_plan(const int *lengths, const int *new_tokens, const int *free_pages, const int *used, int *block_table,
             int *lengths_after, int *cu_new, int *positions, long long *slots, int *used_after, int B, int n_free,

@@ -5,7 +5,8 @@ Each takes lists of per-rank torch tensors and single tensors that all ranks
 read, and calls the library on torch's current HIP stream (or `stream`).  The
 extension module _binding checks shapes, types and layouts (ValueError,
 TypeError) and marshals; the library's own refusals raise RingError.  Nothing
-here computes.  A call's workspace is made when none is given, and returned
+here computes (only kv_plan's outputs for no request at all are filled in
+here).  A call's workspace is made when none is given, and returned
 for the next one.
 """
 from __future__ import annotations
@@ -69,9 +70,16 @@ def kv_plan(lengths, new_tokens, free_pages, used, block_table, lengths_after, c
     block_table (B, W) gets the pages from free_pages[used..] that the new
     tokens need, positions[cu_new[b] + i] = prefix_len + lengths[b] + i and
     slots[...] that token's cache row.  used_after > len(free_pages): the pages
-    ran out, and the tokens without one have slot -1."""
+    ran out, and the tokens without one have slot -1.  Without requests nothing
+    is added: used_after = used, cu_new = [0], positions 0 and slots -1."""
     N.check(_binding().kv_plan(lengths, new_tokens, free_pages, used, block_table, lengths_after, cu_new, positions, slots,
                                used_after, page_size, prefix_len, *_at(stream)), "kv_plan")
+    if not lengths.numel():          # the library launches nothing and writes nothing then
+        with torch.cuda.stream(stream):
+            used_after.copy_(used)
+            cu_new.zero_()
+            positions.zero_()
+            slots.fill_(-1)
 
 
 def tp_qk_norm_rope(qkv, gain_q, gain_k, cos_sin, pos, q, k=None, v=None, k_cache=None, v_cache=None, slots=None,
