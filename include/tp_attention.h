@@ -128,8 +128,8 @@ size_t tp_qk_norm_rope_grad_workspace_bytes(int P, int D);
  * fp32, the softmax weights rounded to bf16 for the second product.
  * Offsets are clamped to [0, Tq] and [0, Tk], and one below its prompt's start
  * makes the prompt empty; rows that no prompt covers are not written.
- * scale > 0.  A key or value that is not finite reaches only the queries that
- * see it.
+ * scale > 0, and finite times log2(e).  A key or value that is not finite
+ * reaches only the queries that see it.
  */
 int tp_attention(const void *const *q, const void *const *k, const void *const *v, void *const *o, float *const *lse,
                  const int *cu_q, const int *cu_k, int P, int B, int Tq, int Tk, int Hq, int Hkv, int D,
@@ -168,7 +168,7 @@ size_t tp_attention_grad_workspace_bytes(int P, int Tq, int Hq);
  * outside [0, pages) take no part; a request without keys gives o = 0.  Rows
  * of the cache that are no key of a request never reach its result.
  * pages * page_size and table_stride * page_size stay below 2^31.
- * scale > 0.  The workspace's size depends on the device's compute units.
+ * scale as in tp_attention.  The workspace's size depends on the device's compute units.
  */
 int tp_attention_decode(const void *const *q, const void *const *k_cache, const void *const *v_cache, void *const *o,
                         const int *block_table, const int *lengths, const int *prefix_pages, int P, int B, int Hq,

@@ -487,7 +487,7 @@ extern "C" int tp_attention_decode(const void* const* q, const void* const* k_ca
     if (P < 1 || P > RING_MAX_RANKS || B < 0 || Hq < 1 || Hkv < 1 || table_stride < 0 || pages < 0 || prefix_len < 0)
         return RING_EINVAL;
     if (page_size < 1 || (page_size & (page_size - 1)) || page_size > (1 << 20)) return RING_EINVAL;
-    if (!(scale > 0.0f) || !(scale <= 3.0e38f)) return RING_EINVAL;
+    if (!scale_ok(scale)) return RING_EINVAL;
     if (!decode_shape(P, B, Hq, Hkv, D, table_stride, page_size, prefix_len) || (long long)pages * page_size >= (1LL << 31))
         return RING_EUNSUPPORTED;
     if (!row_stride_ok(q_stride, Hq, D) || !row_stride_ok(o_stride, Hq, D)) return RING_EINVAL;

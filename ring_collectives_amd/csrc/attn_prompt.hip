@@ -344,7 +344,7 @@ bool fill_prompt_args(PromptArgs& p, const void* const* q, const void* const* k,
 // elements, so that a tile's view stays below 2 GiB.
 int prompt_shape(int P, int B, int Tq, int Tk, int Hq, int Hkv, int D, float scale) {
     if (P < 1 || P > RING_MAX_RANKS || B < 0 || Tq < 0 || Tk < 0 || Hq < 1 || Hkv < 1) return RING_EINVAL;
-    if (!(scale > 0.0f) || !(scale <= 3.0e38f)) return RING_EINVAL;
+    if (!scale_ok(scale)) return RING_EINVAL;
     if (Hq % Hkv || (D != 64 && D != 128) || (long long)Hq * D >= kMaxRow || (long long)Hkv * D >= kMaxRow)
         return RING_EUNSUPPORTED;
     return RING_OK;
