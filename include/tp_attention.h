@@ -18,8 +18,8 @@
  *   - arrays of P pointers are host arrays of device pointers, read during
  *     the call only; single pointers are device pointers to one copy that all
  *     ranks read (lengths, tables, positions).
- *   - bf16 data and fp32 `dtype` data is 16-byte aligned; a row stride counts
- *     elements from one token's row to the next, is a multiple of 8, at least
+ *   - bf16 data and fp32 `dtype` data is 16-byte aligned, integers and lse are
+ *     aligned as their types are; a row stride counts elements from one token's row to the next, is a multiple of 8, at least
  *     heads * D and below 2^21.  The heads of a row lie D apart, so q, k and v
  *     may be slices of one packed row.
  *   - D is 64 or 128 and Hkv divides Hq: query head h reads key head

@@ -517,7 +517,7 @@ extern "C" int tp_attention_grad(const void* const* dout, const void* const* q, 
         !row_stride_ok(dk_stride, Hkv, D) || !row_stride_ok(dv_stride, Hkv, D))
         return RING_EINVAL;
     if (B == 0 || (Tq == 0 && Tk == 0)) return RING_OK;
-    if (!cu_q || !cu_k) return RING_EINVAL;
+    if (!cu_q || !cu_k || (((uintptr_t)cu_q | (uintptr_t)cu_k) & 3)) return RING_EINVAL;
     GradArgs a;
     if (!fill_prompt_args(a.p, q, k, v, cu_q, cu_k, P, B, Tq, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride,
                           causal ? 1 : 0, scale))

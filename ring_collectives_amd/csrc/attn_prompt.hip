@@ -375,7 +375,7 @@ extern "C" int tp_attention(const void* const* q, const void* const* k, const vo
         !row_stride_ok(o_stride, Hq, D))
         return RING_EINVAL;
     if (Tq == 0 || B == 0) return RING_OK;
-    if (!cu_q || !cu_k) return RING_EINVAL;
+    if (!cu_q || !cu_k || (((uintptr_t)cu_q | (uintptr_t)cu_k) & 3)) return RING_EINVAL;
     FwdArgs a;
     if (!fill_prompt_args(a.p, q, k, v, cu_q, cu_k, P, B, Tq, Tk, Hq, Hkv, D, q_stride, k_stride, v_stride,
                           causal ? 1 : 0, scale))

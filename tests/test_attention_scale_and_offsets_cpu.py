@@ -31,3 +31,9 @@ def test_a_scale_that_is_infinite_in_base_2_is_refused(call, scale):
     """The kernels multiply by scale log2(e): an infinite one would make NaN
     of scores of zero, whose weights are plain."""
     assert call(scale=scale) == N.RING_EINVAL
+
+
+@pytest.mark.parametrize("call", [fwd, grad])
+@pytest.mark.parametrize("kw", [dict(cq=0x1002), dict(ck=0x2001), dict(cq=0x1003, ck=0x2003)])
+def test_offsets_off_their_alignment_are_refused(call, kw):
+    assert call(**kw) == N.RING_EINVAL
