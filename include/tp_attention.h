@@ -168,7 +168,9 @@ size_t tp_attention_grad_workspace_bytes(int P, int Tq, int Hq);
  * outside [0, pages) take no part; a request without keys gives o = 0.  Rows
  * of the cache that are no key of a request never reach its result.
  * pages * page_size and table_stride * page_size stay below 2^31.
- * scale as in tp_attention.  The workspace's size depends on the device's compute units.
+ * scale as in tp_attention.  The workspace's size depends on the device's
+ * compute units; that of a batch holds every smaller batch with the same other
+ * sizes.
  */
 int tp_attention_decode(const void *const *q, const void *const *k_cache, const void *const *v_cache, void *const *o,
                         const int *block_table, const int *lengths, const int *prefix_pages, int P, int B, int Hq,

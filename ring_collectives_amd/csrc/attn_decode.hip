@@ -461,6 +461,25 @@ size_t decode_ws(int P, int B, int Hq, int Hkv, int D, const Cuts& c) {
     return kStatusBytes + (parts * P * B * Hq * (D + 2) * sizeof(float) + 255) / 256 * 256;
 }
 
+// The most that a batch of B requests or fewer needs, so that a workspace kept
+// from call to call holds a batch that shrinks: fewer requests are cut into
+// more parts.  Own keys are in one part from 2 cus requests on, and batches of
+// the same number of 128-row tiles have their prefix in the same parts, so the
+// largest of each number and the small batches are all there is to look at.
+size_t decode_ws_upto(int P, int B, int Hq, int Hkv, int D, int width, int page, int prefix, int cus) {
+    size_t most = kStatusBytes;
+    auto look = [&](long long b) {
+        const int n = (int)(b < 1 ? 1 : b < B ? b : B);
+        const size_t w = decode_ws(P, n, Hq, Hkv, D, decode_cuts(P, n, Hq, Hkv, width, page, prefix, cus));
+        if (w > most) most = w;
+    };
+    if (!B) return most;
+    for (int b = 1; b < B && b <= 2 * cus; ++b) look(b);
+    for (int t = 1; prefix && t <= cus && (long long)kPreRows * t / (Hq / Hkv) < B; ++t) look((long long)kPreRows * t / (Hq / Hkv));
+    look(B);
+    return most;
+}
+
 bool decode_shape(int P, int B, int Hq, int Hkv, int D, int width, int page, int prefix) {
     return P >= 1 && P <= RING_MAX_RANKS && B >= 0 && Hq >= 1 && Hkv >= 1 && width >= 0 && prefix >= 0 && page >= 1 &&
            !(page & (page - 1)) && page <= (1 << 20) && Hq % Hkv == 0 && (D == 64 || D == 128) &&
@@ -476,7 +495,7 @@ using namespace ringc;
 extern "C" size_t tp_attention_decode_workspace_bytes(int P, int B, int Hq, int Hkv, int D, int table_stride,
                                                       int page_size, int prefix_len) {
     if (!decode_shape(P, B, Hq, Hkv, D, table_stride, page_size, prefix_len)) return 0;
-    return decode_ws(P, B, Hq, Hkv, D, decode_cuts(P, B ? B : 1, Hq, Hkv, table_stride, page_size, prefix_len, dev_info().cus));
+    return decode_ws_upto(P, B, Hq, Hkv, D, table_stride, page_size, prefix_len, dev_info().cus);
 }
 
 extern "C" int tp_attention_decode(const void* const* q, const void* const* k_cache, const void* const* v_cache,
