@@ -19,9 +19,10 @@
  *     the call only; single pointers are device pointers to one copy that all
  *     ranks read (lengths, tables, positions).
  *   - bf16 data and fp32 `dtype` data is 16-byte aligned, integers and lse are
- *     aligned as their types are; a row stride counts elements from one token's row to the next, is a multiple of 8, at least
- *     heads * D and below 2^21.  The heads of a row lie D apart, so q, k and v
- *     may be slices of one packed row.
+ *     aligned as their types are; a row stride counts elements from one token's
+ *     row to the next, is a multiple of 8, at least heads * D and below 2^21.
+ *     The heads of a row lie D apart, so q, k and v may be slices of one packed
+ *     row.  What has no element may have no address.
  *   - D is 64 or 128 and Hkv divides Hq: query head h reads key head
  *     h / (Hq / Hkv).  Others: RING_EUNSUPPORTED.
  *   - outputs must not overlap inputs or each other (not checked; tensors
@@ -163,7 +164,8 @@ size_t tp_attention_grad_workspace_bytes(int P, int Tq, int Hq);
  * shared by all requests, and its own, key j at page block_table[b *
  * table_stride + j / page_size] likewise for j < lengths[b] (the new token's
  * row among them, if it is to be seen).  o[r] = softmax(scale q k^T) v over
- * both; the prefix is read once for all requests.
+ * both; the prefix is read once for every 128 rows (request, head of the group
+ * that shares a key head).
  * Lengths are clamped to [0, table_stride * page_size]; keys whose page lies
  * outside [0, pages) take no part; a request without keys gives o = 0.  Rows
  * of the cache that are no key of a request never reach its result.

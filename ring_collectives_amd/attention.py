@@ -7,7 +7,7 @@ extension module _binding checks shapes, types and layouts (ValueError,
 TypeError) and marshals; the library's own refusals raise RingError.  Nothing
 here computes (only kv_plan's outputs for no request at all are filled in
 here).  A call's workspace is made when none is given, and returned
-for the next one.
+for the next one of the same sizes.
 """
 from __future__ import annotations
 
@@ -132,8 +132,9 @@ def tp_attention_decode(q, k_cache, v_cache, o, block_table, lengths, page_size:
                         prefix_len: int = 0, scale=None, ws=None, stream=None):
     """o[r] <- attention of one query token per request, q[r] (B, Hq, D), over
     the paged cache k_cache[r], v_cache[r] (rows, Hkv, D): the first prefix_len
-    rows of prefix_pages, shared by all requests and read once, and the first
-    lengths[b] rows of block_table[b] (B, W int32)."""
+    rows of prefix_pages, shared by all requests and read once for every 128
+    (request, head of the group), and the first lengths[b] rows of
+    block_table[b] (B, W int32).  The workspace of a batch holds smaller ones."""
     if ws is None:
         B, Hq, D = _lead(q, 3, "q")
         Hkv, W = _lead(k_cache, 3, "k_cache")[1], _shape(block_table, 2, "block_table")[1]

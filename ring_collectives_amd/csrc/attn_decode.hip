@@ -11,9 +11,22 @@
 //   - own-key workgroups: one request and (rank, key head), up to 32 heads of
 //     the group, against a range of its own keys; each of the four waves takes
 //     a part of the range through LDS of its own, key and value tiles of 32
-//     rows in flight in turn, and the four results join in LDS.
-// The cache rows read bound it: the ranges are cut so that every compute unit
-// has two workgroups' loads in flight, whatever the number of requests.
+//     rows in turn, and the four results join in LDS.
+// The cache rows read bound it.  The ranges are cut for two workgroups a compute
+// unit, whose loads overlap with each other's products, by the shapes alone, so
+// that the grid of a captured call holds for any lengths:
+//   - every request gets as many parts, whatever its length.  64 requests on 4
+//     ranks of 8 heads of 128 on 2, 375 MB of keys and values: of 1430 keys each
+//     70 us, one of 60000 among 63 of 500 733 us, since that one is read by one
+//     workgroup a unit.  A table wider than the lengths makes empty parts: 4 of
+//     700 keys under one of 704 and of 131072 tokens 11 us both.
+//   - at most kMaxParts workgroups go to a request of one (rank, key head), so
+//     one request on less than 4 of them has less than one a compute unit (60000
+//     keys of one key head 20 us, 1.6 TB/s).
+// Within a wave little overlaps: before a tile's first row fragments the
+// compiler waits for every load in flight, which are the prefix's next tile and
+// the own keys' values of the same one.  What stays in flight is the next tile's
+// keys of a request, while this tile's weights and second product are made.
 //
 // 4 ranks of 8 heads of 128 on 2: 4 requests of up to 60000 keys 153 us, 5.35
 // TB/s; 64 requests of up to 700 behind 8192 shared ones 53 us, 3.1 TB/s, the
@@ -170,7 +183,8 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a) {
             seen_next = __ballot(page_row(a.prefix_pages, k0 + lane, a.prefix) >= 0);
         };
         // restrict for the effect told at the prompts' pass: no wait for the
-        // loads in flight before a tile's transposed reads
+        // loads in flight before a tile's transposed reads (the compiler puts
+        // one before its row reads all the same)
         auto pass = [&](const unsigned short* __restrict__ kc, const unsigned short* __restrict__ vc) __attribute__((always_inline)) {
             auto load = [&](int buf) {
 #pragma unroll
@@ -259,8 +273,8 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a) {
             for (int i = 0; i < J; ++i) id[i] = tid[i * R::RPI + lane / R::C];
             return __builtin_amdgcn_readfirstlane((unsigned)__ballot(tid[col] >= 0));
         };
-        // restrict for the effect told at the prompts' pass: no wait for the
-        // loads in flight before a tile's transposed reads
+        // restrict as above: no wait for the next keys before a tile's
+        // transposed reads
         auto pass = [&](const unsigned short* __restrict__ kc, const unsigned short* __restrict__ vc) __attribute__((always_inline)) {
             auto load = [&](const unsigned short* base, const int (&id)[J], int at) __attribute__((always_inline)) {
 #pragma unroll
@@ -283,7 +297,7 @@ __global__ __launch_bounds__(256, 2) void attn_decode_kernel(DecodeArgs a) {
                     int was[J];
 #pragma unroll
                     for (int i = 0; i < J; ++i) was[i] = id[i];
-                    wait_vm(J);                           // the keys of tile j have landed, its values may be in flight
+                    wait_vm(J);                           // the keys of tile j have landed (and, by the compiler's wait, its values)
                     if (~has) blank_rows(was, ka);
                     f32x16 s[1];
 #pragma unroll
@@ -429,8 +443,8 @@ struct Cuts {
     long long pre_tiles;
 };
 
-// Parts of the prefix and of the own keys.  Two workgroups run on a compute
-// unit.  The prefix is cut until it alone would give each one workgroup, as far
+// Parts of the prefix and of the own keys, the same for every request.  Two
+// workgroups run on a compute unit.  The prefix is cut until it alone would give each one workgroup, as far
 // as every part keeps four tiles; the own keys until they would fill the other
 // one (both, without a prefix), as far as every wave keeps a tile.  Own keys
 // that a workgroup's waves see in less than four tiles each stay whole: parts

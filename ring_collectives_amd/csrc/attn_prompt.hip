@@ -17,8 +17,10 @@
 //
 // One prompt of 16384 tokens on 4 ranks of 4 heads of 128 on 1: 1000 to 1020
 // us, 1.09 PFLOP/s, at the card's power limit (matrix cores 56% busy at 1.7
-// GHz).  D = 64 has half the products per weight, whose exponentials bound it:
-// 16384 tokens on 4 ranks of 4 heads of 64, 650 to 680 us.  12 prompts of 8192
+// GHz).  D = 64 has half the products per weight, so its vector instructions
+// count for more (the VALU is active 79% of the time, nearly a third of that in
+// exponentials, the matrix cores 50%, at 1.7 GHz): 16384 tokens on 4 ranks of 4
+// heads of 64 on 1, 610 to 680 us.  12 prompts of 8192
 // tokens in all, 4 ranks of 8 heads of 128 on 2: 93 us, of which reading Q and
 // writing O take 35.
 #include "attn_core.h"
@@ -195,8 +197,8 @@ __global__ __launch_bounds__(256 * kShares, kTileKeys == 32 ? 3 : 2) void attn_f
                     s[kb][v] = exp2_hw(__builtin_fmaf(s[kb][v], c, -sub));
                     lp[v % 4] += s[kb][v];
                 }
-            // P is rounded to bf16 for the matrix cores (relative error 2^-9 of
-            // each weight; l sums the unrounded ones in fp32).
+            // P is rounded to bf16 for the matrix cores (relative error up to
+            // 2^-8 of each weight; l sums the unrounded ones in fp32).
 #pragma unroll
             for (int ks = 0; ks < kTileKeys / 16; ++ks) {
                 const bf16x8 pf = round8(s[ks / 2], ks % 2);
@@ -243,7 +245,11 @@ __global__ __launch_bounds__(256 * kShares, kTileKeys == 32 ? 3 : 2) void attn_f
     // The product of a weight that the mask made 0 with a value that is not
     // finite is NaN, in rows that do not see the value.  So where a result of a
     // causal call is not finite the wave makes its rows again, key by key, each
-    // key added only to the rows that see it.
+    // key added only to the rows that see it.  That is one trip to memory per key,
+    // some 2 us: 16384 tokens on 4 ranks of 4 heads of 128 take 34 ms with one NaN
+    // in the last query and 76 ms where no row is finite, instead of 1.1; 12
+    // prompts of 8192 tokens in all 2.4 and 3.9 ms instead of 0.08.  It also makes
+    // the 32-key kernel spill 109 registers, in this part alone.
     if (sz.causal) {
         float z = 0.0f * l;
 #pragma unroll
