@@ -15,14 +15,14 @@
 // make many workgroups that spend much of their time in their first loads and
 // last stores, tiles of 32 keys and three (kShort).
 //
-// One prompt of 16384 tokens on 4 ranks of 4 heads of 128 on 1: 1000 to 1020
-// us, 1.09 PFLOP/s, at the card's power limit (matrix cores 56% busy at 1.7
+// One prompt of 16384 tokens on 4 ranks of 4 heads of 128 on 1: 1000 to 1080
+// us, 1.02 to 1.1 PFLOP/s, at the card's power limit (matrix cores 56% busy at 1.7
 // GHz).  D = 64 has half the products per weight, so its vector instructions
 // count for more (the VALU is active 79% of the time, nearly a third of that in
 // exponentials, the matrix cores 50%, at 1.7 GHz): 16384 tokens on 4 ranks of 4
-// heads of 64 on 1, 610 to 680 us.  12 prompts of 8192
-// tokens in all, 4 ranks of 8 heads of 128 on 2: 93 us, of which reading Q and
-// writing O take 35.
+// heads of 64 on 1, 610 to 680 us.  12 prompts of 8192 tokens in all, 4 ranks of
+// 8 heads of 128 on 2: 93 us, where reading Q and writing O alone would take 35;
+// the waves wait 40% of their cycles.
 #include "attn_core.h"
 #include "attn_internal.h"
 
