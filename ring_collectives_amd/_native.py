@@ -52,6 +52,18 @@ SIGNATURES = {
     "tp_attention_grad_workspace_bytes": (_sz, [_i] * 3),
     "tp_attention_decode": (_i, [_pp] * 4 + [_vp] * 3 + [_i] * 9 + [_ll, _ll, _f, _vp, _sz, _vp]),
     "tp_attention_decode_workspace_bytes": (_sz, [_i] * 8),
+    "beam_select": (_i, [_pp] + [_vp] * 6 + [_i] * 6 + [_ll, _i, _i, _vp, _sz, _vp]),
+    "beam_select_workspace_bytes": (_sz, [_i] * 5),
+    "kv_fork": (_i, [_vp] * 12 + [_i] * 7 + [_vp, _sz, _vp]),
+    "kv_fork_workspace_bytes": (_sz, [_i] * 2),
+    "kv_compact": (_i, [_vp] * 7 + [_i] * 5 + [_vp, _sz, _vp]),
+    "kv_compact_workspace_bytes": (_sz, [_i]),
+    "kv_copy_pages": (_i, [_pp, _vp, _vp, _i, _i, _i, _ll, _vp]),
+    "kv4_page_bytes": (_sz, [_i] * 3),
+    "tp_kv4_write": (_i, [_pp] * 3 + [_vp] + [_i] * 6 + [_ll, _ll, _vp]),
+    "tp_kv4_read": (_i, [_pp, _vp, _pp, _pp] + [_i] * 6 + [_ll, _ll, _vp]),
+    "tp_attention_decode_kv4": (_i, [_pp] * 3 + [_vp] * 3 + [_i] * 9 + [_ll, _ll, _f, _vp, _sz, _vp]),
+    "tp_attention_decode_kv4_workspace_bytes": (_sz, [_i] * 6),
     "ring_last_error": (_i, [_vp, _sz, _vp, ctypes.POINTER(ctypes.c_int)]),
     "ring_strerror": (ctypes.c_char_p, [_i]),
 }

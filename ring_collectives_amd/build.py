@@ -15,7 +15,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 SOURCES = ["ring_api.hip", "ring_kernels.hip", "gemm_rs.hip", "ag_gemm.hip", "tp_mlp.hip", "kv_plan.hip",
-           "qk_rope.hip", "attn_prompt.hip", "attn_grad.hip", "attn_decode.hip"]
+           "qk_rope.hip", "attn_prompt.hip", "attn_grad.hip", "attn_decode.hip", "beam_select.hip", "kv_pages.hip",
+           "kv4_cache.hip", "attn_decode_kv4.hip"]
 LIB = os.path.join(HERE, "libring_collectives.so")
 BINDING = os.path.join(HERE, "_binding.so")
 ARCH = os.environ.get("RING_OFFLOAD_ARCH", "gfx950")

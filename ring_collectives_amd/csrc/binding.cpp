@@ -1,5 +1,6 @@
-// binding.cpp -- the attention calls' Python entry points, below attention.py:
-// the checks of the tensors and the calls of the C ABI.
+// binding.cpp -- the Python entry points of the attention calls and of the beam
+// search, below attention.py and search.py: the checks of the tensors and the
+// calls of the C ABI.
 //
 // A call takes six to eleven lists of P tensors.  Looking at each in Python
 // (shape, strides, type, device, address) costs over half a microsecond a
@@ -8,7 +9,7 @@
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/autograd/python_variable.h>
 
-#include "tp_attention.h"
+#include "tp_search.h"
 
 namespace {
 
@@ -366,6 +367,187 @@ PyObject* decode(const Args& c) {
                                     c.real(9), ws, bytes, c.stream(11)));
 }
 
+// ---------------------------------------------------------------- beam search
+// two or three tensors that a call takes or writes as one shape, any of them
+void* shaped(const Args& c, Py_ssize_t i, const char* name, ScalarType dt, at::IntArrayRef shape) {
+    const Tensor& t = c.tensor(c.a[i], name);
+    if (t.sizes() != shape)
+        raise(PyExc_ValueError, "%s: %s must be %s, got %s", c.what, name, text(shape).c_str(), text(t.sizes()).c_str());
+    return c.one(i, name, dt);
+}
+// flags: bytes or bools
+void* flags(const Args& c, Py_ssize_t i, const char* name, at::IntArrayRef shape) {
+    if (c.none(i)) return nullptr;
+    const ScalarType dt = c.tensor(c.a[i], name).scalar_type();
+    return shaped(c, i, name, dt == at::kBool ? at::kBool : at::kByte, shape);
+}
+at::DimVector sizes_of(const Args& c, Py_ssize_t i, const char* name, int64_t dims, const char* what) {
+    const Tensor& t = c.tensor(c.a[i], name);
+    if (t.dim() != dims) raise(PyExc_ValueError, "%s: %s is %s, got %s", c.what, name, what, text(t.sizes()).c_str());
+    for (int64_t n : t.sizes())
+        if (n > 0x7fffffffLL) raise(PyExc_ValueError, "%s: %s is too large", c.what, name);
+    return at::DimVector(t.sizes());
+}
+
+// logits, scores, parents, tokens, scores_after, vocab, done, done_after, end_token, ws
+PyObject* select(const Args& c) {
+    int P;
+    ScalarType dt;
+    const auto s = leading(c, 0, "logits", 2, P, &dt);
+    if (dt != at::kFloat && dt != at::kBFloat16)
+        raise(PyExc_TypeError, "%s: logits are float32 or bfloat16, got %s", c.what, name_of(dt));
+    Ranks x = ranks(c, 0, "logits", P, s, dt, false);
+    const auto sc = sizes_of(c, 1, "scores", 2, "(groups, beams)"), out = sizes_of(c, 2, "parents", 2, "(groups, places)");
+    if (sc[0] * sc[1] != s[0])
+        raise(PyExc_ValueError, "%s: %lld rows of logits are not %s beams", c.what, (long long)s[0], text(sc).c_str());
+    if (out[0] != sc[0]) raise(PyExc_ValueError, "%s: parents are (%lld, places), got %s", c.what, (long long)sc[0], text(out).c_str());
+    const void* score = shaped(c, 1, "scores", at::kFloat, sc);
+    int *parents = (int*)shaped(c, 2, "parents", at::kInt, out), *tokens = (int*)shaped(c, 3, "tokens", at::kInt, out);
+    float* after = (float*)shaped(c, 4, "scores_after", at::kFloat, out);
+    const void* done = flags(c, 6, "done", sc);
+    void* done_after = flags(c, 7, "done_after", out);
+    if (!sc[1] || !out[1]) raise(PyExc_ValueError, "%s: groups have at least one beam and one place", c.what);
+    if (c.none(6) != c.none(7)) raise(PyExc_ValueError, "%s: done and done_after go together", c.what);
+    // rows that are one: their stride is any that the call takes
+    const long long row = s[0] > 1 ? x.row : (s[1] + 7) / 8 * 8;
+    size_t bytes;
+    void* ws = c.ws(9, bytes);
+    return code(beam_select(in(x), (const float*)score, (const unsigned char*)done, parents, tokens, after, (unsigned char*)done_after,
+                            P, (int)sc[0], (int)sc[1], (int)out[1], (int)s[1], c.int32(5, "vocab"), row, c.int32(8, "end_token"),
+                            dt == at::kFloat ? RING_F32 : RING_BF16, ws, bytes, c.stream(10)));
+}
+
+// block_table, lengths, parents, keep, free_pages, used, table_after,
+// lengths_after, copies, n_copies, shared, used_after, group, page_size, pages, ws
+PyObject* fork(const Args& c) {
+    const auto tab = sizes_of(c, 0, "block_table", 2, "(rows, pages)"), after = sizes_of(c, 6, "table_after", 2, "(rows, pages)");
+    if (after[1] != tab[1])
+        raise(PyExc_ValueError, "%s: table_after has rows of %lld pages, got %s", c.what, (long long)tab[1], text(after).c_str());
+    const int64_t B = tab[0], B2 = after[0];
+    int64_t nfree;
+    const int* table = (const int*)c.one(0, "block_table", at::kInt);
+    const int* len = (const int*)c.one(1, "lengths", at::kInt, B);
+    const int* par = (const int*)c.one(2, "parents", at::kInt, B2);
+    const int* keep = c.none(3) ? nullptr : (const int*)c.one(3, "keep", at::kInt, B2);
+    int* fp = (int*)c.one(4, "free_pages", at::kInt, -1, &nfree);
+    const int* used = (const int*)c.one(5, "used", at::kInt, 1);
+    int* ta = (int*)c.one(6, "table_after", at::kInt);
+    int* la = (int*)c.one(7, "lengths_after", at::kInt, B2);
+    int* copies = (int*)shaped(c, 8, "copies", at::kInt, {B2, 2});
+    int* nc = (int*)c.one(9, "n_copies", at::kInt, 1);
+    const int group = c.int32(12, "group");
+    if (group < 1 || B2 % group) raise(PyExc_ValueError, "%s: %lld rows are not groups of %d", c.what, (long long)B2, group);
+    int* shared = c.none(10) ? nullptr : (int*)c.one(10, "shared", at::kInt, B2 / group);
+    int* ua = (int*)c.one(11, "used_after", at::kInt, 1);
+    if (nfree > 0x7fffffff) raise(PyExc_ValueError, "%s: sizes must fit 32 bits", c.what);
+    size_t bytes;
+    void* ws = c.ws(15, bytes);
+    return code(kv_fork(table, len, par, keep, fp, used, ta, la, copies, nc, shared, ua, (int)B, (int)B2, group, (int)nfree,
+                        (int)tab[1], c.int32(13, "page_size"), c.int32(14, "pages"), ws, bytes, c.stream(16)));
+}
+
+// block_table, lengths, table_after, free_pages, copies, n_copies, used_after,
+// page_size, first_page, ws
+PyObject* compact(const Args& c) {
+    const auto tab = sizes_of(c, 0, "block_table", 2, "(rows, pages)");
+    int64_t nfree;
+    const int* table = (const int*)c.one(0, "block_table", at::kInt);
+    const int* len = (const int*)c.one(1, "lengths", at::kInt, tab[0]);
+    int* ta = (int*)shaped(c, 2, "table_after", at::kInt, tab);
+    int* fp = (int*)c.one(3, "free_pages", at::kInt, -1, &nfree);
+    if (nfree > 0x7fffffff) raise(PyExc_ValueError, "%s: sizes must fit 32 bits", c.what);
+    int* copies = (int*)shaped(c, 4, "copies", at::kInt, {nfree / 2, 2});
+    int* nc = (int*)c.one(5, "n_copies", at::kInt, 1);
+    int* ua = (int*)c.one(6, "used_after", at::kInt, 1);
+    size_t bytes;
+    void* ws = c.ws(9, bytes);
+    return code(kv_compact(table, len, ta, fp, copies, nc, ua, (int)tab[0], (int)nfree, (int)tab[1], c.int32(7, "page_size"),
+                           c.int32(8, "first_page"), ws, bytes, c.stream(10)));
+}
+
+// caches, copies, n_copies, pages
+PyObject* copy_pages(const Args& c) {
+    const List l(c.a[0], c.what, "caches");
+    if (l.size() < 1 || l.size() > 2 * RING_MAX_RANKS)
+        raise(PyExc_ValueError, "%s: 1..%d caches, got %lld", c.what, 2 * RING_MAX_RANKS, (long long)l.size());
+    void* p[2 * RING_MAX_RANKS];
+    const int pages = c.int32(3, "pages");
+    if (pages < 0) raise(PyExc_ValueError, "%s: pages must not be negative", c.what);
+    long long bytes = -1;
+    for (Py_ssize_t i = 0; i < l.size(); ++i) {
+        const Tensor& t = c.tensor(l.at(i), "caches");
+        c.on_device(t, "caches");
+        if (!t.is_contiguous()) raise(PyExc_ValueError, "%s: caches must be contiguous", c.what);
+        const long long n = (long long)t.nbytes();
+        if (pages ? n % pages : n) raise(PyExc_ValueError, "%s: a cache of %lld bytes is not %d pages", c.what, n, pages);
+        if (bytes >= 0 && n != bytes) raise(PyExc_ValueError, "%s: every cache must be of the same size", c.what);
+        bytes = n;
+        p[i] = t.data_ptr();
+    }
+    const auto s = sizes_of(c, 1, "copies", 2, "(copies, 2)");
+    const int* copies = (const int*)shaped(c, 1, "copies", at::kInt, {s[0], 2});
+    const int* nc = (const int*)c.one(2, "n_copies", at::kInt, 1);
+    return code(kv_copy_pages(p, copies, nc, (int)l.size(), (int)s[0], pages, pages ? bytes / pages : 0, c.stream(4)));
+}
+
+// A 4-bit cache: P tensors (pages, Hkv, kv4_page_bytes(1, D, page_size)).
+struct Cache4 {
+    Ranks p;
+    int pages, Hkv, page;
+};
+Cache4 cache4(const Args& c, Py_ssize_t i, int P, int64_t D, int page) {
+    int P2;
+    const auto s = leading(c, i, "cache", 3, P2);
+    Cache4 r;
+    r.p = ranks(c, i, "cache", P, s, at::kByte, true);
+    r.pages = (int)s[0];
+    r.Hkv = (int)s[1];
+    r.page = page;
+    const size_t bytes = D == 64 || D == 128 ? kv4_page_bytes(1, (int)D, page) : 0;
+    if (bytes && (int64_t)bytes != s[2])
+        raise(PyExc_ValueError, "%s: a page of %d rows of %lld values takes %lld bytes a head, the cache has %lld", c.what, page,
+              (long long)D, (long long)bytes, (long long)s[2]);
+    return r;
+}
+
+// k, v, cache, slots, page_size
+PyObject* kv4_rows(const Args& c, Py_ssize_t k_at, Py_ssize_t cache_at, Py_ssize_t slots_at, bool write) {
+    int P;
+    const auto s = leading(c, k_at, "k", 3, P);
+    Ranks k = ranks(c, k_at, "k", P, s, at::kBFloat16, false), v = ranks(c, k_at + 1, "v", P, s, at::kBFloat16, false);
+    Cache4 h = cache4(c, cache_at, P, s[2], c.int32(4, "page_size"));
+    if (h.Hkv != s[1]) raise(PyExc_ValueError, "%s: the cache holds %d heads, k %lld", c.what, h.Hkv, (long long)s[1]);
+    const long long* slots = (const long long*)c.one(slots_at, "slots", at::kLong, s[0]);
+    if (write)
+        return code(tp_kv4_write(in(k), in(v), as<void>(h.p), slots, P, (int)s[0], h.Hkv, (int)s[2], h.page, h.pages, k.row, v.row,
+                                 c.stream(5)));
+    return code(tp_kv4_read(in(h.p), slots, as<void>(k), as<void>(v), P, (int)s[0], h.Hkv, (int)s[2], h.page, h.pages, k.row, v.row,
+                            c.stream(5)));
+}
+PyObject* kv4_write(const Args& c) { return kv4_rows(c, 0, 2, 3, true); }
+// cache, slots, k, v, page_size
+PyObject* kv4_read(const Args& c) { return kv4_rows(c, 2, 0, 1, false); }
+
+// q, cache, o, block_table, lengths, page_size, shared, group, scale, ws
+PyObject* decode_kv4(const Args& c) {
+    int P;
+    const auto s = leading(c, 0, "q", 3, P);
+    const int64_t B = s[0], D = s[2];
+    Ranks q = ranks(c, 0, "q", P, s, at::kBFloat16, false), o = ranks(c, 2, "o", P, s, at::kBFloat16, false);
+    Cache4 h = cache4(c, 1, P, D, c.int32(5, "page_size"));
+    const auto tab = sizes_of(c, 3, "block_table", 2, "(requests, pages)");
+    if (tab[0] != B) raise(PyExc_ValueError, "%s: block_table is (%lld, pages), got %s", c.what, (long long)B, text(tab).c_str());
+    const int* tp = (const int*)c.one(3, "block_table", at::kInt);
+    const int* len = (const int*)c.one(4, "lengths", at::kInt, B);
+    const int group = c.int32(7, "group");
+    if (group < 1 || B % group) raise(PyExc_ValueError, "%s: %lld rows are not groups of %d", c.what, (long long)B, group);
+    const int* shared = c.none(6) ? nullptr : (const int*)c.one(6, "shared", at::kInt, B / group);
+    size_t bytes;
+    void* ws = c.ws(9, bytes);
+    return code(tp_attention_decode_kv4(in(q), in(h.p), as<void>(o), tp, len, shared, P, (int)B, group, (int)s[1], h.Hkv, (int)D,
+                                        (int)tab[1], h.page, h.pages, q.row, o.row, c.real(8), ws, bytes, c.stream(10)));
+}
+
 struct Entry {
     const char* name;
     int args;               // before the stream and the current device, which every call ends with
@@ -373,7 +555,9 @@ struct Entry {
 };
 constexpr Entry kEntries[] = {{"kv_plan", 12, plan}, {"tp_qk_norm_rope", 12, rope}, {"tp_qk_norm_rope_grad", 13, rope_grad},
                               {"tp_attention", 9, prompt}, {"tp_attention_grad", 14, prompt_grad},
-                              {"tp_attention_decode", 11, decode}};
+                              {"tp_attention_decode", 11, decode}, {"beam_select", 10, select}, {"kv_fork", 16, fork},
+                              {"kv_compact", 10, compact}, {"kv_copy_pages", 4, copy_pages}, {"tp_kv4_write", 5, kv4_write},
+                              {"tp_kv4_read", 5, kv4_read}, {"tp_attention_decode_kv4", 10, decode_kv4}};
 
 template <int I> PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
     constexpr const Entry& e = kEntries[I];
@@ -390,7 +574,8 @@ template <int I> PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 #define ENTRY(I) {kEntries[I].name, (PyCFunction)(void (*)(void))entry<I>, METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {ENTRY(0), ENTRY(1), ENTRY(2), ENTRY(3), ENTRY(4), ENTRY(5), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {ENTRY(0), ENTRY(1), ENTRY(2), ENTRY(3), ENTRY(4), ENTRY(5), ENTRY(6), ENTRY(7), ENTRY(8), ENTRY(9),
+                         ENTRY(10), ENTRY(11), ENTRY(12), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,528 @@
+// kv_pages.hip -- the pages of a paged cache: forked with the rows of a block
+// table, freed, compacted and copied.
+//
+// Which pages are in use follows from the block table alone, so no counts of
+// holders have to be kept in step with it.  With bit sets over the pages,
+//   freed = held before & ~held after,
+//   moved = in use & at or above n,  holes = free & below n   (n pages in use),
+// in order of their numbers by running sums of the sets' words.
+//
+// What has to move is small next to the latencies, so the launches and the
+// trips to memory bound it: one launch makes the sets, a wave a row, and its
+// last workgroup to finish does what needs them whole (rewriting the table of
+// kv_compact, which needs all workgroups again, is a launch of its own).  Marks
+// are device-scope atomics, which that workgroup reads at device scope; it
+// leaves them zero.  A row marks what the row above it does not hold at the
+// same place: beams of one prompt hold mostly the same pages.
+#include "attn_internal.h"
+#include "tp_search.h"
+
+#include <hip/hip_runtime.h>
+
+namespace ringc {
+namespace {
+
+constexpr int kThreads = 1024, kRowWaves = kThreads / 64;
+constexpr int kMaxBlocks = 512;
+
+__device__ __forceinline__ void mark(unsigned* set, int i) {
+    __hip_atomic_fetch_or(set + (i >> 5), 1u << (i & 31), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class T> __device__ __forceinline__ T seen(const T* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void raise_to(int* p, int x) {
+    __hip_atomic_fetch_max(p, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+// True in the launch's last workgroup to get here, once what all of them did at
+// device scope is done.
+__device__ __forceinline__ bool last_block(int* counter) {
+    __shared__ int last;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (int)gridDim.x - 1;
+    __syncthreads();
+    return last;
+}
+
+// The sum of x over the workgroup's lower threads, and over all of them.
+__device__ __forceinline__ int block_scan(int x, int& total) {
+    __shared__ int part[kRowWaves];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, s = wave_scan(x);
+    __syncthreads();
+    if (lane == 63) part[wave] = s;
+    __syncthreads();
+    int below = 0;
+    total = 0;
+#pragma unroll
+    for (int w = 0; w < kRowWaves; ++w) {
+        if (w < wave) below += part[w];
+        total += part[w];
+    }
+    return below + s - x;
+}
+
+struct ForkArgs {
+    const int *table, *lengths, *parents, *keep, *used;
+    int *free_pages, *table_after, *lengths_after, *copies, *n_copies, *shared, *used_after;
+    int B, B2, group, n_free, width, shift, pages, words;
+    Status* status;
+    WsSpan zero;
+    int *counter, *owner, *differ;       // owner[page]: B2 - its first row, differ[group]: width - the first differing entry
+    unsigned *old, *full, *part;         // pages the old rows held, those the new ones have full, and partly filled
+};
+
+struct ForkRow {
+    int parent, tokens, held, full;      // held: pages, full: of them without a free place
+    __device__ __forceinline__ bool partial() const { return held > full; }
+};
+__device__ __forceinline__ int row_tokens(int n, int width, int shift) {
+    const long long room = (long long)width << shift;
+    return n < 0 ? 0 : n < room ? n : (int)room;
+}
+__device__ __forceinline__ ForkRow fork_row(const ForkArgs& a, int i) {
+    ForkRow r;
+    r.parent = a.parents[i];
+    const bool any = r.parent >= 0 && r.parent < a.B;
+    if (!any) r.parent = 0;
+    int n = any ? row_tokens(a.lengths[r.parent], a.width, a.shift) : 0;
+    if (any && a.keep) {
+        const int k = a.keep[i];
+        n = k < 0 ? 0 : k < n ? k : n;
+    }
+    r.tokens = n;
+    r.full = n >> a.shift;
+    r.held = (int)(((long long)n + (1 << a.shift) - 1) >> a.shift);
+    return r;
+}
+__device__ __forceinline__ bool is_page(int e, int pages) { return e >= 0 && e < pages; }
+
+// The workgroup that finishes: copies are counted in row order, freed pages by
+// number, and the one handed to the other.
+__device__ __forceinline__ void finish_fork(const ForkArgs& a, int* lds) {
+    int *rank = lds, *taken = lds + a.B2, *least = lds + 2 * a.B2;      // per row: its copy or -1; per copy: a freed page; per group
+    const int tid = threadIdx.x, groups = a.B2 / (a.group ? a.group : 1);
+    const int used = *a.used;
+    __syncthreads();
+    for (int g = tid; g < groups; g += kThreads) least[g] = 0x7fffffff;
+    __syncthreads();
+    int n_copies = 0, n_freed = 0, all;
+    for (int i0 = 0; i0 < a.B2; i0 += kThreads) {
+        const int i = i0 + tid;
+        int copy = 0;
+        if (i < a.B2) {
+            const ForkRow r = fork_row(a, i);
+            __hip_atomic_fetch_min(least + i / a.group, r.tokens, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+            if (r.partial()) {
+                const int e = a.table[(long long)r.parent * a.width + r.full];
+                if (is_page(e, a.pages))
+                    copy = (seen(a.full + (e >> 5)) >> (e & 31) & 1) || seen(a.owner + e) != a.B2 - i;
+                if (copy && a.group > 1) raise_to(a.differ + i / a.group, a.width - r.full);
+            }
+        }
+        const int k = block_scan(copy, all);
+        if (i < a.B2) rank[i] = copy ? n_copies + k : -1;
+        n_copies += all;
+    }
+    auto freed = [&](int w) { return w < a.words ? seen(a.old + w) & ~seen(a.full + w) & ~seen(a.part + w) : 0u; };
+    int mine = 0;
+    for (int w = tid; w < a.words; w += kThreads) mine += __builtin_popcount(freed(w));
+    block_scan(mine, n_freed);
+    if (n_freed) {
+        int before = 0;
+        for (int w0 = 0; w0 < a.words; w0 += kThreads) {
+            unsigned bits = freed(w0 + tid);
+            int k = before + block_scan(__builtin_popcount(bits), all);
+            for (; bits; bits &= bits - 1, ++k) {
+                const int page = (w0 + tid) * 32 + __builtin_ctz(bits);
+                const long long at = (long long)used - n_freed + k;
+                if (k < n_copies) taken[k] = page;
+                else if (at >= 0 && at < a.n_free) a.free_pages[at] = page;
+            }
+            before += all;
+        }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __syncthreads();
+    for (int i = tid; i < a.B2; i += kThreads) {
+        const ForkRow r = fork_row(a, i);
+        if (r.partial()) {
+            int e = a.table[(long long)r.parent * a.width + r.full];
+            const int k = rank[i];
+            if (is_page(e, a.pages)) a.owner[e] = 0;
+            if (k >= 0) {
+                const long long at = (long long)used + k - n_freed;
+                const int to = k < n_freed ? taken[k] : at >= 0 && at < a.n_free ? a.free_pages[at] : -1;
+                a.copies[2 * k] = e;
+                a.copies[2 * k + 1] = to;
+                e = to;
+            }
+            a.table_after[(long long)i * a.width + r.full] = e;
+        }
+        if (i >= n_copies) a.copies[2 * i] = a.copies[2 * i + 1] = -1;
+    }
+    for (int g = tid; g < groups; g += kThreads) {
+        const int d = seen(a.differ + g);
+        const long long same = (long long)(a.width - d) << a.shift;
+        if (a.shared) a.shared[g] = least[g] < same ? least[g] : (int)same;
+        a.differ[g] = 0;
+    }
+    for (int w = tid; w < a.words; w += kThreads) a.old[w] = a.full[w] = a.part[w] = 0;
+    if (tid == 0) {
+        const long long after = (long long)used + n_copies - n_freed;
+        *a.used_after = after > 0x7fffffff ? 0x7fffffff : (int)after;
+        *a.n_copies = n_copies;
+        *a.counter = 0;
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void kv_fork_kernel(ForkArgs a) {
+    extern __shared__ int lds[];
+    __shared__ unsigned whole[KV_FORK_MAX_ROWS / 32];     // old rows that some new row keeps all tokens of
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const WsRecord rec = ws_record(a.status);
+    for (int w = tid; w < (a.B + 31) / 32; w += kThreads) whole[w] = 0;
+    __syncthreads();
+    for (int i = tid; i < a.B2; i += kThreads) {
+        const int p = a.parents[i];
+        if (p >= 0 && p < a.B && (!a.keep || a.keep[i] >= a.lengths[p]))
+            __hip_atomic_fetch_or(whole + (p >> 5), 1u << (p & 31), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    }
+    __syncthreads();
+    if (!ws_ok(a.status, rec, a.zero, lane)) return;
+    const int step = gridDim.x * kRowWaves;
+    for (int i = blockIdx.x * kRowWaves + wave; i < a.B2; i += step) {
+        const ForkRow r = fork_row(a, i);
+        ForkRow up = {0, 0, 0, 0};
+        if (i) up = fork_row(a, i - 1);
+        const int *row = a.table + (long long)r.parent * a.width, *above = a.table + (long long)up.parent * a.width;
+        int* to = a.table_after + (long long)i * a.width;
+        const bool grouped = a.shared && i % a.group;
+        bool differs = false;
+        for (int j0 = 0; j0 < a.width; j0 += 64) {
+            const int j = j0 + lane;
+            const int e = j < r.held ? row[j] : -1, x = j < up.held ? above[j] : -1;
+            if (j < a.width && (j >= r.held || j < r.full)) to[j] = e;
+            const bool same = j < up.held && e == x;
+            if (j < r.held && is_page(e, a.pages)) {
+                if (j >= r.full) {
+                    mark(a.part, e);
+                    raise_to(a.owner + e, a.B2 - i);
+                } else if (!(same && j < up.full)) {
+                    mark(a.full, e);
+                }
+            }
+            if (grouped && !differs) {
+                const unsigned long long other = __ballot(j < r.held && j < up.held && e != x);
+                if (other) {
+                    differs = true;
+                    if (lane == 0) raise_to(a.differ + i / a.group, a.width - (j0 + __builtin_ctzll(other)));
+                }
+            }
+        }
+        if (lane == 0) a.lengths_after[i] = r.tokens;
+    }
+    for (int b = blockIdx.x * kRowWaves + wave; b < a.B; b += step) {
+        if (whole[b >> 5] >> (b & 31) & 1) continue;
+        auto pages = [&](int n) { return (int)(((long long)row_tokens(n, a.width, a.shift) + (1 << a.shift) - 1) >> a.shift); };
+        const int held = pages(a.lengths[b]);
+        const int up_held = b ? pages(a.lengths[b - 1]) : 0;
+        const int* row = a.table + (long long)b * a.width;
+        for (int j = lane; j < held; j += 64) {
+            const int e = row[j];
+            // what the row above holds too it marks, or a new row keeps
+            const bool same = j < up_held && e == row[j - a.width];
+            if (is_page(e, a.pages) && !same) mark(a.old, e);
+        }
+    }
+    if (last_block(a.counter)) finish_fork(a, lds);
+}
+
+// ---------------------------------------------------------------- compaction
+struct CompactArgs {
+    const int *table, *lengths;
+    int *table_after, *free_pages, *copies, *n_copies, *used_after;
+    int B, n, width, shift, first, words;
+    Status* status;
+    WsSpan zero, data;
+    int* counter;
+    unsigned* live;                      // marks of the pool's pages in use
+    unsigned* in_use;                    // a copy of them for the second launch
+    int* before;                         // per word: pages in use below it, and last the ones below page n
+};
+
+__device__ __forceinline__ int held_pages(const CompactArgs& a, int b) {
+    return (int)(((long long)row_tokens(a.lengths[b], a.width, a.shift) + (1 << a.shift) - 1) >> a.shift);
+}
+
+__device__ __forceinline__ void finish_compact(const CompactArgs& a) {
+    const int tid = threadIdx.x;
+    __shared__ int below;
+    int n = 0;
+    for (int w0 = 0; w0 < a.words; w0 += kThreads) {
+        const int w = w0 + tid;
+        const unsigned bits = w < a.words ? seen(a.live + w) : 0u;
+        int all;
+        const int k = n + block_scan(__builtin_popcount(bits), all);
+        if (w < a.words) {
+            a.before[w] = k;
+            a.in_use[w] = bits;
+        }
+        n += all;
+    }
+    __syncthreads();
+    // pages in use below number n: the rest moves
+    for (int w = tid; w < a.words; w += kThreads)
+        if (w == n >> 5) below = a.before[w] + __builtin_popcount(a.in_use[w] & ((1u << (n & 31)) - 1));
+    if (tid == 0 && n >> 5 >= a.words) below = n;
+    __syncthreads();
+    const int stay = below;
+    for (int w = tid; w < a.words; w += kThreads) {
+        const unsigned bits = a.in_use[w];
+        const int k0 = a.before[w], p0 = w * 32;
+        const unsigned under = n - p0 >= 32 ? ~0u : n > p0 ? (1u << (n - p0)) - 1 : 0u;
+        int h = p0 - k0, m = k0 + __builtin_popcount(bits & under) - stay;
+        for (unsigned x = ~bits & under; x; x &= x - 1) a.copies[2 * h++ + 1] = a.first + p0 + __builtin_ctz(x);
+        for (unsigned x = bits & ~under; x; x &= x - 1) a.copies[2 * m++] = a.first + p0 + __builtin_ctz(x);
+        a.live[w] = 0;
+    }
+    if (tid == 0) {
+        a.before[a.words] = stay;
+        *a.used_after = n;
+        *a.n_copies = n - stay;
+        *a.counter = 0;
+        ws_add_data(a.status, a.data);
+    }
+}
+
+__global__ __launch_bounds__(kThreads) void kv_compact_kernel(CompactArgs a) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (!ws_ok(a.status, ws_record(a.status), a.zero, lane)) return;
+    for (int b = blockIdx.x * kRowWaves + wave; b < a.B; b += gridDim.x * kRowWaves) {
+        const int held = held_pages(a, b), up = b ? held_pages(a, b - 1) : 0;
+        const int* row = a.table + (long long)b * a.width;
+        for (int j = lane; j < held; j += 64) {
+            const long long e = (long long)row[j] - a.first;
+            if (e >= 0 && e < a.n && !(j < up && row[j - a.width] == row[j])) mark(a.live, (int)e);
+        }
+    }
+    if (last_block(a.counter)) finish_compact(a);
+}
+
+__global__ __launch_bounds__(256) void kv_renumber_kernel(CompactArgs a) {
+    // the first launch stopped: nothing here holds numbers of this call
+    if (seen(&a.status->code) != RING_OK) return;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = *a.used_after, stay = a.before[a.words], moves = n - stay;
+    const int step = gridDim.x * 256, first = blockIdx.x * 256 + threadIdx.x;
+    for (int i = first; i < a.n; i += step) a.free_pages[i] = a.first + i;
+    for (int i = first; i < a.n / 2; i += step)
+        if (i >= moves) a.copies[2 * i] = a.copies[2 * i + 1] = -1;
+    for (int b = blockIdx.x * 4 + wave; b < a.B; b += gridDim.x * 4) {
+        const int held = held_pages(a, b);
+        const int* row = a.table + (long long)b * a.width;
+        int* to = a.table_after + (long long)b * a.width;
+        for (int j = lane; j < a.width; j += 64) {
+            int e = j < held ? row[j] : -1;
+            const long long i = (long long)e - a.first;
+            if (i >= n && i < a.n) {
+                const int w = (int)i >> 5;
+                e = a.copies[2 * (a.before[w] + __builtin_popcount(a.in_use[w] & ((1u << (i & 31)) - 1)) - stay) + 1];
+            }
+            to[j] = e;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- copies
+struct CopyArgs {
+    char* cache[2 * RING_MAX_RANKS];
+    const int *copies, *n_copies;
+    int n_caches, capacity, pages, chunks, vecs, per;    // of a page: chunks of `per` 16-byte vectors, vecs in all
+};
+
+// A wave copies a chunk of a page, four 16-byte vectors a lane in flight.
+__global__ __launch_bounds__(256) void kv_copy_kernel(CopyArgs a) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int n = *a.n_copies;
+    if (n > a.capacity) n = a.capacity;
+    const unsigned each = (unsigned)(a.n_caches * a.chunks);
+    const long long items = (long long)(n < 0 ? 0 : n) * each;
+    for (long long it = blockIdx.x * 4 + wave; it < items; it += (long long)gridDim.x * 4) {
+        const int i = (int)(it / each), rest = (int)(it % each), c = rest / a.chunks, k = rest % a.chunks;
+        const int from = a.copies[2 * i], to = a.copies[2 * i + 1];
+        if (!is_page(from, a.pages) || !is_page(to, a.pages) || from == to) continue;
+        const u32x4* src = (const u32x4*)a.cache[c] + (long long)from * a.vecs;
+        u32x4* dst = (u32x4*)a.cache[c] + (long long)to * a.vecs;
+        const int v0 = k * a.per, v1 = v0 + a.per < a.vecs ? v0 + a.per : a.vecs;
+        for (int v = v0 + lane; v < v1; v += 256) {
+            u32x4 x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (v + 64 * u < v1) x[u] = src[v + 64 * u];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (v + 64 * u < v1) dst[v + 64 * u] = x[u];
+        }
+    }
+}
+
+int shift_of(int page_size) {
+    int s = 0;
+    while ((1 << s) < page_size) ++s;
+    return s;
+}
+bool page_size_ok(int page_size) { return page_size >= 1 && !(page_size & (page_size - 1)) && page_size <= (1 << 20); }
+bool misaligned4(const void* p) { return (uintptr_t)p & 3; }
+
+size_t fork_words(int pages) { return ((size_t)pages + 31) / 32; }
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+
+int row_blocks(int rows) {
+    const int n = (rows + kRowWaves - 1) / kRowWaves;
+    return n < 1 ? 1 : n < kMaxBlocks ? n : kMaxBlocks;
+}
+
+}  // namespace
+}  // namespace ringc
+
+using namespace ringc;
+
+extern "C" size_t kv_fork_workspace_bytes(int B_after, int pages) {
+    if (B_after < 0 || B_after > KV_FORK_MAX_ROWS || pages < 0) return 0;
+    return kStatusBytes + up256((64 + 3 * fork_words(pages) + (size_t)pages + (size_t)B_after) * 4);
+}
+
+extern "C" int kv_fork(const int* block_table, const int* lengths, const int* parents, const int* keep, int* free_pages,
+                       const int* used, int* table_after, int* lengths_after, int* copies, int* n_copies, int* shared,
+                       int* used_after, int B, int B_after, int group, int n_free, int table_stride, int page_size, int pages,
+                       void* ws, size_t ws_bytes, void* stream) {
+    if (B < 0 || B_after < 0 || n_free < 0 || table_stride < 0 || pages < 0 || group < 1 || B_after % group) return RING_EINVAL;
+    if (!page_size_ok(page_size)) return RING_EINVAL;
+    if (B > KV_FORK_MAX_ROWS || B_after > KV_FORK_MAX_ROWS || (long long)table_stride * page_size >= (1LL << 31))
+        return RING_EUNSUPPORTED;
+    if (!used || !used_after || !n_copies || (B && !lengths) || (B && table_stride && !block_table) || (n_free && !free_pages) ||
+        (B_after && (!parents || !lengths_after || !copies)) || (B_after && table_stride && !table_after))
+        return RING_EINVAL;
+    for (const void* p : {(const void*)block_table, (const void*)lengths, (const void*)parents, (const void*)keep,
+                          (const void*)free_pages, (const void*)used, (const void*)table_after, (const void*)lengths_after,
+                          (const void*)copies, (const void*)n_copies, (const void*)shared, (const void*)used_after})
+        if (misaligned4(p)) return RING_EINVAL;
+    if (used_after == used || (B_after && (lengths_after == lengths || (table_stride && table_after == block_table))))
+        return RING_EINVAL;
+    const size_t need = kv_fork_workspace_bytes(B_after, pages);
+    if (!ws || ((uintptr_t)ws & 255) || ws_bytes < need) return RING_EWORKSPACE;
+    ForkArgs a;
+    a.table = block_table;
+    a.lengths = lengths;
+    a.parents = parents;
+    a.keep = keep;
+    a.used = used;
+    a.free_pages = free_pages;
+    a.table_after = table_after;
+    a.lengths_after = lengths_after;
+    a.copies = copies;
+    a.n_copies = n_copies;
+    a.shared = shared;
+    a.used_after = used_after;
+    a.B = B;
+    a.B2 = B_after;
+    a.group = group;
+    a.n_free = n_free;
+    a.width = table_stride;
+    a.shift = shift_of(page_size);
+    a.pages = pages;
+    a.words = (int)fork_words(pages);
+    a.status = (Status*)ws;
+    a.zero = WsSpan{kStatusBytes, need};
+    a.counter = (int*)((char*)ws + kStatusBytes);
+    a.old = (unsigned*)a.counter + 64;
+    a.full = a.old + a.words;
+    a.part = a.full + a.words;
+    a.owner = (int*)a.part + a.words;
+    a.differ = a.owner + pages;
+    hipLaunchKernelGGL(kv_fork_kernel, dim3((unsigned)row_blocks(B > B_after ? B : B_after)), dim3(kThreads),
+                       3 * (size_t)B_after * sizeof(int), (hipStream_t)stream, a);
+    return hipGetLastError() == hipSuccess ? RING_OK : RING_EHIP;
+}
+
+extern "C" size_t kv_compact_workspace_bytes(int n_free) {
+    if (n_free < 0) return 0;
+    const size_t words = fork_words(n_free);
+    return kStatusBytes + up256((64 + words) * 4) + up256((2 * words + 1) * 4);
+}
+
+extern "C" int kv_compact(const int* block_table, const int* lengths, int* table_after, int* free_pages, int* copies,
+                          int* n_copies, int* used_after, int B, int n_free, int table_stride, int page_size, int first_page,
+                          void* ws, size_t ws_bytes, void* stream) {
+    if (B < 0 || n_free < 0 || table_stride < 0 || first_page < 0 || !page_size_ok(page_size)) return RING_EINVAL;
+    if (B > KV_FORK_MAX_ROWS || (long long)table_stride * page_size >= (1LL << 31) || (long long)first_page + n_free >= (1LL << 31))
+        return RING_EUNSUPPORTED;
+    if (!used_after || !n_copies || (B && !lengths) || (B && table_stride && (!block_table || !table_after)) ||
+        (n_free && !free_pages) || (n_free > 1 && !copies))
+        return RING_EINVAL;
+    for (const void* p : {(const void*)block_table, (const void*)lengths, (const void*)table_after, (const void*)free_pages,
+                          (const void*)copies, (const void*)n_copies, (const void*)used_after})
+        if (misaligned4(p)) return RING_EINVAL;
+    if (B && table_stride && table_after == block_table) return RING_EINVAL;
+    const size_t need = kv_compact_workspace_bytes(n_free);
+    if (!ws || ((uintptr_t)ws & 255) || ws_bytes < need) return RING_EWORKSPACE;
+    CompactArgs a;
+    a.table = block_table;
+    a.lengths = lengths;
+    a.table_after = table_after;
+    a.free_pages = free_pages;
+    a.copies = copies;
+    a.n_copies = n_copies;
+    a.used_after = used_after;
+    a.B = B;
+    a.n = n_free;
+    a.width = table_stride;
+    a.shift = shift_of(page_size);
+    a.first = first_page;
+    a.words = (int)fork_words(n_free);
+    a.status = (Status*)ws;
+    const size_t data = kStatusBytes + up256((64 + (size_t)a.words) * 4);
+    a.zero = WsSpan{kStatusBytes, data};
+    a.data = WsSpan{data, need};
+    a.counter = (int*)((char*)ws + kStatusBytes);
+    a.live = (unsigned*)a.counter + 64;
+    a.in_use = (unsigned*)((char*)ws + data);
+    a.before = (int*)a.in_use + a.words;
+    hipLaunchKernelGGL(kv_compact_kernel, dim3((unsigned)row_blocks(B)), dim3(kThreads), 0, (hipStream_t)stream, a);
+    if (hipGetLastError() != hipSuccess) return RING_EHIP;
+    const int work = (n_free + 255) / 256 > (B + 3) / 4 ? (n_free + 255) / 256 : (B + 3) / 4;
+    const int blocks = work < 1 ? 1 : work < 4 * kMaxBlocks ? work : 4 * kMaxBlocks;
+    hipLaunchKernelGGL(kv_renumber_kernel, dim3((unsigned)blocks), dim3(256), 0, (hipStream_t)stream, a);
+    return hipGetLastError() == hipSuccess ? RING_OK : RING_EHIP;
+}
+
+extern "C" int kv_copy_pages(void* const* caches, const int* copies, const int* n_copies, int n_caches, int capacity,
+                             int pages, long long page_bytes, void* stream) {
+    if (n_caches < 1 || n_caches > 2 * RING_MAX_RANKS || capacity < 0 || pages < 0 || page_bytes < 0 || page_bytes % 16)
+        return RING_EINVAL;
+    if (page_bytes >= (1LL << 31)) return RING_EUNSUPPORTED;
+    if (!caches || !n_copies || misaligned4(n_copies) || (capacity && !copies) || misaligned4(copies)) return RING_EINVAL;
+    if (!capacity || !pages || !page_bytes) return RING_OK;
+    CopyArgs a;
+    for (int c = 0; c < n_caches; ++c) {
+        if (!caches[c] || ((uintptr_t)caches[c] & 15)) return RING_EINVAL;
+        a.cache[c] = (char*)caches[c];
+    }
+    a.copies = copies;
+    a.n_copies = n_copies;
+    a.n_caches = n_caches;
+    a.capacity = capacity;
+    a.pages = pages;
+    a.vecs = (int)(page_bytes / 16);
+    a.chunks = (a.vecs + 255) / 256;
+    a.per = ((a.vecs + a.chunks - 1) / a.chunks + 63) / 64 * 64;
+    a.chunks = (a.vecs + a.per - 1) / a.per;
+    if ((long long)n_caches * a.chunks >= (1LL << 31)) return RING_EUNSUPPORTED;
+    const long long items = ((long long)capacity * n_caches * a.chunks + 3) / 4;
+    const long long most = 8LL * dev_info().cus;
+    hipLaunchKernelGGL(kv_copy_kernel, dim3((unsigned)(items < most ? items : most)), dim3(256), 0, (hipStream_t)stream, a);
+    return hipGetLastError() == hipSuccess ? RING_OK : RING_EHIP;
+}
