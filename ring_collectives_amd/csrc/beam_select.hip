@@ -2,15 +2,19 @@
 //
 // With m = max x and s = sum 2^((x - m) log2 e) over a row's logits,
 //   lp = x - (m + ln s),
-// and a group's best are among each row's `keep` largest logits: within a row
-// lp orders as x does.  One pass over the logits gives m, s and those:
-//   - a wave takes a part of a row's columns of one rank; every lane keeps a
-//     running maximum and sum of its own, and the wave a list of its largest
-//     values, the i-th in lane i.  A value that exceeds the list's last is put
-//     in; after the first few hundred columns few do.
+// and within a row lp orders as x does.  One pass over the logits gives m, s and
+// where a row's largest logits lie:
+//   - a wave takes a part of a row's columns of one rank, 1024 a step; every
+//     lane keeps a running maximum and sum of its own, and the wave a list of
+//     its `keep` largest lane maxima of a step, the i-th in lane i: the part's
+//     `keep` largest logits are among the 16 values each that those are the
+//     maxima of.  After the first steps few maxima exceed the list's last.
 //   - a second launch, a workgroup a group, joins each row's parts to ln s in
-//     64 bits and takes the group's best off the heads of the parts' lists, one
-//     after the other.
+//     64 bits, takes the group's `keep` best maxima off the heads of the parts'
+//     lists, reads their values again (some 64 bytes each), and puts those that
+//     are no worse than the last maximum in order.
+// (Lists of values instead of maxima took a wave 144 operations where one is
+// put in, 25 so: of 512 rows of 100003 logits two thirds of all operations.)
 // The logits read bound it: an exponential is a sixteenth of the rate of a
 // plain operation, four exponentials a cycle and SIMD.
 //
@@ -27,7 +31,9 @@ namespace ringc {
 namespace {
 
 constexpr int kChunk = 1024;           // columns of a wave's step, 16 a lane
-constexpr int kMaxLists = 4096;        // of a group
+constexpr int kLists = 64;             // of a group, unless there are more rows and ranks
+constexpr int kMaxLists = BEAM_SELECT_MAX * RING_MAX_RANKS;
+constexpr int kLdsEntries = 4096;      // of all lists of a group, kept in LDS
 
 struct BeamArgs {
     const void* logits[RING_MAX_RANKS];
@@ -41,7 +47,7 @@ struct BeamArgs {
     Status* status;
     WsSpan data;
     float2* ms;                        // [row][rank][part] m, s
-    float2* list;                      // [row][rank][part][K] value and (bits of) column
+    float2* list;                      // [row][rank][part][K] maximum and (bits of) its step and lane
 };
 
 // (by value: of a vector's element itself, __builtin_bit_cast takes element 0)
@@ -54,26 +60,48 @@ __device__ __forceinline__ float exp2_of(float d) {            // 2^(d log2 e)
     return exp2_hw(__builtin_fmaf(d, hi, d * lo));
 }
 
-// The wave's maximum; its least integer.
+// A wave's maximum, and its least number, in every lane: four steps within rows
+// of 16 lanes and two across them on the VALU, then the last lane's.  (Through
+// LDS, six exchanges, a value put into a list took 0.9 us.)
+template <class Op> __device__ __forceinline__ int wave_reduce(int x, Op op) {
+    x = op(x, __builtin_amdgcn_update_dpp(x, x, 0x111, 0xf, 0xf, false));
+    x = op(x, __builtin_amdgcn_update_dpp(x, x, 0x112, 0xf, 0xf, false));
+    x = op(x, __builtin_amdgcn_update_dpp(x, x, 0x114, 0xf, 0xf, false));
+    x = op(x, __builtin_amdgcn_update_dpp(x, x, 0x118, 0xf, 0xf, false));
+    x = op(x, __builtin_amdgcn_update_dpp(x, x, 0x142, 0xa, 0xf, false));
+    x = op(x, __builtin_amdgcn_update_dpp(x, x, 0x143, 0xc, 0xf, false));
+    return __builtin_amdgcn_readlane(x, 63);
+}
+__device__ __forceinline__ float as_float(int x) { return __builtin_bit_cast(float, x); }
+__device__ __forceinline__ int as_bits(float x) { return __builtin_bit_cast(int, x); }
 __device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) x = fmaxf(x, __shfl_xor(x, d));
-    return x;
+    return as_float(wave_reduce(as_bits(x), [](int a, int b) { return as_bits(fmaxf(as_float(a), as_float(b))); }));
 }
 __device__ __forceinline__ int wave_min(int x) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        const int y = __shfl_xor(x, d);
-        x = x < y ? x : y;
-    }
-    return x;
+    return wave_reduce(x, [](int a, int b) { return a < b ? a : b; });
 }
+__device__ __forceinline__ unsigned wave_umax(unsigned x) {
+    return (unsigned)wave_reduce((int)x, [](int a, int b) { return (unsigned)a > (unsigned)b ? a : b; });
+}
+// The value one lane below (lane 0 keeps its own).
+__device__ __forceinline__ int lane_below(int x) { return __builtin_amdgcn_update_dpp(x, x, 0x138, 0xf, 0xf, false); }
+
+// Where in a wave's step a value lies: column of lane and element, and the lane of a column.
+template <bool F32> struct Step {
+    static constexpr int V = F32 ? 4 : 8;                  // values of a 16-byte vector
+    static __device__ __forceinline__ int column(int lane, int e) { return (e / V * 64 + lane) * V + e % V; }
+    static __device__ __forceinline__ int lane(int column) { return column / V % 64; }
+};
 
 template <bool F32> __global__ __launch_bounds__(256) void beam_scan_kernel(BeamArgs a, unsigned works) {
-    const unsigned w = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    typedef Step<F32> At;
+    __shared__ float reached[4];               // the last value of each wave's list
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    if (lane == 0) reached[wave] = -INFINITY;
+    __syncthreads();
+    const unsigned w = blockIdx.x * 4 + wave;
     if (blockIdx.x == 0 && threadIdx.x == 0) ws_add_data(a.status, a.data);
     if (w >= works) return;
-    const int lane = threadIdx.x & 63;
     const int part = (int)(w % (unsigned)a.parts), rank = (int)(w / (unsigned)a.parts % (unsigned)a.P);
     const int row = (int)(w / (unsigned)a.parts / (unsigned)a.P);
     if ((a.done && a.done[row]) || !(__builtin_fabsf(a.scores[row]) < INFINITY)) return;
@@ -85,11 +113,14 @@ template <bool F32> __global__ __launch_bounds__(256) void beam_scan_kernel(Beam
     // a view holds whole words: the last of an odd number of bf16 values is loaded by itself
     const bool odd = !F32 && (cols & 1);
     const rsrc_t view = tile_view(base, (long long)(odd ? cols - 1 : cols) * E);
-    const float tail = odd ? only_finite(bf16_bits(((const unsigned short*)base)[cols - 1])) : 0.0f;
+    const float tail = odd ? bf16_bits(((const unsigned short*)base)[cols - 1]) : 0.0f;
+    // the workgroup's waves that have the same row
+    const unsigned each = (unsigned)a.parts * a.P;
+    const int v0 = (int)(blockIdx.x * 4 >= row * each ? 0 : row * each - blockIdx.x * 4);
+    const int v1 = (int)((row + 1) * each - blockIdx.x * 4 < 4 ? (row + 1) * each - blockIdx.x * 4 : 4);
     float m = -INFINITY, s = 0.0f;             // this lane's
-    float best = -INFINITY, last = -INFINITY;  // the list: lane i's value, and the K-th
-    int at = -1;                               // its column
-    auto column = [&](int e) { return F32 ? (e / 4 * 64 + lane) * 4 + e % 4 : (e / 8 * 64 + lane) * 8 + e % 8; };
+    float best = -INFINITY, last = -INFINITY;  // the list: lane i's maximum, and the K-th
+    int at = -1;                               // the step and lane it is the maximum of
     auto load = [&](int c, u32x4 (&r)[E]) {
 #pragma unroll
         for (int v = 0; v < E; ++v) r[v] = ld16<POL_NT>(view, (unsigned)(c * E + (v * 64 + lane) * 16));
@@ -102,56 +133,72 @@ template <bool F32> __global__ __launch_bounds__(256) void beam_scan_kernel(Beam
         for (int e = 0; e < 16; ++e) {
             if (F32) x[e] = f32_bits(raw[e / 4][e % 4]);
             else x[e] = bf16_bits(e % 2 ? raw[(e / 8) % E][e % 8 / 2] >> 16 : raw[(e / 8) % E][e % 8 / 2] & 0xffffu);
-            x[e] = only_finite(x[e]);
         }
         if (c + kChunk < c1) load(c + kChunk, raw);
         if (c + kChunk > c1) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e)
-                if (c + column(e) >= c1) x[e] = -INFINITY;
-                else if (odd && c + column(e) == cols - 1) x[e] = tail;
+            for (int e = 0; e < 16; ++e) {
+                const int col = c + At::column(lane, e);
+                if (col >= c1) x[e] = -INFINITY;
+                else if (odd && col == cols - 1) x[e] = tail;
+            }
         }
-        float top = x[0];
+        float top, mn, sum;
+        auto weigh = [&]() __attribute__((always_inline)) {
+            top = x[0];
 #pragma unroll
-        for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
-        const float mn = fmaxf(m, top);
-        if (mn > -INFINITY) {
+            for (int e = 1; e < 16; ++e) top = fmaxf(top, x[e]);
+            mn = fmaxf(m, top);
+            const float sub = mn == -INFINITY ? 0.0f : mn;
             float y[16];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) y[e] = exp2_of(x[e] - mn);
+            for (int e = 0; e < 16; ++e) y[e] = exp2_of(x[e] - sub);
 #pragma unroll
             for (int d = 8; d; d /= 2)
 #pragma unroll
                 for (int e = 0; e < d; ++e) y[e] += y[e + d];
-            s = s * exp2_of(m - mn) + y[0];
-            m = mn;
-        }
-        while (__any(top > last)) {
-            const float v = wave_max(top);
-            int col = 0x7fffffff;
+            sum = s * exp2_of(m - sub) + y[0];
+        };
+        weigh();
+        // NaN and infinity make NaN of the sum: once more without them
+        if (__any(!(sum < INFINITY))) {
 #pragma unroll
-            for (int e = 15; e >= 0; --e)
-                if (x[e] == v) col = c + column(e);
-            const int first = wave_min(col);
+            for (int e = 0; e < 16; ++e) x[e] = only_finite(x[e]);
+            weigh();
+        }
+        s = sum;
+        m = mn;
+        float others = -INFINITY;
+        for (int v = v0; v < v1; ++v) others = fmaxf(others, ((volatile float*)reached)[v]);
+        bool put = false;
+        while (__any(top > last && top >= others)) {
+            // (what the row's other waves have K of can only tie)
+            const float v = wave_max(top);
+            const unsigned long long has = __ballot(top == v);
+            int owner = __builtin_ctzll(has);
+            if (has & (has - 1)) {                         // several lanes: the lowest column
+                int col = 0x7fffffff;
+#pragma unroll
+                for (int e = 15; e >= 0; --e)
+                    if (x[e] == v) col = At::column(lane, e);
+                owner = At::lane(wave_min(top == v ? col : 0x7fffffff));
+            }
             const int pos = __builtin_popcountll(__ballot(lane < a.K && at >= 0 && best >= v));
-            const float b1 = __shfl_up(best, 1);
-            const int a1 = __shfl_up(at, 1);
+            const float b1 = as_float(lane_below(as_bits(best)));
+            const int a1 = lane_below(at);
             if (lane > pos) {
                 best = b1;
                 at = a1;
             }
             if (lane == pos) {
                 best = v;
-                at = first;
+                at = c / kChunk * 64 + owner;
             }
-            last = __shfl(best, a.K - 1);
-            top = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                if (c + column(e) == first) x[e] = -INFINITY;
-                top = fmaxf(top, x[e]);
-            }
+            last = as_float(__builtin_amdgcn_readlane(as_bits(best), a.K - 1));
+            put = true;
+            if (lane == owner) top = -INFINITY;
         }
+        if (put && lane == 0) ((volatile float*)reached)[wave] = last;
     }
     const float mw = wave_max(m);
     float sw = m > -INFINITY ? s * exp2_of(m - mw) : 0.0f;
@@ -161,105 +208,228 @@ template <bool F32> __global__ __launch_bounds__(256) void beam_scan_kernel(Beam
     if (lane < a.K) a.list[(long long)w * a.K + lane] = float2{best, __builtin_bit_cast(float, at)};
 }
 
-// A candidate: its score, and its place among equals.
-struct Cand {
-    double score;
-    long long place;                   // beam * vocab + token; none: score -inf
-    __device__ __forceinline__ bool beats(const Cand& o) const { return score > o.score || (score == o.score && place < o.place); }
-};
-__device__ __forceinline__ Cand wave_best(Cand c) {
-#pragma unroll
-    for (int d = 1; d < 64; d *= 2) {
-        Cand o;
-        o.score = __shfl_xor(c.score, d);
-        o.place = __shfl_xor(c.place, d);
-        if (o.beats(c)) c = o;
-    }
-    return c;
+// Scores as numbers that order as they do; 0: none.
+__device__ __forceinline__ unsigned long long order_of(double x) {
+    const unsigned long long u = __builtin_bit_cast(unsigned long long, x);
+    return u >> 63 ? ~u : u | 1ull << 63;
 }
+__device__ __forceinline__ double score_of(unsigned long long u) {
+    return __builtin_bit_cast(double, u >> 63 ? u & ~(1ull << 63) : ~u);
+}
+struct Cand {
+    unsigned long long score;
+    int beam, token;
+};
 
-__global__ __launch_bounds__(256) void beam_join_kernel(BeamArgs a) {
+template <bool F32> __global__ __launch_bounds__(1024) void beam_join_kernel(BeamArgs a, int in_lds) {
+    typedef Step<F32> At;
+    constexpr int E = F32 ? 4 : 2, V = At::V;
+    extern __shared__ unsigned long long keys[];           // [lists][K] scores, where they fit, and their steps and lanes
     __shared__ double lse[BEAM_SELECT_MAX], score[BEAM_SELECT_MAX];
-    __shared__ unsigned char head[kMaxLists];              // entries of a list that are taken
+    __shared__ unsigned char head[kMaxLists], ended[BEAM_SELECT_MAX];      // entries of a list that are taken; done
+    __shared__ int2 group[BEAM_SELECT_MAX];                // the best maxima: list and entry
+    __shared__ Cand cand[16 * BEAM_SELECT_MAX];
+    __shared__ unsigned long long least;                   // the last of the best maxima
+    __shared__ int count;
     const int n = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int per = a.P * a.parts, lists = a.W * per;
-    for (int i = tid; i < lists; i += 256) head[i] = 0;
-    for (int w = wave; w < a.W; w += 4) {
+    const int per = a.P * a.parts, lists = a.W * per, waves = blockDim.x / 64;
+    const float2* from = a.list + (long long)n * lists * a.K;
+    // the first loads of each kind in one trip
+    const int row0 = n * a.W + (wave < a.W ? wave : 0);
+    const float sc0 = a.scores[row0];
+    const bool done0 = a.done && a.done[row0];
+    const float2 first = lane < per ? a.ms[(long long)row0 * per + lane] : float2{-INFINITY, 0.0f};
+    int* places = (int*)(keys + lists * a.K);
+    constexpr int kEarly = 4;
+    float2 early[kEarly];
+#pragma unroll
+    for (int u = 0; u < kEarly; ++u)
+        if (in_lds && tid + u * (int)blockDim.x < lists * a.K) early[u] = from[tid + u * blockDim.x];
+    for (int i = tid; i < lists; i += blockDim.x) head[i] = 0;
+    for (int i = tid; i < a.K; i += blockDim.x) group[i] = int2{-1, 0};
+    if (tid == 0) count = 0;
+    for (int w = wave; w < a.W; w += waves) {
         const int row = n * a.W + w;
-        const float sc = a.scores[row];
-        const bool live = __builtin_fabsf(sc) < INFINITY, done = a.done && a.done[row];
+        const float sc = w == wave ? sc0 : a.scores[row];
+        const float2* p = a.ms + (long long)row * per;
+        const float2 p0 = w == wave ? first : lane < per ? p[lane] : float2{-INFINITY, 0.0f};
+        const bool live = __builtin_fabsf(sc) < INFINITY, done = w == wave ? done0 : a.done && a.done[row];
         double l = 0.0;
         if (live && !done) {
-            const float2* p = a.ms + (long long)row * per;
-            float m = -INFINITY;
-            for (int i = lane; i < per; i += 64) m = fmaxf(m, p[i].x);
+            float m = p0.x;
+            for (int i = lane + 64; i < per; i += 64) m = fmaxf(m, p[i].x);
             m = wave_max(m);
-            double s = 0.0;
-            for (int i = lane; i < per; i += 64)
-                if (p[i].x > -INFINITY) s += (double)p[i].y * exp((double)p[i].x - (double)m);
-#pragma unroll
-            for (int d = 1; d < 64; d *= 2) s += __shfl_xor(s, d);
+            double s = p0.x > -INFINITY ? (double)p0.y * exp2_of(p0.x - m) : 0.0;
+            for (int i = lane + 64; i < per; i += 64)
+                if (p[i].x > -INFINITY) s += (double)p[i].y * exp2_of(p[i].x - m);
+            for (int d = 1; d < per && d < 64; d *= 2) s += __shfl_xor(s, d);
             l = (double)m + log(s);
         }
         if (lane == 0) {
             lse[w] = l;
             score[w] = live ? (double)sc : -INFINITY;
+            ended[w] = done;
         }
     }
     __syncthreads();
-    if (wave) return;
-    // the best head of this lane's lists
-    auto look = [&]() {
-        Cand c = {-INFINITY, 0x7fffffffffffffffLL};
-        for (int i = lane; i < lists; i += 64) {
-            const int w = i / per, row = n * a.W + w;
-            if (!(score[w] > -INFINITY)) continue;
-            Cand x = {-INFINITY, 0x7fffffffffffffffLL};
-            if (a.done && a.done[row]) {
-                if (i % per == 0 && !head[i]) x = Cand{score[w], (long long)w * a.vocab + a.end};
-            } else if (head[i] < a.K) {
-                const float2 e = a.list[((long long)row * per + i % per) * a.K + head[i]];
-                const int at = __builtin_bit_cast(int, e.y);
-                if (at >= 0) x = Cand{score[w] + ((double)e.x - lse[w]), (long long)w * a.vocab + i % per / a.parts * a.width + at};
+    // the score of list i's entry e (its h-th), 0 where there is none
+    auto key = [&](int i, int h, float2 e) -> unsigned long long {
+        const int w = (int)((unsigned)i / (unsigned)per);
+        if (!(score[w] > -INFINITY)) return 0;
+        if (ended[w]) return i == w * per && !h ? order_of(score[w]) : 0;
+        return as_bits(e.y) < 0 ? 0 : order_of(score[w] + ((double)e.x - lse[w]));
+    };
+    if (in_lds) {
+#pragma unroll
+        for (int u = 0; u < kEarly; ++u) {
+            const int j = tid + u * blockDim.x;
+            if (j < lists * a.K) {
+                keys[j] = key(j / a.K, j % a.K, early[u]);
+                places[j] = as_bits(early[u].y);
             }
-            if (x.beats(c)) c = x;
         }
-        return c;
-    };
-    auto list_of = [&](long long place) {                  // the list a candidate came from
-        const int w = (int)(place / a.vocab), t = (int)(place % a.vocab);
-        if (a.done && a.done[n * a.W + w]) return w * per;
-        return w * per + t / a.width * a.parts + t % a.width / a.part_cols;
-    };
-    Cand mine = look();
-    for (int k = 0; k < a.K; ++k) {
-        const Cand c = wave_best(mine);
-        const bool any = c.score > -INFINITY;
-        const int w = any ? (int)(c.place / a.vocab) : 0, t = any ? (int)(c.place % a.vocab) : -1;
-        if (lane == 0) {
-            const long long o = (long long)n * a.K + k;
-            a.parents[o] = any ? n * a.W + w : -1;
-            a.tokens[o] = t;
-            a.after[o] = any ? (float)c.score : -INFINITY;
-            if (a.done_after) a.done_after[o] = any && (a.done[n * a.W + w] || t == a.end);
+        for (int j = tid + kEarly * blockDim.x; j < lists * a.K; j += blockDim.x) {
+            const float2 e = from[j];
+            keys[j] = key(j / a.K, j % a.K, e);
+            places[j] = as_bits(e.y);
         }
-        if (any && mine.place == c.place) {
-            ++head[list_of(c.place)];
-            mine = look();
+        __syncthreads();
+    }
+    if (wave == 0) {
+        // The wave's best head by the score's halves, of equals the first list's:
+        // lists are in the order of beams and columns.
+        unsigned long long top = 0, u = 0;
+        int list = lane;
+        auto best = [&](int& owner) {
+            const unsigned hi = wave_umax((unsigned)(top >> 32));
+            const unsigned lo = wave_umax((unsigned)(top >> 32) == hi ? (unsigned)top : 0u);
+            u = (unsigned long long)hi << 32 | lo;
+            const unsigned long long tie = __ballot(top == u);
+            owner = __builtin_ctzll(tie);
+            return tie;
+        };
+        int owner;
+        if (in_lds && lists <= 64) {
+            // a list a lane, its next score at hand (a look at LDS in every
+            // round took it from 350 to 1300 cycles)
+            const unsigned long long* mine = keys + (lane < lists ? lane : 0) * a.K;
+            int h = 0;
+            if (lane < lists) top = mine[0];
+            unsigned long long next = lane < lists && a.K > 1 ? mine[1] : 0;
+            for (int k = 0; k < a.K; ++k) {
+                best(owner);
+                if (!u) break;
+                if (lane == owner) {
+                    group[k] = int2{lane, h};
+                    top = next;
+                    ++h;
+                    next = h + 1 < a.K ? mine[h + 1] : 0;
+                }
+            }
+        } else {
+            auto look = [&]() {
+                top = 0;
+                list = 0;
+                for (int i = lane; i < lists; i += 64) {
+                    const int h = head[i];
+                    if (h >= a.K) continue;
+                    const unsigned long long x = in_lds ? keys[i * a.K + h] : key(i, h, from[i * a.K + h]);
+                    if (x > top) {
+                        top = x;
+                        list = i;
+                    }
+                }
+            };
+            look();
+            for (int k = 0; k < a.K; ++k) {
+                const unsigned long long tie = best(owner);
+                if (!u) break;
+                if (tie & (tie - 1)) owner = wave_min(top == u ? list : 0x7fffffff) & 63;
+                if (lane == owner) {
+                    group[k] = int2{list, head[list]++};
+                    look();
+                }
+            }
+        }
+        if (lane == 0) least = u;
+    }
+    __syncthreads();
+    // the values that those are the maxima of, as far as they can be among the best
+    auto put = [&](unsigned long long u, int w, int token) {
+        cand[__hip_atomic_fetch_add(&count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)] = Cand{u, w, token};
+    };
+    for (int t = tid; t < a.K * E; t += blockDim.x) {
+        int2 g = group[t / E];
+        if (g.x < 0) continue;
+        g.y = in_lds ? places[g.x * a.K + g.y] : as_bits(from[g.x * a.K + g.y].y);
+        const int w = (int)((unsigned)g.x / (unsigned)per), row = n * a.W + w;
+        if (ended[w]) {
+            if (t % E == 0) put(order_of(score[w]), w, a.end);
+            continue;
+        }
+        const int rank = (int)((unsigned)(g.x - w * per) / (unsigned)a.parts), c = g.y / 64 * kChunk + At::column(g.y % 64, t % E * V);
+        const long long left = (long long)a.vocab - (long long)rank * a.width;
+        const int cols = left < a.width ? (int)left : a.width;
+        const char* p = (const char*)a.logits[rank] + ((long long)row * a.stride + c) * (F32 ? 4 : 2);
+        unsigned x[4] = {0, 0, 0, 0};
+        if (c + V <= cols) {
+            const u32x4 y = *(const u32x4*)p;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) x[v] = y[v];
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (c + e < cols) {
+                    if (F32) x[e % 4] = *(const unsigned*)(p + 4 * e);
+                    else x[e / 2 % 4] |= (unsigned)*(const unsigned short*)(p + 2 * e) << (e % 2 * 16);
+                }
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+            const float f = F32 ? f32_bits(x[e % 4]) : bf16_bits(e % 2 ? x[e / 2 % 4] >> 16 : x[e / 2 % 4] & 0xffffu);
+            if (c + e >= cols || !(__builtin_fabsf(f) < INFINITY)) continue;
+            const unsigned long long u = order_of(score[w] + ((double)f - lse[w]));
+            if (u >= least) put(u, w, rank * a.width + c + e);
         }
     }
+    __syncthreads();
+    // each one's place is the number of those that beat it
+    const int all = count;
+    for (int i = tid; i < all; i += blockDim.x) {
+        const Cand c = cand[i];
+        int k = 0;
+#pragma unroll 4
+        for (int j = 0; j < all; ++j) {
+            const Cand o = cand[j];
+            k += o.score > c.score || (o.score == c.score && (o.beam < c.beam || (o.beam == c.beam && o.token < c.token)));
+        }
+        if (k < a.K) {
+            const long long o = (long long)n * a.K + k;
+            a.parents[o] = n * a.W + c.beam;
+            a.tokens[o] = c.token;
+            a.after[o] = (float)score_of(c.score);
+            if (a.done_after) a.done_after[o] = ended[c.beam] || c.token == a.end;
+        }
+    }
+    for (int k = tid; k < a.K; k += blockDim.x)
+        if (k >= all) {
+            const long long o = (long long)n * a.K + k;
+            a.parents[o] = a.tokens[o] = -1;
+            a.after[o] = -INFINITY;
+            if (a.done_after) a.done_after[o] = 0;
+        }
 }
 
 // Parts of a row of one rank: as many as give every SIMD four waves, as far as
-// a part keeps two steps and a group's lists are few enough.
+// there are steps, and a group's lists are few enough.
 struct BeamCut {
     int parts, cols;
 };
 BeamCut beam_cut(int P, int N, int beams, int width, int cus) {
     const long long rows = (long long)N * beams * P, steps = ((long long)width + kChunk - 1) / kChunk;
     long long n = rows ? (16LL * cus + rows - 1) / rows : 1;
-    if (n > steps / 2) n = steps / 2;
-    if (n > kMaxLists / (beams * P)) n = kMaxLists / (beams * P);
+    if (n > steps) n = steps;
+    if (n > kLists / (beams * P)) n = kLists / (beams * P);
     if (n < 1) n = 1;
     const long long cols = (steps + n - 1) / n * kChunk;
     BeamCut c;
@@ -332,6 +502,10 @@ extern "C" int beam_select(const void* const* logits, const float* scores, const
     if (dtype == RING_F32) hipLaunchKernelGGL(beam_scan_kernel<true>, grid, dim3(256), 0, s, a, (unsigned)lists);
     else hipLaunchKernelGGL(beam_scan_kernel<false>, grid, dim3(256), 0, s, a, (unsigned)lists);
     if (hipGetLastError() != hipSuccess) return RING_EHIP;
-    hipLaunchKernelGGL(beam_join_kernel, dim3((unsigned)N), dim3(256), 0, s, a);
+    const int entries = beams * P * c.parts * keep, in_lds = entries <= kLdsEntries;
+    const dim3 block(64u * (beams < 4 ? 4 : beams < 16 ? beams : 16));
+    const size_t dyn = in_lds ? entries * 12 : 0;
+    if (dtype == RING_F32) hipLaunchKernelGGL(beam_join_kernel<true>, dim3((unsigned)N), block, dyn, s, a, in_lds);
+    else hipLaunchKernelGGL(beam_join_kernel<false>, dim3((unsigned)N), block, dyn, s, a, in_lds);
     return hipGetLastError() == hipSuccess ? RING_OK : RING_EHIP;
 }
