@@ -657,7 +657,9 @@ extern "C" int tp_attention_decode_kv4(const void* const* q, const void* const* 
     }
     if (group == 1) shared = nullptr;                        // a row's shared keys are its own
     const Kv4Cut c = kv4_cut(P, B, group, shared != nullptr, Hq, Hkv, dev_info().cus);
-    const size_t need = kv4_ws(c, D);
+    // rows that no workgroup shares need no scan, no parts and no second launch
+    a.whole = !shared && (long long)table_stride * page_size <= kWholeTiles * kKeys;
+    const size_t need = a.whole ? kStatusBytes : kv4_ws(c, D);
     if (!ws || ((uintptr_t)ws & 255) || ws_bytes < need) return RING_EWORKSPACE;
     // costs and rows of parts are counted in 32 bits
     if ((long long)(B / group * c.shared_rbs + B * c.own_rbs) * ((long long)table_stride * page_size / kKeys + 1) * 8 >= (1LL << 31) ||
@@ -693,8 +695,6 @@ extern "C" int tp_attention_decode_kv4(const void* const* q, const void* const* 
     a.data = WsSpan{kStatusBytes, need};
     hipStream_t s = (hipStream_t)stream;
     const int units = P * Hkv;
-    // rows that no workgroup shares need no scan, no parts and no second launch
-    a.whole = !shared && (long long)table_stride * page_size <= kWholeTiles * kKeys;
     if (a.whole) a.blocks = B * c.own_rbs;
     if ((long long)units * a.blocks >= (1LL << 31)) return RING_EUNSUPPORTED;
     const dim3 grid((unsigned)(units * a.blocks));

@@ -64,19 +64,53 @@ __device__ __forceinline__ int block_scan(int x, int& total) {
     return below + s - x;
 }
 
+// kWords words of a set a thread, kThreads apart, so that neighbours' bits are
+// spread over the lanes; and, of each, the bits of all words before it.
+constexpr int kWords = 8;
+struct Words {
+    unsigned w[kWords];
+};
+__device__ __forceinline__ void word_scan(const Words& x, int words, int (&before)[kWords], int& total) {
+    __shared__ int part[kWords * kRowWaves + 1];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < kWords; ++v) {
+        int n = 0, s = 0;
+        if (v * kThreads < words) {
+            n = __builtin_popcount(x.w[v]);
+            s = wave_scan(n);
+        }
+        before[v] = s - n;
+        if (lane == 63) part[v * kRowWaves + wave] = s;
+    }
+    __syncthreads();
+    if (wave == 0) {
+        static_assert(kWords * kRowWaves == 128, "two sums a lane");
+        const int a = part[2 * lane], b = part[2 * lane + 1], s = wave_scan(a + b);
+        part[2 * lane] = s - a - b;
+        part[2 * lane + 1] = s - b;
+        if (lane == 63) part[128] = s;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < kWords; ++v) before[v] += part[v * kRowWaves + wave];
+    total = part[128];
+}
+
 struct ForkArgs {
     const int *table, *lengths, *parents, *keep, *used;
     int *free_pages, *table_after, *lengths_after, *copies, *n_copies, *shared, *used_after;
-    int B, B2, group, n_free, width, shift, pages, words;
+    int B, B2, group, n_free, width, shift, pages, words, new_blocks;
     Status* status;
     WsSpan zero;
-    int *counter, *owner, *differ;       // owner[page]: B2 - its first row, differ[group]: width - the first differing entry
+    int *counter, *owner, *apart;        // owner[page]: B2 - its first row, apart[group]: the room less the shared tokens
     unsigned *old, *full, *part;         // pages the old rows held, those the new ones have full, and partly filled
+    unsigned long long* last;            // per new row: its partly filled page + 1 (0: none), and its place above
 };
 
 struct ForkRow {
     int parent, tokens, held, full;      // held: pages, full: of them without a free place
-    __device__ __forceinline__ bool partial() const { return held > full; }
 };
 __device__ __forceinline__ int row_tokens(int n, int width, int shift) {
     const long long room = (long long)width << shift;
@@ -99,75 +133,150 @@ __device__ __forceinline__ ForkRow fork_row(const ForkArgs& a, int i) {
 }
 __device__ __forceinline__ bool is_page(int e, int pages) { return e >= 0 && e < pages; }
 
+// A new row, by a wave: its entries, and the marks of its pages.
+__device__ __forceinline__ void new_row(const ForkArgs& a, int i, int lane) {
+    const int near = lane < i ? a.parents[i - 1 - lane] : -1;
+    const ForkRow r = fork_row(a, i);
+    ForkRow up = {0, 0, 0, 0};
+    if (i) up = fork_row(a, i - 1);
+    // one of the 64 rows above has the same pages, and marks them
+    const bool again = !a.keep && __any(near == r.parent);
+    const int *row = a.table + (long long)r.parent * a.width, *above = a.table + (long long)up.parent * a.width;
+    int* to = a.table_after + (long long)i * a.width;
+    const bool grouped = a.shared && a.group > 1;
+    int common = r.tokens;               // tokens that the row above holds on the same pages
+    for (int j0 = 0; j0 < a.width; j0 += 256) {
+        int e[4], x[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int j = j0 + 64 * u + lane;
+            e[u] = j < r.held ? row[j] : -1;
+            x[u] = j < up.held ? above[j] : -1;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int j = j0 + 64 * u + lane;
+            // (the finishing workgroup writes the entry of a partly filled page)
+            if (j < a.width && (j >= r.held || j < r.full)) to[j] = e[u];
+            if (j < r.held && is_page(e[u], a.pages)) {
+                if (j >= r.full) {
+                    mark(a.part, e[u]);
+                    raise_to(a.owner + e[u], a.B2 - i);
+                    __hip_atomic_store(a.last + i, (unsigned long long)(unsigned)j << 32 | (unsigned)(e[u] + 1), __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+                } else if (!again && !(j < up.full && e[u] == x[u])) {
+                    mark(a.full, e[u]);
+                }
+            }
+            const unsigned long long other = __ballot(j < r.held && j < up.held && e[u] != x[u]);
+            if (other) {
+                const long long n = (long long)(j0 + 64 * u + __builtin_ctzll(other)) << a.shift;
+                if (n < common) common = (int)n;
+            }
+        }
+    }
+    if (lane) return;
+    a.lengths_after[i] = r.tokens;
+    // a partly filled entry that is no page is passed on
+    if (r.held > r.full && !is_page(row[r.full], a.pages)) to[r.full] = row[r.full];
+    if (!grouped) return;
+    const int room = (int)((long long)a.width << a.shift);
+    raise_to(a.apart + i / a.group, room - (i % a.group ? common : r.tokens));
+}
+
 // The workgroup that finishes: copies are counted in row order, freed pages by
 // number, and the one handed to the other.
 __device__ __forceinline__ void finish_fork(const ForkArgs& a, int* lds) {
-    int *rank = lds, *taken = lds + a.B2, *least = lds + 2 * a.B2;      // per row: its copy or -1; per copy: a freed page; per group
-    const int tid = threadIdx.x, groups = a.B2 / (a.group ? a.group : 1);
-    const int used = *a.used;
-    __syncthreads();
-    for (int g = tid; g < groups; g += kThreads) least[g] = 0x7fffffff;
-    __syncthreads();
-    int n_copies = 0, n_freed = 0, all;
+    int *page = lds, *at = lds + a.B2, *rank = lds + 2 * a.B2, *taken = lds + 3 * a.B2;      // per row: as in last, and its copy; per copy: a freed page
+    const int tid = threadIdx.x, used = *a.used;
+    const bool grouped = a.shared && a.group > 1;
+    constexpr int kChunk = kThreads * kWords;
+    auto freed = [&](int w0) {
+        Words r;
+#pragma unroll
+        for (int v = 0; v < kWords; ++v) {
+            const int w = w0 + v * kThreads + tid;
+            r.w[v] = 0;
+            if (w < a.words) r.w[v] = seen(a.old + w) & ~seen(a.full + w) & ~seen(a.part + w);
+        }
+        return r;
+    };
+    const Words gone = freed(0);
+    int before[kWords], n_copies = 0, n_freed, all;
     for (int i0 = 0; i0 < a.B2; i0 += kThreads) {
         const int i = i0 + tid;
         int copy = 0;
         if (i < a.B2) {
-            const ForkRow r = fork_row(a, i);
-            __hip_atomic_fetch_min(least + i / a.group, r.tokens, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-            if (r.partial()) {
-                const int e = a.table[(long long)r.parent * a.width + r.full];
-                if (is_page(e, a.pages))
-                    copy = (seen(a.full + (e >> 5)) >> (e & 31) & 1) || seen(a.owner + e) != a.B2 - i;
-                if (copy && a.group > 1) raise_to(a.differ + i / a.group, a.width - r.full);
-            }
+            const unsigned long long l = seen(a.last + i);
+            const int e = (int)(unsigned)l - 1;
+            page[i] = e;
+            at[i] = (int)(l >> 32);
+            if (e >= 0) copy = (seen(a.full + (e >> 5)) >> (e & 31) & 1) || seen(a.owner + e) != a.B2 - i;
+            if (copy && grouped) raise_to(a.apart + i / a.group, (a.width - at[i]) << a.shift);
         }
         const int k = block_scan(copy, all);
         if (i < a.B2) rank[i] = copy ? n_copies + k : -1;
         n_copies += all;
     }
-    auto freed = [&](int w) { return w < a.words ? seen(a.old + w) & ~seen(a.full + w) & ~seen(a.part + w) : 0u; };
-    int mine = 0;
-    for (int w = tid; w < a.words; w += kThreads) mine += __builtin_popcount(freed(w));
-    block_scan(mine, n_freed);
-    if (n_freed) {
-        int before = 0;
-        for (int w0 = 0; w0 < a.words; w0 += kThreads) {
-            unsigned bits = freed(w0 + tid);
-            int k = before + block_scan(__builtin_popcount(bits), all);
-            for (; bits; bits &= bits - 1, ++k) {
-                const int page = (w0 + tid) * 32 + __builtin_ctz(bits);
-                const long long at = (long long)used - n_freed + k;
-                if (k < n_copies) taken[k] = page;
-                else if (at >= 0 && at < a.n_free) a.free_pages[at] = page;
-            }
-            before += all;
-        }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");        // what raise_to did is done behind the scan's barriers
+    word_scan(gone, a.words, before, n_freed);
+    const int chunk0 = n_freed;
+    for (int w0 = kChunk; w0 < a.words; w0 += kChunk) {
+        int some[kWords];
+        word_scan(freed(w0), a.words - w0, some, all);
+        n_freed += all;
     }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    auto hand_out = [&](const Words& x, int w0, int base) {
+#pragma unroll
+        for (int v = 0; v < kWords; ++v) {
+            int k = base + before[v];
+            const int p = (w0 + v * kThreads + tid) * 32, entry = used - n_freed + k;
+            if (k >= n_copies && entry >= 0 && entry <= a.n_free - 32) {      // all of the word's pages go back
+                for (unsigned bits = x.w[v], i = entry; bits; bits &= bits - 1, ++i) a.free_pages[i] = p + __builtin_ctz(bits);
+            } else {
+                for (unsigned bits = x.w[v]; bits; bits &= bits - 1, ++k) {
+                    const int q = p + __builtin_ctz(bits), i = used - n_freed + k;
+                    if (k < n_copies) taken[k] = q;
+                    else if (i >= 0 && i < a.n_free) a.free_pages[i] = q;
+                }
+            }
+        }
+    };
+    hand_out(gone, 0, 0);
+    for (int w0 = kChunk, base = chunk0; w0 < a.words; w0 += kChunk) {
+        const Words x = freed(w0);
+        word_scan(x, a.words - w0, before, all);
+        hand_out(x, w0, base);
+        base += all;
+    }
     __syncthreads();
     for (int i = tid; i < a.B2; i += kThreads) {
-        const ForkRow r = fork_row(a, i);
-        if (r.partial()) {
-            int e = a.table[(long long)r.parent * a.width + r.full];
-            const int k = rank[i];
-            if (is_page(e, a.pages)) a.owner[e] = 0;
+        const int k = rank[i];
+        int e = page[i];
+        if (e >= 0) {
+            a.owner[e] = 0;
             if (k >= 0) {
-                const long long at = (long long)used + k - n_freed;
-                const int to = k < n_freed ? taken[k] : at >= 0 && at < a.n_free ? a.free_pages[at] : -1;
+                const long long entry = (long long)used + k - n_freed;
+                const int to = k < n_freed ? taken[k] : entry >= 0 && entry < a.n_free ? a.free_pages[entry] : -1;
                 a.copies[2 * k] = e;
                 a.copies[2 * k + 1] = to;
                 e = to;
             }
-            a.table_after[(long long)i * a.width + r.full] = e;
+            a.table_after[(long long)i * a.width + at[i]] = e;
         }
         if (i >= n_copies) a.copies[2 * i] = a.copies[2 * i + 1] = -1;
+        a.last[i] = 0;
     }
-    for (int g = tid; g < groups; g += kThreads) {
-        const int d = seen(a.differ + g);
-        const long long same = (long long)(a.width - d) << a.shift;
-        if (a.shared) a.shared[g] = least[g] < same ? least[g] : (int)same;
-        a.differ[g] = 0;
+    if (a.shared) {
+        const int room = (int)((long long)a.width << a.shift);
+        for (int g = tid; g < a.B2 / a.group; g += kThreads) {
+            if (grouped) {
+                a.shared[g] = room - seen(a.apart + g);
+                a.apart[g] = 0;
+            } else {
+                a.shared[g] = fork_row(a, g).tokens;
+            }
+        }
     }
     for (int w = tid; w < a.words; w += kThreads) a.old[w] = a.full[w] = a.part[w] = 0;
     if (tid == 0) {
@@ -183,58 +292,38 @@ __global__ __launch_bounds__(kThreads) void kv_fork_kernel(ForkArgs a) {
     __shared__ unsigned whole[KV_FORK_MAX_ROWS / 32];     // old rows that some new row keeps all tokens of
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const WsRecord rec = ws_record(a.status);
-    for (int w = tid; w < (a.B + 31) / 32; w += kThreads) whole[w] = 0;
-    __syncthreads();
-    for (int i = tid; i < a.B2; i += kThreads) {
-        const int p = a.parents[i];
-        if (p >= 0 && p < a.B && (!a.keep || a.keep[i] >= a.lengths[p]))
-            __hip_atomic_fetch_or(whole + (p >> 5), 1u << (p & 31), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-    }
-    __syncthreads();
-    if (!ws_ok(a.status, rec, a.zero, lane)) return;
-    const int step = gridDim.x * kRowWaves;
-    for (int i = blockIdx.x * kRowWaves + wave; i < a.B2; i += step) {
-        const ForkRow r = fork_row(a, i);
-        ForkRow up = {0, 0, 0, 0};
-        if (i) up = fork_row(a, i - 1);
-        const int *row = a.table + (long long)r.parent * a.width, *above = a.table + (long long)up.parent * a.width;
-        int* to = a.table_after + (long long)i * a.width;
-        const bool grouped = a.shared && i % a.group;
-        bool differs = false;
-        for (int j0 = 0; j0 < a.width; j0 += 64) {
-            const int j = j0 + lane;
-            const int e = j < r.held ? row[j] : -1, x = j < up.held ? above[j] : -1;
-            if (j < a.width && (j >= r.held || j < r.full)) to[j] = e;
-            const bool same = j < up.held && e == x;
-            if (j < r.held && is_page(e, a.pages)) {
-                if (j >= r.full) {
-                    mark(a.part, e);
-                    raise_to(a.owner + e, a.B2 - i);
-                } else if (!(same && j < up.full)) {
-                    mark(a.full, e);
-                }
-            }
-            if (grouped && !differs) {
-                const unsigned long long other = __ballot(j < r.held && j < up.held && e != x);
-                if (other) {
-                    differs = true;
-                    if (lane == 0) raise_to(a.differ + i / a.group, a.width - (j0 + __builtin_ctzll(other)));
-                }
-            }
+    if ((int)blockIdx.x < a.new_blocks) {
+        if (!ws_ok(a.status, rec, a.zero, lane)) return;
+        for (int i = blockIdx.x * kRowWaves + wave; i < a.B2; i += a.new_blocks * kRowWaves) new_row(a, i, lane);
+    } else {
+        for (int w = tid; w < (a.B + 31) / 32; w += kThreads) whole[w] = 0;
+        __syncthreads();
+        for (int i = tid; i < a.B2; i += kThreads) {
+            const int p = a.parents[i];
+            if (p >= 0 && p < a.B && (!a.keep || a.keep[i] >= a.lengths[p]))
+                __hip_atomic_fetch_or(whole + (p >> 5), 1u << (p & 31), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
         }
-        if (lane == 0) a.lengths_after[i] = r.tokens;
-    }
-    for (int b = blockIdx.x * kRowWaves + wave; b < a.B; b += step) {
-        if (whole[b >> 5] >> (b & 31) & 1) continue;
-        auto pages = [&](int n) { return (int)(((long long)row_tokens(n, a.width, a.shift) + (1 << a.shift) - 1) >> a.shift); };
-        const int held = pages(a.lengths[b]);
-        const int up_held = b ? pages(a.lengths[b - 1]) : 0;
-        const int* row = a.table + (long long)b * a.width;
-        for (int j = lane; j < held; j += 64) {
-            const int e = row[j];
-            // what the row above holds too it marks, or a new row keeps
-            const bool same = j < up_held && e == row[j - a.width];
-            if (is_page(e, a.pages) && !same) mark(a.old, e);
+        __syncthreads();
+        if (!ws_ok(a.status, rec, a.zero, lane)) return;
+        const int blocks = (int)gridDim.x - a.new_blocks;
+        for (int b = ((int)blockIdx.x - a.new_blocks) * kRowWaves + wave; b < a.B; b += blocks * kRowWaves) {
+            if (whole[b >> 5] >> (b & 31) & 1) continue;
+            auto pages = [&](int n) { return (int)(((long long)row_tokens(n, a.width, a.shift) + (1 << a.shift) - 1) >> a.shift); };
+            const int held = pages(a.lengths[b]), up_held = b ? pages(a.lengths[b - 1]) : 0;
+            const int* row = a.table + (long long)b * a.width;
+            for (int j0 = 0; j0 < held; j0 += 256) {
+                int e[4], x[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int j = j0 + 64 * u + lane;
+                    e[u] = j < held ? row[j] : -1;
+                    x[u] = j < up_held ? row[j - a.width] : -1;
+                }
+                // what the row above holds too it marks, or a new row keeps
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (is_page(e[u], a.pages) && e[u] != x[u]) mark(a.old, e[u]);
+            }
         }
     }
     if (last_block(a.counter)) finish_fork(a, lds);
@@ -260,33 +349,64 @@ __device__ __forceinline__ int held_pages(const CompactArgs& a, int b) {
 __device__ __forceinline__ void finish_compact(const CompactArgs& a) {
     const int tid = threadIdx.x;
     __shared__ int below;
-    int n = 0;
-    for (int w0 = 0; w0 < a.words; w0 += kThreads) {
-        const int w = w0 + tid;
-        const unsigned bits = w < a.words ? seen(a.live + w) : 0u;
-        int all;
-        const int k = n + block_scan(__builtin_popcount(bits), all);
-        if (w < a.words) {
-            a.before[w] = k;
-            a.in_use[w] = bits;
+    constexpr int kChunk = kThreads * kWords;
+    auto used = [&](int w0) {
+        Words r;
+#pragma unroll
+        for (int v = 0; v < kWords; ++v) {
+            const int w = w0 + v * kThreads + tid;
+            r.w[v] = 0;
+            if (w < a.words) r.w[v] = seen(a.live + w);
         }
+        return r;
+    };
+    const Words chunk0 = used(0);
+    int before[kWords], n, n0, all;
+    word_scan(chunk0, a.words, before, n0);
+    n = n0;
+    for (int w0 = kChunk; w0 < a.words; w0 += kChunk) {
+        int some[kWords];
+        word_scan(used(w0), a.words - w0, some, all);
         n += all;
     }
-    __syncthreads();
-    // pages in use below number n: the rest moves
-    for (int w = tid; w < a.words; w += kThreads)
-        if (w == n >> 5) below = a.before[w] + __builtin_popcount(a.in_use[w] & ((1u << (n & 31)) - 1));
+    // the pages in use below number n stay: in the word of page n, or all of them
+    auto find = [&](const Words& x, int w0, int base) {
+#pragma unroll
+        for (int v = 0; v < kWords; ++v)
+            if (w0 + v * kThreads + tid == n >> 5)
+                below = base + before[v] + __builtin_popcount(x.w[v] & ((1u << (n & 31)) - 1));
+    };
+    auto move = [&](const Words& x, int w0, int base, int stay) {
+#pragma unroll
+        for (int v = 0; v < kWords; ++v) {
+            const int w = w0 + v * kThreads + tid, k = base + before[v], p = w * 32;
+            if (w >= a.words) continue;
+            const unsigned under = n - p >= 32 ? ~0u : n > p ? (1u << (n - p)) - 1 : 0u;
+            int h = p - k, m = k + __builtin_popcount(x.w[v] & under) - stay;
+            for (unsigned y = ~x.w[v] & under; y; y &= y - 1, ++h) a.copies[2 * h + 1] = a.first + p + __builtin_ctz(y);
+            for (unsigned y = x.w[v] & ~under; y; y &= y - 1, ++m) a.copies[2 * m] = a.first + p + __builtin_ctz(y);
+            a.before[w] = k;
+            a.in_use[w] = x.w[v];
+            a.live[w] = 0;
+        }
+    };
     if (tid == 0 && n >> 5 >= a.words) below = n;
+    find(chunk0, 0, 0);
+    for (int w0 = kChunk, base = n0; w0 < a.words; w0 += kChunk) {
+        const Words x = used(w0);
+        word_scan(x, a.words - w0, before, all);
+        find(x, w0, base);
+        base += all;
+    }
     __syncthreads();
     const int stay = below;
-    for (int w = tid; w < a.words; w += kThreads) {
-        const unsigned bits = a.in_use[w];
-        const int k0 = a.before[w], p0 = w * 32;
-        const unsigned under = n - p0 >= 32 ? ~0u : n > p0 ? (1u << (n - p0)) - 1 : 0u;
-        int h = p0 - k0, m = k0 + __builtin_popcount(bits & under) - stay;
-        for (unsigned x = ~bits & under; x; x &= x - 1) a.copies[2 * h++ + 1] = a.first + p0 + __builtin_ctz(x);
-        for (unsigned x = bits & ~under; x; x &= x - 1) a.copies[2 * m++] = a.first + p0 + __builtin_ctz(x);
-        a.live[w] = 0;
+    if (a.words > kChunk) word_scan(chunk0, a.words, before, all);
+    move(chunk0, 0, 0, stay);
+    for (int w0 = kChunk, base = n0; w0 < a.words; w0 += kChunk) {
+        const Words x = used(w0);
+        word_scan(x, a.words - w0, before, all);
+        move(x, w0, base, stay);
+        base += all;
     }
     if (tid == 0) {
         a.before[a.words] = stay;
@@ -303,9 +423,19 @@ __global__ __launch_bounds__(kThreads) void kv_compact_kernel(CompactArgs a) {
     for (int b = blockIdx.x * kRowWaves + wave; b < a.B; b += gridDim.x * kRowWaves) {
         const int held = held_pages(a, b), up = b ? held_pages(a, b - 1) : 0;
         const int* row = a.table + (long long)b * a.width;
-        for (int j = lane; j < held; j += 64) {
-            const long long e = (long long)row[j] - a.first;
-            if (e >= 0 && e < a.n && !(j < up && row[j - a.width] == row[j])) mark(a.live, (int)e);
+        for (int j0 = 0; j0 < held; j0 += 256) {
+            int e[4], x[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int j = j0 + 64 * u + lane;
+                e[u] = j < held ? row[j] : -1;
+                x[u] = j < up ? row[j - a.width] : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const long long i = (long long)e[u] - a.first;
+                if (i >= 0 && i < a.n && e[u] != x[u]) mark(a.live, (int)i);
+            }
         }
     }
     if (last_block(a.counter)) finish_compact(a);
@@ -361,10 +491,10 @@ __global__ __launch_bounds__(256) void kv_copy_kernel(CopyArgs a) {
             u32x4 x[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                if (v + 64 * u < v1) x[u] = src[v + 64 * u];
+                if (v + 64 * u < v1) x[u] = __builtin_nontemporal_load(src + v + 64 * u);
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-                if (v + 64 * u < v1) dst[v + 64 * u] = x[u];
+                if (v + 64 * u < v1) __builtin_nontemporal_store(x[u], dst + v + 64 * u);
         }
     }
 }
@@ -392,7 +522,7 @@ using namespace ringc;
 
 extern "C" size_t kv_fork_workspace_bytes(int B_after, int pages) {
     if (B_after < 0 || B_after > KV_FORK_MAX_ROWS || pages < 0) return 0;
-    return kStatusBytes + up256((64 + 3 * fork_words(pages) + (size_t)pages + (size_t)B_after) * 4);
+    return kStatusBytes + up256((64 + 2 * (size_t)B_after + 3 * fork_words(pages) + (size_t)pages + (size_t)B_after) * 4);
 }
 
 extern "C" int kv_fork(const int* block_table, const int* lengths, const int* parents, const int* keep, int* free_pages,
@@ -438,13 +568,15 @@ extern "C" int kv_fork(const int* block_table, const int* lengths, const int* pa
     a.status = (Status*)ws;
     a.zero = WsSpan{kStatusBytes, need};
     a.counter = (int*)((char*)ws + kStatusBytes);
-    a.old = (unsigned*)a.counter + 64;
+    a.last = (unsigned long long*)(a.counter + 64);
+    a.old = (unsigned*)(a.last + B_after);
     a.full = a.old + a.words;
     a.part = a.full + a.words;
     a.owner = (int*)a.part + a.words;
-    a.differ = a.owner + pages;
-    hipLaunchKernelGGL(kv_fork_kernel, dim3((unsigned)row_blocks(B > B_after ? B : B_after)), dim3(kThreads),
-                       3 * (size_t)B_after * sizeof(int), (hipStream_t)stream, a);
+    a.apart = a.owner + pages;
+    a.new_blocks = row_blocks(B_after);
+    hipLaunchKernelGGL(kv_fork_kernel, dim3((unsigned)(a.new_blocks + row_blocks(B))), dim3(kThreads),
+                       4 * (size_t)B_after * sizeof(int), (hipStream_t)stream, a);
     return hipGetLastError() == hipSuccess ? RING_OK : RING_EHIP;
 }
 

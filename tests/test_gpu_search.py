@@ -268,9 +268,9 @@ def test_fork_of_many_pages():
 def test_fork_refuses_a_workspace_with_data_in_it():
     """Counters would lie in what decoding left: an error, not a wrong table."""
     table, lens, free, used, pages = fork_state(8, 16, 200, 14, 30, 3)
-    ws = torch.zeros(1 << 20, dtype=torch.uint8, device="cuda")
     q, cache = [torch.ones(2, 4, 64, dtype=BF, device="cuda")], [S.kv4_cache(9, 2, 64, 16)]
-    S.tp_attention_decode_kv4(q, cache, [torch.empty_like(q[0])], i32([[0, 1], [2, 3]]), i32([30, 20]), page_size=16, ws=ws)
+    pages_of = i32([[0, 1] + [-1] * 60, [2, 3] + [-1] * 60])
+    ws = S.tp_attention_decode_kv4(q, cache, [torch.empty_like(q[0])], pages_of, i32([30, 20]), page_size=16)
     run_fork(table, lens, [0] * 8, None, free, used, 16, pages, 1, ws=ws)
     from ring_collectives_amd import collectives as rc
     assert rc.last_error(ws)[0] == N.RING_EWORKSPACE
