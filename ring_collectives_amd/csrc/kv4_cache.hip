@@ -74,7 +74,7 @@ template <int D, bool WRITE> __global__ __launch_bounds__(256) void kv4_kernel(K
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
             const int t = k.tile * kTokens + s * kRows + lane / L;
-            x[s] = *(const u32x4*)(in + (t < a.T ? t : 0) * stride);
+            x[s] = __builtin_nontemporal_load((const u32x4*)(in + (t < a.T ? t : 0) * stride));
         }
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
@@ -115,7 +115,7 @@ template <int D, bool WRITE> __global__ __launch_bounds__(256) void kv4_kernel(K
 #pragma unroll
         for (int s = 0; s < kSteps; ++s) {
             const int t = k.tile * kTokens + s * kRows + lane / L;
-            if (t < a.T) *(bf16x8*)(out + t * stride) = kv4_values(c[s], kv4_scale(f[s]));
+            if (t < a.T) __builtin_nontemporal_store(kv4_values(c[s], kv4_scale(f[s])), (bf16x8*)(out + t * stride));
         }
     }
 }
