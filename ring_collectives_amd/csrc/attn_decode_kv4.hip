@@ -36,6 +36,7 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kKeys = 32;              // of a tile
 constexpr int kOwnCost = 2;            // of a tile of own keys
+constexpr int kItemCost = 4;           // of an item besides its tiles: its look-ups, and storing its part
 constexpr int kWholeTiles = 16;        // a row of as many at most is one workgroup's
 constexpr int kMinCost = 4;            // of a wave, if there is as much (and no less than a tile's)
 
@@ -48,13 +49,18 @@ struct alignas(16) ItemParts {
         return p < head ? w0 + p : p < head + mid ? inner + (p - head) * kWaves : outer + (p - head - mid);
     }
 };
-// Of an item of cost [lo, hi) of `total`, tiles of cost c and waves of cost quota.
+// Of an item of cost [lo, hi) of `total`, kItemCost and its tiles' c each, and
+// waves of cost quota.
 __device__ __forceinline__ ItemParts item_parts(unsigned lo, unsigned hi, unsigned c, unsigned total, unsigned quota) {
     if (lo == hi) return ItemParts{0, 0, 0, 0};
-    const unsigned quad = kWaves * quota, w0 = lo / quota, w1 = (hi - c) / quota + 1;       // w1: past the wave that the last tile begins in
-    unsigned b0 = (lo + quad - 1) / quad, b1 = hi == total ? (hi + quad - 1) / quad : hi / quad;
-    if (b1 * kWaves > w1) b1 = (w1 + kWaves - 1) / kWaves;      // a last workgroup without a tile, or with few waves' share
+    const unsigned quad = kWaves * quota;
+    unsigned w0 = (lo + kItemCost) / quota;                // that the first tile begins in
+    const unsigned w1 = (hi - c) / quota + 1;              // past the one that the last tile begins in
+    unsigned b0 = w0 / kWaves, b1 = hi == total ? (hi + quad - 1) / quad : hi / quad;
+    if (b0 * quad < lo) ++b0;
+    if (b1 * kWaves > w1) b1 = (w1 + kWaves - 1) / kWaves; // a last workgroup without a tile, or with few waves' share
     const unsigned inner = b0 < b1 ? b0 * kWaves : w1, outer = b0 < b1 ? b1 * kWaves : w1;
+    if (w0 > inner) w0 = inner;                            // a first workgroup that is within the item
     return ItemParts{(int)w0, (int)inner, (int)outer, (int)(inner - w0 + (outer - inner) / kWaves + (outer < w1 ? w1 - outer : 0))};
 }
 
@@ -403,40 +409,44 @@ __device__ __forceinline__ void run_piece(const Kv4DecodeArgs& a, const Fixed& f
 }
 
 template <int D, int NT> __global__ __launch_bounds__(256, NT == 1 ? 3 : NT == 2 ? 2 : 1) void kv4_decode_kernel(Kv4DecodeArgs a) {
-    extern __shared__ int lens[];                          // [B] lengths, [groups] shared tiles
+    extern __shared__ int lens[];                          // [B] lengths, [B] own tiles, [groups] shared tiles
     __shared__ __align__(4096) unsigned short lds[kWaves * kTileBytes<D> / 2];
     __shared__ float wave_ml[kWaves][16][2];
     __shared__ int part_sum[kWaves], found[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int units = a.P * a.Hkv, unit = blockIdx.x % units, blk = blockIdx.x / units;
     const Items n = items_of(a);
-    int* few = lens + a.B;                                 // per group: the shared keys' tiles
+    int *own = lens + a.B, *few = own + a.B;
     if (blockIdx.x == 0 && tid == 0) ws_add_data(a.status, a.data);
     const int len0 = tid < a.B ? a.lengths[tid] : 0, few0 = tid < n.groups ? a.shared[tid] : 0;     // in one trip, where few
     const Fixed f = read_fixed(a, unit / a.Hkv);
     auto tokens = [&](int x) { return f.pages ? clamp_len(x, f.width, f.shift) : 0; };
     if (a.whole) {
-        if (tid == 0) lens[blk / a.own_rbs] = tokens(a.lengths[blk / a.own_rbs]);
+        if (tid == 0) {
+            const int b = blk / a.own_rbs, len = tokens(a.lengths[b]);
+            lens[b] = len;
+            own[b] = (len + kKeys - 1) / kKeys;
+        }
     } else {
         for (int b = tid; b < a.B; b += 256) lens[b] = tokens(b < 256 ? len0 : a.lengths[b]);
         for (int g = tid; g < n.groups; g += 256) few[g] = tokens(g < 256 ? few0 : a.shared[g]);
         __syncthreads();
-        if (n.groups)
+        if (n.groups) {
             for (int b = tid; b < a.B; b += 256)
                 __hip_atomic_fetch_min(few + b / f.group, lens[b], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
-        __syncthreads();
-        for (int g = tid; g < n.groups; g += 256) few[g] /= kKeys;   // whole tiles; the rest is every row's own
+            __syncthreads();
+        }
+        // whole tiles are shared; the rest is every row's own
+        for (int b = tid; b < a.B; b += 256) own[b] = (lens[b] + kKeys - 1) / kKeys - (n.groups ? few[b / f.group] / kKeys : 0);
     }
     __syncthreads();
-    // the tiles of item it; a row's own follow its shared ones
-    auto first_tile = [&](int b) { return n.groups ? few[b / f.group] : 0; };
-    auto tiles = [&](int it) {
-        if (it < n.shared) return few[it / a.shared_rbs];
-        const int b = (it - n.shared) / a.own_rbs;
-        return (lens[b] + kKeys - 1) / kKeys - first_tile(b);
-    };
+    auto per = [](int x, int y) { return y == 1 ? x : x / y; };
+    auto tiles = [&](int it) { return it < n.shared ? few[per(it, a.shared_rbs)] / kKeys : own[per(it - n.shared, a.own_rbs)]; };
     auto tile_cost = [&](int it) { return it < n.shared ? a.shared_cost : kOwnCost; };
-    auto cost = [&](int it) { return tiles(it) * tile_cost(it); };
+    auto cost = [&](int it) {
+        const int m = tiles(it);
+        return m ? m * tile_cost(it) + kItemCost : 0;
+    };
     Piece w;
     w.head = unit % f.Hkv;
     int it = blk, at = 0, worker = 0;
@@ -487,9 +497,10 @@ template <int D, int NT> __global__ __launch_bounds__(256, NT == 1 ? 3 : NT == 2
     }
     for (bool more = a.whole || at < t1; more; ++it) {
         const int m = __builtin_amdgcn_readfirstlane(tiles(it)), c = tile_cost(it);
-        const int lo = t0 > at ? (int)((t0 - at + c - 1) / c) : 0;
-        const int hi = !a.whole && t1 < at + (long long)m * c ? (int)((t1 - at + c - 1) / c) : m;
-        at += m * c;
+        const int begin = at + kItemCost;                  // of its tiles
+        const int lo = t0 > begin ? (int)((t0 - begin + c - 1) / c) : 0;
+        const int hi = a.whole || t1 >= begin + (long long)m * c ? m : t1 > begin ? (int)((t1 - begin + c - 1) / c) : 0;
+        if (m) at = begin + m * c;
         more = !a.whole && at < t1;
         if (lo >= hi && !a.whole) continue;
         if (it < n.shared) {
@@ -497,14 +508,15 @@ template <int D, int NT> __global__ __launch_bounds__(256, NT == 1 ? 3 : NT == 2
             w.j1 = hi;
             w.part = unit * (n.shared + a.waves) + it + worker;
             w.direct = false;
-            run_piece<D, NT, true>(a, f, w, it / a.shared_rbs * f.group, it % a.shared_rbs, m * kKeys, lds, wave_ml);
+            const int g = per(it, a.shared_rbs);
+            run_piece<D, NT, true>(a, f, w, g * f.group, it - g * a.shared_rbs, m * kKeys, lds, wave_ml);
         } else {
-            const int b = (it - n.shared) / a.own_rbs, first = __builtin_amdgcn_readfirstlane(first_tile(b));
+            const int b = per(it - n.shared, a.own_rbs), len = __builtin_amdgcn_readfirstlane(lens[b]), first = (len + kKeys - 1) / kKeys - m;
             w.j0 = first + lo;
             w.j1 = first + hi;
             w.part = unit * (n.own + a.waves) + it - n.shared + worker;
             w.direct = first == 0 && lo == 0 && hi == m;
-            run_piece<D, 1, false>(a, f, w, b, (it - n.shared) % a.own_rbs, __builtin_amdgcn_readfirstlane(lens[b]), lds, wave_ml);
+            run_piece<D, 1, false>(a, f, w, b, it - n.shared - b * a.own_rbs, len, lds, wave_ml);
         }
     }
 }
@@ -662,7 +674,7 @@ extern "C" int tp_attention_decode_kv4(const void* const* q, const void* const* 
     const size_t need = a.whole ? kStatusBytes : kv4_ws(c, D);
     if (!ws || ((uintptr_t)ws & 255) || ws_bytes < need) return RING_EWORKSPACE;
     // costs and rows of parts are counted in 32 bits
-    if ((long long)(B / group * c.shared_rbs + B * c.own_rbs) * ((long long)table_stride * page_size / kKeys + 1) * 8 >= (1LL << 31) ||
+    if ((long long)(B / group * c.shared_rbs + B * c.own_rbs) * ((long long)table_stride * page_size / kKeys + 2) * 8 >= (1LL << 31) ||
         (long long)P * B * Hq >= (1LL << 31) || (c.shared_parts * 16 * c.nt + c.own_parts * c.own_rows) >= (1ull << 31))
         return RING_EUNSUPPORTED;
     a.table = block_table;
@@ -698,7 +710,7 @@ extern "C" int tp_attention_decode_kv4(const void* const* q, const void* const* 
     if (a.whole) a.blocks = B * c.own_rbs;
     if ((long long)units * a.blocks >= (1LL << 31)) return RING_EUNSUPPORTED;
     const dim3 grid((unsigned)(units * a.blocks));
-    const size_t dyn = ((size_t)B + (shared ? B / group : 0)) * sizeof(int);
+    const size_t dyn = (2 * (size_t)B + (shared ? B / group : 0)) * sizeof(int);
     const long long rows = (long long)P * B * Hq;
     const bool few = rows <= 2LL * dev_info().cus;           // 256 lanes a row, else 64
     const dim3 jg((unsigned)(few ? B * Hq : B * ((Hq + 3) / 4)), (unsigned)P);
