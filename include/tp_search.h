@@ -161,14 +161,15 @@ int tp_kv4_read(const void *const *cache, const long long *slots, void *const *k
  * requests behind one prompt): the first shared[g] keys of all rows of group g
  * are the same ones (kv_fork gives such numbers; NULL: none are), are found
  * through the table row of the group's first row, and are read once for up to
- * 64 (row, head of the group that shares a key head).  shared[g] is clamped to
+ * 32 (row, head of the group that shares a key head).  shared[g] is clamped to
  * the lengths of the group's rows.
  * Products in bf16 on the matrix cores (4-bit values are exact in bf16) with
  * fp32 sums, statistics in fp32, the softmax weights rounded to bf16.
  * Lengths are clamped to [0, table_stride * page_size]; keys whose page lies
  * outside [0, pages) take no part; a row without keys gives o = 0.  Rows of the
  * cache that are no key of a row never reach its result.
- * The keys are shared out evenly among the compute units whatever the lengths.
+ * Where the table's rows hold more than 2048 keys, or keys are shared, the keys
+ * are shared out evenly among the compute units whatever the lengths.
  * B <= KV_FORK_MAX_ROWS, group divides B.  The workspace of a batch holds every
  * smaller one with the same other sizes.
  */

@@ -14,7 +14,7 @@
 // are all within one item join their results in LDS, so that long items make
 // few parts; others go through their items by themselves, without a barrier.
 // A part that is all of its row's keys is the result; a second launch joins the
-// rest.  Where the table's rows hold 512 keys at most and nothing is shared,
+// rest.  Where the table's rows hold 2048 keys at most and nothing is shared,
 // every row is one workgroup's and there is neither scan nor second launch.
 //
 // A wave's tile goes from memory to registers (two 16-byte loads a lane each
@@ -37,7 +37,12 @@ constexpr int kWaves = 4;
 constexpr int kKeys = 32;              // of a tile
 constexpr int kOwnCost = 2;            // of a tile of own keys
 constexpr int kItemCost = 4;           // of an item besides its tiles: its look-ups, and storing its part
-constexpr int kWholeTiles = 16;        // a row of as many at most is one workgroup's
+// Rows of at most as many tiles are a workgroup's each.  3 requests of up to 600 /
+// 1100 keys on 2 ranks of 2 key heads 7.6 / 9.2 us so, shared out 12; 64 on 4
+// ranks 12.7 / 17.5, shared out 17.9 / 21.7, of 2200 27.7 and 29.7; but the only
+// long row of a batch is one workgroup's too, and at 2048 keys that takes as
+// long as sharing out and joining.
+constexpr int kWholeTiles = 64;
 constexpr int kMinCost = 4;            // of a wave, if there is as much (and no less than a tile's)
 
 // An item's parts: a wave's each, those before the first and after the last
@@ -408,7 +413,7 @@ __device__ __forceinline__ void run_piece(const Kv4DecodeArgs& a, const Fixed& f
     }
 }
 
-template <int D, int NT> __global__ __launch_bounds__(256, NT == 1 ? 3 : NT == 2 ? 2 : 1) void kv4_decode_kernel(Kv4DecodeArgs a) {
+template <int D, int NT> __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void kv4_decode_kernel(Kv4DecodeArgs a) {
     extern __shared__ int lens[];                          // [B] lengths, [B] own tiles, [groups] shared tiles
     __shared__ __align__(4096) unsigned short lds[kWaves * kTileBytes<D> / 2];
     __shared__ float wave_ml[kWaves][16][2];
@@ -606,16 +611,20 @@ struct Kv4Cut {
     int nt, blocks, waves, shared_rbs, own_rbs, own_rows;
     size_t shared_parts, own_parts, items;                   // parts over all (rank, key head)
 };
+// Shared keys are taken against 32 rows at a time where there are more than 16:
+// groups of 8 / 16 / 64 beams of 4 heads 24.1 / 28.9 / 33.9 us so, against 16
+// 24.9 / 28.6 / 34.4, against 64, whose registers leave one wave a SIMD for the
+// rows' own keys too, 24.0 / 41.3 / 46.1.
 Kv4Cut kv4_cut(int P, int B, int group, bool shared, int Hq, int Hkv, int cus) {
     Kv4Cut c;
     const int G = Hq / Hkv;
     const long long units = (long long)P * Hkv, rows = (long long)group * G;
-    c.nt = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
+    c.nt = rows <= 16 ? 1 : 2;
     c.shared_rbs = (int)((rows + 16 * c.nt - 1) / (16 * c.nt));
     c.own_rbs = (G + 15) / 16;
     c.own_rows = G < 16 ? G : 16;
-    // as many workgroups as run at once: by registers three a compute unit, one for four row tiles
-    c.blocks = (int)(((c.nt == 4 && shared ? 1 : 3) * (long long)cus + units - 1) / units);
+    // as many workgroups as run at once: by registers three a compute unit, two with two row tiles
+    c.blocks = (int)(((c.nt == 2 && shared ? 2 : 3) * (long long)cus + units - 1) / units);
     c.waves = c.blocks * kWaves;
     const size_t ns = shared ? (size_t)(B / group) * c.shared_rbs : 0, no = (size_t)B * c.own_rbs;
     c.items = ns + no;
@@ -725,8 +734,7 @@ extern "C" int tp_attention_decode_kv4(const void* const* q, const void* const* 
     };
     auto with_nt = [&](auto d) -> int {
         if (!shared || c.nt == 1) return go(d, std::integral_constant<int, 1>());
-        if (c.nt == 2) return go(d, std::integral_constant<int, 2>());
-        return go(d, std::integral_constant<int, 4>());
+        return go(d, std::integral_constant<int, 2>());
     };
     return D == 128 ? with_nt(std::integral_constant<int, 128>()) : with_nt(std::integral_constant<int, 64>());
 }

@@ -97,7 +97,7 @@ def tp_attention_decode_kv4(q, cache, o, block_table, lengths, page_size: int, s
     """o[r] <- attention of one query token per row, q[r] (B, Hq, D), over the
     first lengths[b] rows of block_table[b] (B, W int32) of the 4-bit cache.
     The first shared[g] of them are the same for `group` rows in turn, and read
-    once for up to 64 (row, head of the group that shares a key head).  The
+    once for up to 32 (row, head of the group that shares a key head).  The
     workspace of a batch holds smaller ones."""
     if ws is None:
         B, Hq, D = _lead(q, 3, "q")

@@ -269,7 +269,7 @@ def test_fork_refuses_a_workspace_with_data_in_it():
     """Counters would lie in what decoding left: an error, not a wrong table."""
     table, lens, free, used, pages = fork_state(8, 16, 200, 14, 30, 3)
     q, cache = [torch.ones(2, 4, 64, dtype=BF, device="cuda")], [S.kv4_cache(9, 2, 64, 16)]
-    pages_of = i32([[0, 1] + [-1] * 60, [2, 3] + [-1] * 60])
+    pages_of = i32([[0, 1] + [-1] * 200, [2, 3] + [-1] * 200])
     ws = S.tp_attention_decode_kv4(q, cache, [torch.empty_like(q[0])], pages_of, i32([30, 20]), page_size=16)
     run_fork(table, lens, [0] * 8, None, free, used, 16, pages, 1, ws=ws)
     from ring_collectives_amd import collectives as rc
@@ -473,9 +473,12 @@ def random_cache(P, pages, Hkv, D, page, seed):
     return out
 
 
-def check_decode_kv4(q, cache, table, lengths, page, shared=None, group=1, scale=None, ws=None, o=None):
-    """Runs the call and holds every row to the oracle's bound."""
+def check_decode_kv4(q, cache, table, lengths, page, shared=None, group=1, scale=None, ws=None, o=None, wide=False):
+    """Runs the call and holds every row to the oracle's bound; wide: with a
+    table of more than 2048 keys a row, whose keys are shared out."""
     P, (B, Hq, D) = len(q), q[0].shape
+    if wide:
+        table = [list(row) + [-1] * (2048 // page + 1) for row in table]
     pages, Hkv = cache[0].shape[:2]
     o = o or [poisoned((B, Hq, D)) for _ in range(P)]
     ws = S.tp_attention_decode_kv4(q, cache, o, i32(table).reshape(B, -1), i32(lengths), page_size=page,
@@ -529,10 +532,11 @@ DECODE = [(1, [1], 1, 1, 64, 16), (1, [16], 4, 1, 128, 16), (2, [5, 0, 33], 8, 2
 
 
 @pytest.mark.parametrize("P,lengths,Hq,Hkv,D,page", DECODE)
-def test_decode_kv4(P, lengths, Hq, Hkv, D, page):
-    note("decode_kv4 P=%d lengths=%s heads=%d/%d D=%d page=%d" % (P, lengths[:6], Hq, Hkv, D, page))
+@pytest.mark.parametrize("wide", [False, True])
+def test_decode_kv4(P, lengths, Hq, Hkv, D, page, wide):
+    note("decode_kv4 P=%d lengths=%s heads=%d/%d D=%d page=%d wide=%s" % (P, lengths[:6], Hq, Hkv, D, page, wide))
     q, cache, table = decode_state(P, len(lengths), Hq, Hkv, D, page, lengths, len(lengths) * 7 + D)
-    check_decode_kv4(q, cache, table, lengths, page)
+    check_decode_kv4(q, cache, table, lengths, page, wide=wide)
 
 
 @pytest.mark.parametrize("group,G,D,page,shared,own", [
@@ -555,6 +559,7 @@ def test_decode_kv4_of_groups(group, G, D, page, shared, own):
     ws = check_decode_kv4(q, cache, table, lengths, page, shared=sh, group=group)
     check_decode_kv4(q, cache, table, lengths, page, shared=lead, group=group, ws=ws)
     check_decode_kv4(q, cache, table, lengths, page, group=group, ws=ws)
+    check_decode_kv4(q, cache, table, lengths, page, shared=sh, group=group, ws=ws, wide=True)
 
 
 def test_decode_kv4_of_shared_lengths_past_the_rows():
@@ -582,9 +587,10 @@ def test_decode_kv4_of_pages_that_are_none():
     lengths = [100, 70, 50, 20]
     q, cache, table = decode_state(1, 4, 4, 2, 128, 16, lengths, 9)
     table[0][1], table[0][4], table[1][0], table[3] = -1, 5000, 1 << 30, [-1] * len(table[3])
-    check_decode_kv4(q, cache, table, lengths, 16)
-    check_decode_kv4(q, cache, table, lengths, 16, shared=[64, 0], group=2)
-    check_decode_kv4(q, cache, table, [1 << 30, -4, 50, 20], 16)          # lengths past the table
+    for wide in (False, True):
+        check_decode_kv4(q, cache, table, lengths, 16, wide=wide)
+        check_decode_kv4(q, cache, table, lengths, 16, shared=[64, 0], group=2, wide=wide)
+        check_decode_kv4(q, cache, table, [1 << 30, -4, 50, 20], 16, wide=wide)          # lengths past the table
 
 
 def test_decode_kv4_without_a_cache():
@@ -609,6 +615,7 @@ def test_decode_kv4_sees_no_row_that_is_no_key():
             if (p, i) not in used:
                 scales[p, :, :, i] = 255
     check_decode_kv4(q, cache, table, lengths, 16)
+    check_decode_kv4(q, cache, table, lengths, 16, wide=True)
     check_decode_kv4(q, cache, table, lengths, 16, shared=[0, 32], group=2)
 
 
@@ -620,10 +627,11 @@ def test_decode_kv4_of_keys_and_values_that_are_nan():
     scales = cache[0][:, :, n:].view(cache[0].shape[0], 1, 2, 16, 2)
     scales[table[0][1], 0, 0, 3, 0] = 255                     # a key of row 0
     scales[table[1][2], 0, 1, 5, 1] = 255                     # a value of row 1: its second block
-    o = [poisoned((3, 2, 64))]
-    S.tp_attention_decode_kv4(q, cache, o, i32(table), i32(lengths), page_size=16)
-    x = f64(o[0])
-    assert np.isnan(x[0]).all() and np.isnan(x[1, :, 32:]).all() and np.isfinite(x[1, :, :32]).all() and np.isfinite(x[2]).all()
+    for pad in (0, 200):
+        o = [poisoned((3, 2, 64))]
+        S.tp_attention_decode_kv4(q, cache, o, i32([row + [-1] * pad for row in table]), i32(lengths), page_size=16)
+        x = f64(o[0])
+        assert np.isnan(x[0]).all() and np.isnan(x[1, :, 32:]).all() and np.isfinite(x[1, :, :32]).all() and np.isfinite(x[2]).all()
 
 
 @pytest.mark.parametrize("sharp", [0.0, 30.0])
@@ -631,6 +639,7 @@ def test_decode_kv4_of_flat_and_sharp_rows(sharp):
     lengths = [600, 1000]
     q, cache, table = decode_state(1, 2, 4, 1, 128, 16, lengths, 14, sharp)
     check_decode_kv4(q, cache, table, lengths, 16)
+    check_decode_kv4(q, cache, table, lengths, 16, wide=True)
 
 
 def test_decode_kv4_of_slices_of_wider_rows():

@@ -342,7 +342,7 @@ def test_decode_workspace_of_smaller_batches():
 
 def test_large_batches():
     """As many rows as the calls take."""
-    note("decode_kv4 of 8192 rows, fork of 8192")
+    note("decode_kv4 of 8192 rows")
     B, page, D = 8192, 16, 64
     q = [torch.randn(B, 1, D, device="cuda").to(BF)]
     cache = random_cache(1, 100, 1, D, page, 3)
@@ -350,7 +350,7 @@ def test_large_batches():
     shared = torch.randint(0, 641, (B // 8,), device="cuda").int()
     table = table.view(-1, 8, 40)[:, :1].expand(-1, 8, -1).reshape(B, 40).contiguous()       # groups on the same pages
     o1, o2 = [poisoned((B, 1, D))], [poisoned((B, 1, D))]
-    S.tp_attention_decode_kv4(q, cache, o1, table, lens, page_size=page)
+    S.tp_attention_decode_kv4(q, cache, o1, torch.cat([table, table.new_full((B, 100), -1)], 1), lens, page_size=page)
     S.tp_attention_decode_kv4(q, cache, o2, table, lens, page_size=page, shared=shared, group=8)
     some = torch.arange(0, B, 997, device="cuda")
     check_decode_kv4([q[0][some]], cache, table[some].tolist(), lens[some].tolist(), page)
