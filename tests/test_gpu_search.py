@@ -178,6 +178,8 @@ def check_fork(table, lengths, parents, keep, free, used, page, pages, group, **
         if name == "shared" and not kw.get("shared", True):
             continue
         assert np.array_equal(g.reshape(-1), np.asarray(w).reshape(-1)), name
+    if pages <= 8192:                                          # and as with more pages than one workgroup's LDS holds
+        check_fork(table, lengths, parents, keep, free, used, page, pages + 8193, group, **{**kw, "ws": None})
     return got, ws
 
 
@@ -271,11 +273,11 @@ def test_fork_refuses_a_workspace_with_data_in_it():
     q, cache = [torch.ones(2, 4, 64, dtype=BF, device="cuda")], [S.kv4_cache(9, 2, 64, 16)]
     pages_of = i32([[0, 1] + [-1] * 200, [2, 3] + [-1] * 200])
     ws = S.tp_attention_decode_kv4(q, cache, [torch.empty_like(q[0])], pages_of, i32([30, 20]), page_size=16)
-    run_fork(table, lens, [0] * 8, None, free, used, 16, pages, 1, ws=ws)
+    run_fork(table, lens, [0] * 8, None, free, used, 16, pages + 9000, 1, ws=ws)
     from ring_collectives_amd import collectives as rc
     assert rc.last_error(ws)[0] == N.RING_EWORKSPACE
     ws.zero_()
-    check_fork(table, lens, [0] * 8, None, free, used, 16, pages, 1, ws=ws)
+    check_fork(table, lens, [0] * 8, None, free, used, 16, pages + 9000, 1, ws=ws)
 
 
 # ---------------------------------------------------------------- kv_compact
@@ -289,6 +291,8 @@ def check_compact(table, lengths, first, pool, page, ws=None):
     want = osr.compact(table, lengths, first, pool, page)
     for g, w, name in zip((out, copies, n, used, fp), want, ("table", "copies", "n_copies", "used", "free")):
         assert np.array_equal(g.cpu().numpy().reshape(-1), np.asarray(w).reshape(-1)), name
+    if pool <= 8192:                                           # and as with more pages than one workgroup's LDS holds
+        check_compact(table, lengths, first, pool + 8193, page)
     return ws
 
 
