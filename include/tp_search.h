@@ -18,8 +18,9 @@
  * device memory holds trusted).  In ws, besides:
  *   - kv_fork and kv_compact need their counters in ws zero and leave them
  *     zero; where another call left data there, they stop with RING_EWORKSPACE
- *     in the workspace's error word (ring_last_error) and undefined outputs.
- *     The calls of this header that leave data record where.
+ *     in the workspace's error word (ring_last_error) and undefined outputs
+ *     (with few rows and pages they use no counters, and do not).  The calls of
+ *     this header that leave data record where.
  */
 #ifndef TP_SEARCH_H
 #define TP_SEARCH_H
@@ -42,7 +43,8 @@ extern "C" {
  * the candidates of group n are scores[n][w] + lp(n * beams + w, t) over all w
  * and t; with done != NULL, a beam with done[n][w] != 0 has the one candidate
  * (w, end_token) of score scores[n][w] instead.  Written, best first, of equal
- * scores the lowest w, then the lowest t:
+ * scores the lowest w, then the largest logit (scores[n][w] may be so large
+ * that logits that differ give one score), then the lowest t:
  *   parents       [N][keep] the candidate's row, n * beams + w
  *   tokens        [N][keep] its t
  *   scores_after  [N][keep] its score

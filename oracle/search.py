@@ -32,7 +32,8 @@ def log_probs(logits):
 
 def select(logits, scores, vocab, keep, done=None, end=-1):
     """logits: (rows, vocab); (parents, tokens, scores, done_after, bound): best
-    first, ties to the lowest beam, then token."""
+    first, of equal scores the lowest beam, then the largest logit, then the
+    lowest token."""
     N, W = scores.shape
     parents, tokens = np.full((N, keep), -1), np.full((N, keep), -1)
     after, done_after = np.full((N, keep), -np.inf), np.zeros((N, keep), bool)
@@ -49,7 +50,11 @@ def select(logits, scores, vocab, keep, done=None, end=-1):
             every[n, w] = float(scores[n, w]) + lp
             bound = max(bound, b)
         flat = every[n].ravel()
-        order = np.argsort(-flat, kind="stable")[:keep]
+        x = logits[n * W : (n + 1) * W, :vocab].astype(np.float64)
+        if done is not None:
+            x = np.where(done[n][:, None], 0.0, x)
+        beam, token = np.divmod(np.arange(W * vocab), vocab)
+        order = np.lexsort((token, -x.ravel(), beam, -flat))[:keep]
         for k, at in enumerate(order):
             if flat[at] == -np.inf:
                 break

@@ -216,15 +216,21 @@ __device__ __forceinline__ unsigned long long order_of(double x) {
 __device__ __forceinline__ double score_of(unsigned long long u) {
     return __builtin_bit_cast(double, u >> 63 ? u & ~(1ull << 63) : ~u);
 }
+// A candidate: of equal scores the lowest beam goes first, then the largest
+// logit, whose bits in order, turned round, are the lower half of `after`.
 struct Cand {
-    unsigned long long score;
-    int beam, token;
+    unsigned long long score, after;
+    int token;
 };
+__device__ __forceinline__ unsigned long long after_of(int beam, float logit) {
+    const unsigned u = __builtin_bit_cast(unsigned, logit + 0.0f);       // (-0 is 0)
+    return (unsigned long long)beam << 32 | (u >> 31 ? u : ~(u | 1u << 31));
+}
 
 template <bool F32> __global__ __launch_bounds__(1024) void beam_join_kernel(BeamArgs a, int in_lds) {
     typedef Step<F32> At;
     constexpr int E = F32 ? 4 : 2, V = At::V;
-    extern __shared__ unsigned long long keys[];           // [lists][K] scores, where they fit, and their steps and lanes
+    extern __shared__ unsigned long long keys[];           // [lists][K] scores, where they fit, and the lists
     __shared__ double lse[BEAM_SELECT_MAX], score[BEAM_SELECT_MAX];
     __shared__ unsigned char head[kMaxLists], ended[BEAM_SELECT_MAX];      // entries of a list that are taken; done
     __shared__ int2 group[BEAM_SELECT_MAX];                // the best maxima: list and entry
@@ -239,7 +245,7 @@ template <bool F32> __global__ __launch_bounds__(1024) void beam_join_kernel(Bea
     const float sc0 = a.scores[row0];
     const bool done0 = a.done && a.done[row0];
     const float2 first = lane < per ? a.ms[(long long)row0 * per + lane] : float2{-INFINITY, 0.0f};
-    int* places = (int*)(keys + lists * a.K);
+    float2* entries = (float2*)(keys + lists * a.K);
     constexpr int kEarly = 4;
     float2 early[kEarly];
 #pragma unroll
@@ -285,28 +291,34 @@ template <bool F32> __global__ __launch_bounds__(1024) void beam_join_kernel(Bea
             const int j = tid + u * blockDim.x;
             if (j < lists * a.K) {
                 keys[j] = key(j / a.K, j % a.K, early[u]);
-                places[j] = as_bits(early[u].y);
+                entries[j] = early[u];
             }
         }
         for (int j = tid + kEarly * blockDim.x; j < lists * a.K; j += blockDim.x) {
             const float2 e = from[j];
             keys[j] = key(j / a.K, j % a.K, e);
-            places[j] = as_bits(e.y);
+            entries[j] = e;
         }
         __syncthreads();
     }
     if (wave == 0) {
-        // The wave's best head by the score's halves, of equals the first list's:
-        // lists are in the order of beams and columns.
+        // The wave's best head by the score's halves.  Of equals the first beam's,
+        // of its (a large score takes the difference away) the largest logit,
+        // of equals the first list's: lists are in the order of beams and columns.
         unsigned long long top = 0, u = 0;
         int list = lane;
-        auto best = [&](int& owner) {
+        auto best = [&](int& owner, int h) {
             const unsigned hi = wave_umax((unsigned)(top >> 32));
             const unsigned lo = wave_umax((unsigned)(top >> 32) == hi ? (unsigned)top : 0u);
             u = (unsigned long long)hi << 32 | lo;
             const unsigned long long tie = __ballot(top == u);
             owner = __builtin_ctzll(tie);
-            return tie;
+            if (!u || !(tie & (tie - 1))) return;
+            const int w = (int)((unsigned)list / (unsigned)per), w0 = wave_min(top == u ? w : 0x7fffffff);
+            const bool mine = top == u && w == w0;
+            const float x = !mine || ended[w0] ? -INFINITY : in_lds ? entries[list * a.K + h].x : from[list * a.K + h].x;
+            const float most = wave_max(x);
+            owner = wave_min(mine && x == most ? list : 0x7fffffff) & 63;
         };
         int owner;
         if (in_lds && lists <= 64) {
@@ -317,7 +329,7 @@ template <bool F32> __global__ __launch_bounds__(1024) void beam_join_kernel(Bea
             if (lane < lists) top = mine[0];
             unsigned long long next = lane < lists && a.K > 1 ? mine[1] : 0;
             for (int k = 0; k < a.K; ++k) {
-                best(owner);
+                best(owner, h);
                 if (!u) break;
                 if (lane == owner) {
                     group[k] = int2{lane, h};
@@ -342,9 +354,8 @@ template <bool F32> __global__ __launch_bounds__(1024) void beam_join_kernel(Bea
             };
             look();
             for (int k = 0; k < a.K; ++k) {
-                const unsigned long long tie = best(owner);
+                best(owner, head[list]);
                 if (!u) break;
-                if (tie & (tie - 1)) owner = wave_min(top == u ? list : 0x7fffffff) & 63;
                 if (lane == owner) {
                     group[k] = int2{list, head[list]++};
                     look();
@@ -355,16 +366,17 @@ template <bool F32> __global__ __launch_bounds__(1024) void beam_join_kernel(Bea
     }
     __syncthreads();
     // the values that those are the maxima of, as far as they can be among the best
-    auto put = [&](unsigned long long u, int w, int token) {
-        cand[__hip_atomic_fetch_add(&count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP)] = Cand{u, w, token};
+    auto put = [&](unsigned long long u, int w, int token, float x) {
+        const int i = __hip_atomic_fetch_add(&count, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+        cand[i] = Cand{u, after_of(w, x), token};
     };
     for (int t = tid; t < a.K * E; t += blockDim.x) {
         int2 g = group[t / E];
         if (g.x < 0) continue;
-        g.y = in_lds ? places[g.x * a.K + g.y] : as_bits(from[g.x * a.K + g.y].y);
+        g.y = as_bits((in_lds ? entries[g.x * a.K + g.y] : from[g.x * a.K + g.y]).y);
         const int w = (int)((unsigned)g.x / (unsigned)per), row = n * a.W + w;
         if (ended[w]) {
-            if (t % E == 0) put(order_of(score[w]), w, a.end);
+            if (t % E == 0) put(order_of(score[w]), w, a.end, 0.0f);
             continue;
         }
         const int rank = (int)((unsigned)(g.x - w * per) / (unsigned)a.parts), c = g.y / 64 * kChunk + At::column(g.y % 64, t % E * V);
@@ -389,7 +401,7 @@ template <bool F32> __global__ __launch_bounds__(1024) void beam_join_kernel(Bea
             const float f = F32 ? f32_bits(x[e % 4]) : bf16_bits(e % 2 ? x[e / 2 % 4] >> 16 : x[e / 2 % 4] & 0xffffu);
             if (c + e >= cols || !(__builtin_fabsf(f) < INFINITY)) continue;
             const unsigned long long u = order_of(score[w] + ((double)f - lse[w]));
-            if (u >= least) put(u, w, rank * a.width + c + e);
+            if (u >= least) put(u, w, rank * a.width + c + e, f);
         }
     }
     __syncthreads();
@@ -401,14 +413,15 @@ template <bool F32> __global__ __launch_bounds__(1024) void beam_join_kernel(Bea
 #pragma unroll 4
         for (int j = 0; j < all; ++j) {
             const Cand o = cand[j];
-            k += o.score > c.score || (o.score == c.score && (o.beam < c.beam || (o.beam == c.beam && o.token < c.token)));
+            k += o.score > c.score || (o.score == c.score && (o.after < c.after || (o.after == c.after && o.token < c.token)));
         }
         if (k < a.K) {
             const long long o = (long long)n * a.K + k;
-            a.parents[o] = n * a.W + c.beam;
+            const int beam = (int)(c.after >> 32);
+            a.parents[o] = n * a.W + beam;
             a.tokens[o] = c.token;
             a.after[o] = (float)score_of(c.score);
-            if (a.done_after) a.done_after[o] = ended[c.beam] || c.token == a.end;
+            if (a.done_after) a.done_after[o] = ended[beam] || c.token == a.end;
         }
     }
     for (int k = tid; k < a.K; k += blockDim.x)
@@ -504,7 +517,7 @@ extern "C" int beam_select(const void* const* logits, const float* scores, const
     if (hipGetLastError() != hipSuccess) return RING_EHIP;
     const int entries = beams * P * c.parts * keep, in_lds = entries <= kLdsEntries;
     const dim3 block(64u * (beams < 4 ? 4 : beams < 16 ? beams : 16));
-    const size_t dyn = in_lds ? entries * 12 : 0;
+    const size_t dyn = in_lds ? entries * 16 : 0;
     if (dtype == RING_F32) hipLaunchKernelGGL(beam_join_kernel<true>, dim3((unsigned)N), block, dyn, s, a, in_lds);
     else hipLaunchKernelGGL(beam_join_kernel<false>, dim3((unsigned)N), block, dyn, s, a, in_lds);
     return hipGetLastError() == hipSuccess ? RING_OK : RING_EHIP;

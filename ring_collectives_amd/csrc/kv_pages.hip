@@ -540,9 +540,9 @@ __global__ __launch_bounds__(kThreads) void kv_compact_kernel(CompactArgs a) {
 }
 
 __global__ __launch_bounds__(256) void kv_renumber_kernel(CompactArgs a) {
-    // the first launch stopped: nothing here holds numbers of this call
-    if (seen(&a.status->code) != RING_OK) return;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    // (its own data lies past the counters: the record says what it said to the first launch)
+    if (!ws_ok(a.status, ws_record(a.status), a.zero, lane)) return;
     const int n = *a.used_after, stay = a.before[a.words], moves = n - stay;
     const int step = gridDim.x * 256, first = blockIdx.x * 256 + threadIdx.x;
     for (int i = first; i < a.n; i += step) a.free_pages[i] = a.first + i;

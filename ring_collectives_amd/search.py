@@ -19,11 +19,12 @@ def beam_select(logits, scores, parents, tokens, scores_after, vocab: int, done=
     beams, width; fp32 or bf16) are the columns of tokens r * width on, those
     from `vocab` on padding; scores (groups, beams) fp32.  parents, tokens
     (int32) and scores_after (fp32), (groups, places), get the candidates
-    scores + log softmax(logits) in order, best first, the lowest beam and then
-    token of equal ones: parents the rows of logits they go on from, -1 where
-    there are none left.  A beam of which done (uint8 or bool) is set goes on
-    as end_token with the score it has; done_after tells which places are done
-    or end with it.  Logits and scores that are not finite take no part."""
+    scores + log softmax(logits) in order, best first, of equal ones the lowest
+    beam, then the largest logit, then the lowest token: parents the rows of
+    logits they go on from, -1 where there are none left.  A beam of which done
+    (uint8 or bool) is set goes on as end_token with the score it has;
+    done_after tells which places are done or end with it.  Logits and scores
+    that are not finite take no part."""
     if ws is None:
         s, out = _shape(scores, 2, "scores"), _shape(parents, 2, "parents")
         ws = _new_ws(N.lib().beam_select_workspace_bytes(len(logits), s[0], s[1], out[1], _lead(logits, 2, "logits")[1]),

@@ -142,6 +142,21 @@ def test_select_takes_the_lowest_of_equals():
     assert parents.tolist() == [[0, 1, 2, 3] * 2] and tokens.tolist() == [[top[0]] * 4 + [top[1]] * 4]
 
 
+@pytest.mark.parametrize("W,P,keep", [(2, 1, 7), (2, 3, 7), (33, 4, 5), (64, 2, 64)])
+@pytest.mark.parametrize("score,std", [(-1e25, 1.0), (0.0, 1e-25)])
+def test_select_orders_by_logits_where_scores_are_equal(score, std, W, P, keep):
+    """Logits that differ, and scores that do not in 64 bits: next to a large
+    score, and next to the logarithm of the number of tokens."""
+    note("beam_select equal scores W=%d P=%d %g" % (W, P, score))
+    x = torch.randn(W, 5001, generator=torch.Generator().manual_seed(W)) * std
+    s, done = np.full((1, W), score, np.float32), np.zeros((1, W), bool)
+    done[0, 0] = True
+    parents, tokens, _, _ = run_select(split(x, P, -(-5001 // P // 8) * 8, torch.float32), s, 5001, keep, done, 3)
+    ep, et = osr.select(x.numpy(), s, 5001, keep, done, 3)[:2]
+    assert et[0, 1:].tolist() == x[1].argsort(descending=True)[:keep - 1].tolist()
+    assert parents.tolist() == ep.tolist() and tokens.tolist() == et.tolist()
+
+
 @pytest.mark.parametrize("base", [-1e4, 0.0, 3e4])
 def test_select_at_any_level(base):
     """Logits far from zero, ascending (every step raises the maximum) and descending."""
