@@ -25,7 +25,12 @@
 // and Q alike.  Values go to LDS as bf16 and are read transposed for
 // O^T += V^T P^T, whose B operand are S^T's accumulators rounded to bf16.
 //
-// The cache read bounds it: 4.25 bits a value.
+// The cache read bounds it, 4.25 bits a value: 4 rows of 120000 keys of 2 heads
+// on 4 ranks, 382 MB, take 63 us, 6.1 TB/s, what reads alone reach here.  24
+// groups of 4 beams of 3000 keys, 2700 of them shared, take 24 us for 89 MB read
+// and 12 MB of parts written: 2.5 before the first load (lengths, costs and the
+// search), 14 at 6.3 TB/s, then 4 until the last wave, whose pieces and pages
+// the costs do not foresee.  The launches that join take 5 to 6.
 #include "kv4_core.h"
 
 #include <hip/hip_runtime.h>
@@ -77,6 +82,7 @@ struct Kv4DecodeArgs {
     long long q_stride, o_stride;
     int P, B, group, Hq, Hkv, width, shift, pages;
     int blocks, waves;                 // workgroups and waves of a (rank, key head)
+    int planners;                      // workgroups that write the items' parts
     int shared_cost;                   // of a tile of shared keys
     int whole;                         // every row's keys are one workgroup's
     int shared_rbs, own_rbs, own_rows; // row blocks of a group, of a row; rows of an own part
@@ -420,6 +426,7 @@ template <int D, int NT> __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void
     __shared__ int part_sum[kWaves], found[2];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int units = a.P * a.Hkv, unit = blockIdx.x % units, blk = blockIdx.x / units;
+    const int planner = (int)blockIdx.x - units * a.blocks;
     const Items n = items_of(a);
     int *own = lens + a.B, *few = own + a.B;
     if (blockIdx.x == 0 && tid == 0) ws_add_data(a.status, a.data);
@@ -474,13 +481,14 @@ template <int D, int NT> __global__ __launch_bounds__(256, NT == 1 ? 3 : 2) void
         int quota = (total + a.waves - 1) / a.waves;       // of a wave
         if (quota < kMinCost) quota = kMinCost;
         if (quota < a.shared_cost) quota = a.shared_cost;
-        if (unit == 0) {                                   // for the launch that joins: an item a workgroup in turn
+        if (planner >= 0) {                                // for the launch that joins
             int x = before;
             for (int i = i0; i < i1; ++i) {
                 const int c = cost(i);
-                if (i % a.blocks == blk) a.parts[i] = item_parts(x, x + c, tile_cost(i), total, quota);
+                if (i % a.planners == planner) a.parts[i] = item_parts(x, x + c, tile_cost(i), total, quota);
                 x += c;
             }
+            return;
         }
         // a tile is the wave's in whose share its cost begins
         const long long block0 = (long long)blk * kWaves * quota;
@@ -717,8 +725,10 @@ extern "C" int tp_attention_decode_kv4(const void* const* q, const void* const* 
     hipStream_t s = (hipStream_t)stream;
     const int units = P * Hkv;
     if (a.whole) a.blocks = B * c.own_rbs;
-    if ((long long)units * a.blocks >= (1LL << 31)) return RING_EUNSUPPORTED;
-    const dim3 grid((unsigned)(units * a.blocks));
+    // (workgroups of their own, the last to start: within others' time 0.7 us of theirs)
+    a.planners = a.whole ? 0 : (int)((c.items + 255) / 256);
+    if ((long long)units * a.blocks + a.planners >= (1LL << 31)) return RING_EUNSUPPORTED;
+    const dim3 grid((unsigned)(units * a.blocks + a.planners));
     const size_t dyn = (2 * (size_t)B + (shared ? B / group : 0)) * sizeof(int);
     const long long rows = (long long)P * B * Hq;
     const bool few = rows <= 2LL * dev_info().cus;           // 256 lanes a row, else 64

@@ -15,8 +15,13 @@
 //     are no worse than the last maximum in order.
 // (Lists of values instead of maxima took a wave 144 operations where one is
 // put in, 25 so: of 512 rows of 100003 logits two thirds of all operations.)
-// The logits read bound it: an exponential is a sixteenth of the rate of a
-// plain operation, four exponentials a cycle and SIMD.
+// The logits read bound it, and an exponential a logit, at a quarter of the
+// rate of a plain operation: the 184 MB of 460 such rows take 36 us, 5.1 TB/s
+// with the VALU 63% busy, and their join 8.  Four rows of 8000 take 5 and 6 us:
+// launches and five trips to memory one after another.  A join by a group's
+// last workgroup to finish instead of a launch was no faster (44 us for the
+// large case in all, 43 so; 11.2 for the small one, 10.5 so): what it reads
+// then has to pass the caches.
 //
 // The sum is of fp32 exponentials (the exponent's product with log2 e in two
 // parts, so that its error is the rounding of x - m alone), added 16 at a time
@@ -433,8 +438,9 @@ template <bool F32> __global__ __launch_bounds__(1024) void beam_join_kernel(Bea
         }
 }
 
-// Parts of a row of one rank: as many as give every SIMD four waves, as far as
-// there are steps, and a group's lists are few enough.
+// Parts of a row of one rank: as many as give every SIMD four waves (eight, each
+// with a list of its own to fill, took 71 us where four took 58), as far as
+// there are steps, and few enough that the join has a list a lane.
 struct BeamCut {
     int parts, cols;
 };

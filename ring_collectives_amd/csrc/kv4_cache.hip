@@ -8,7 +8,10 @@
 // Memory bounds both.  Four lanes hold a block, 16 bytes of bf16 each, which
 // are four bytes of codes; a wave takes one head of kTokens tokens, keys or
 // values, so what it writes lies together where the tokens' slots do, and its
-// loads are in flight together.
+// loads are in flight together.  16381 tokens of 4 heads of 64 on 4 ranks, 67 MB
+// of bf16 and 18 of cache: written in 20 us, read in 15, 4.2 and 5.7 TB/s with
+// the bf16 rows past the caches (both 41 us with them, 35 so).  32 tokens take 4
+// us each, an empty launch and three trips to memory.
 #include "kv4_core.h"
 
 #include <hip/hip_runtime.h>
