@@ -166,7 +166,8 @@ int tp_kv4_read(const void *const *cache, const long long *slots, void *const *k
  * 32 (row, head of the group that shares a key head).  shared[g] is clamped to
  * the lengths of the group's rows.
  * Products in bf16 on the matrix cores (4-bit values are exact in bf16) with
- * fp32 sums, statistics in fp32, the softmax weights rounded to bf16.
+ * fp32 sums, statistics in fp32, the softmax weights rounded to bf16 and summed
+ * as rounded.
  * Lengths are clamped to [0, table_stride * page_size]; keys whose page lies
  * outside [0, pages) take no part; a row without keys gives o = 0.  Rows of the
  * cache that are no key of a row never reach its result.

@@ -26,7 +26,7 @@
 // O^T += V^T P^T, whose B operand are S^T's accumulators rounded to bf16.
 //
 // The cache read bounds it, 4.25 bits a value: 4 rows of 120000 keys of 2 heads
-// on 4 ranks, 382 MB, take 63 us, 6.1 TB/s, what reads alone reach here.  24
+// on 4 ranks, 382 MB, take 62 us, 6.2 TB/s, what reads alone reach here.  24
 // groups of 4 beams of 3000 keys, 2700 of them shared, take 24 us for 89 MB read
 // and 12 MB of parts written: 2.5 before the first load (lengths, costs and the
 // search), 14 at 6.3 TB/s, then 4 until the last wave, whose pieces and pages
@@ -129,24 +129,21 @@ __device__ __forceinline__ int clamp_len(int n, int width, int shift) {
 }
 
 // The running state of 16 rows, one a lane of 16: a lane has every fourth
-// block of four of the values, and its own quarter of the sum.
+// block of four of the values, and the sum of the weights four times (of which
+// only the first is kept up when the maximum rises).
 template <int D> struct State {
-    f32x4 o[D / 16];
-    float mc, l;
+    f32x4 o[D / 16], l;
+    float mc;
     __device__ __forceinline__ void init() {
 #pragma unroll
         for (int db = 0; db < D / 16; ++db) o[db] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         mc = -INFINITY;
-        l = 0.0f;
+        l = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 };
 __device__ __forceinline__ float max_quarters(float x) {
     x = fmaxf(x, __shfl_xor(x, 16));
     return fmaxf(x, __shfl_xor(x, 32));
-}
-__device__ __forceinline__ float sum_quarters(float x) {
-    x += __shfl_xor(x, 16);
-    return x + __shfl_xor(x, 32);
 }
 
 // One tile of a wave, as loaded: half h holds keys 16 h + lane % 16.
@@ -176,6 +173,9 @@ __device__ __forceinline__ void run_tiles(State<D> (&st)[NT], const bf16x8 (&q)[
     const unsigned mask = (1u << f.shift) - 1;
     const int write = at + i * kRowBytes<D> + quarter * (D / 2);
     const int read = at + (4 * quarter + (i >> 2)) * kRowBytes<D> + (i & 3) * 8;
+    bf16x8 ones;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ones[e] = (__bf16)1.0f;
     // 64 pages are looked up at a time; loads within them wait for no look-up
     for (int jc = j0; jc < j1;) {
         const int first = (int)((unsigned)jc * kKeys >> f.shift);
@@ -271,7 +271,7 @@ __device__ __forceinline__ void run_tiles(State<D> (&st)[NT], const bf16x8 (&q)[
                     const float mn = fmaxf(st[n].mc, max_quarters(mx));
                     const float alpha = mn == -INFINITY ? 1.0f : exp2_hw(st[n].mc - mn);
                     st[n].mc = mn;
-                    st[n].l *= alpha;
+                    st[n].l[0] *= alpha;
 #pragma unroll
                     for (int db = 0; db < D / 16; ++db)
 #pragma unroll
@@ -283,11 +283,13 @@ __device__ __forceinline__ void run_tiles(State<D> (&st)[NT], const bf16x8 (&q)[
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int v = 0; v < 4; ++v) {
-                        w[4 * h + v] = exp2_hw(__builtin_fmaf(s[n][h][v], f.c, -sub));
-                        st[n].l += w[4 * h + v];
-                    }
+                    for (int v = 0; v < 4; ++v) w[4 * h + v] = exp2_hw(__builtin_fmaf(s[n][h][v], f.c, -sub));
                 p[n] = __builtin_convertvector(w, bf16x8);
+                // the sum is of the weights as rounded, so that where few keys have
+                // most of the weight its rounding cancels (3 rows of 200 keys are off
+                // by 1.7e-3 so, 2.0e-3 with the sum of unrounded ones), and a product
+                // with ones (66.5 us for 4 rows of 120000 keys, 67.5 with additions)
+                st[n].l = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, p[n], st[n].l, 0, 0, 0);
             }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
@@ -360,7 +362,7 @@ __device__ __forceinline__ void run_piece(const Kv4DecodeArgs& a, const Fixed& f
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int row = (rb * NT + nt) * 16 + i, at_row = nt * 16 + i;
-            const float l = sum_quarters(st[nt].l);
+            const float l = st[nt].l[0];
             if (row >= rows) continue;
             if (w.direct) {
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
@@ -380,7 +382,7 @@ __device__ __forceinline__ void run_piece(const Kv4DecodeArgs& a, const Fixed& f
     static_assert(16 * D * 4 <= kTile, "a wave's output fits its tile");
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-        const float l = sum_quarters(st[nt].l);
+        const float l = st[nt].l[0];
         if (quarter == 0) {
             wave_ml[wave][i][0] = st[nt].mc;
             wave_ml[wave][i][1] = l;

@@ -527,6 +527,10 @@ def check_decode_kv4(q, cache, table, lengths, page, shared=None, group=1, scale
                 k, v = np.array(ks).reshape(-1, D), np.array(vs).reshape(-1, D)
                 qq = f64(q[r][b, h * G:(h + 1) * G])
                 want, _, bound, _, _, _ = oa.attention(qq, k, v, np.ones((G, len(k)), bool), scale or D ** -0.5)
+                # the oracle's sum is of weights w as they are; the call's is of the
+                # rounded w (1 + d), |d| <= UB, so that o is off by sum w d (v - o)
+                # instead of sum w d v: UB |o| more at most, as the w add up to 1
+                bound = bound + oa.UB * np.abs(want)
                 within(o[r][b, h * G:(h + 1) * G], want, bound, "rank %d row %d head %d" % (r, b, h))
     return ws
 
