@@ -76,7 +76,8 @@ size_t beam_select_workspace_bytes(int P, int N, int beams, int keep, int width)
  *                  the others get a page of their own
  *   n_copies       how many
  *   shared         [B_after / group] or NULL: the leading tokens whose pages all
- *                  rows of each `group` rows in turn have in common
+ *                  rows of each `group` rows in turn have in common (a copy
+ *                  that no page is left for is in common with none)
  *   used_after, free_pages   the free pages are free_pages[*used .. n_free)
  *                  before and free_pages[*used_after .. n_free) after.  Pages
  *                  of the old table that no new row holds become free.

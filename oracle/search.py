@@ -84,8 +84,8 @@ def fork(table, lengths, parents, keep, free, used, page, pages, group, width=0)
     held = {e for row in rows for e in row}
     gone = sorted(before - held)
     full = {e for row, n in zip(rows, lens) for e in row[:n // page]}
-    copies, writes = [], set(full)
-    for row, n in zip(rows, lens):
+    copies, writes, own = [], set(full), [list(row) for row in rows]      # own: copies told apart, also where no page is left
+    for i, (row, n) in enumerate(zip(rows, lens)):
         if n % page and 0 <= row[-1] < pages:
             if row[-1] in writes:
                 k = len(copies)
@@ -93,6 +93,7 @@ def fork(table, lengths, parents, keep, free, used, page, pages, group, width=0)
                 to = gone[k] if k < len(gone) else free[at] if 0 <= at < len(free) else -1
                 copies.append((row[-1], to))
                 row[-1] = to
+                own[i][-1] = "copy %d" % i
             else:
                 writes.add(row[-1])
     after = used + len(copies) - len(gone)
@@ -101,7 +102,7 @@ def fork(table, lengths, parents, keep, free, used, page, pages, group, width=0)
             free[after + k] = e
     shared = []
     for g in range(len(rows) // group):
-        rs, ls = rows[g * group:(g + 1) * group], lens[g * group:(g + 1) * group]
+        rs, ls = own[g * group:(g + 1) * group], lens[g * group:(g + 1) * group]
         n = min(len(r) for r in rs)
         same = next((j for j in range(n) if any(r[j] != rs[0][j] for r in rs)), None)
         shared.append(min(ls) if same is None else min(min(ls), same * page))

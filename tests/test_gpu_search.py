@@ -257,6 +257,13 @@ def test_fork_when_pages_run_out():
     check_fork([[0, 1], [2, 3]], [20, 25], [0, 0, 0], None, [], 0, 16, 10, 1)
 
 
+def test_fork_of_one_row_into_a_group_when_pages_run_out():
+    """Copies that get no page are not in common, though the table holds -1 for each."""
+    for spare in (0, 1, 2):
+        got, _ = check_fork([[0, 1]], [20], [0] * 8, None, [1, 0] + [2, 3][:spare], 2, 16, 2 + spare, 4)
+        assert got[4].tolist() == [16, 16] and got[5][0] == 9
+
+
 def test_fork_passes_on_what_is_no_page():
     check_fork([[-1, 5, 900], [3, -4, 2]], [40, 40], [0, 0, 1, 1], None, list(range(6, 20)), 0, 16, 20, 2)
     check_fork([[5, 6, 7]], [-3], [0], None, [1, 2], 0, 16, 10, 1)
