@@ -91,7 +91,7 @@ size_t beam_select_workspace_bytes(int P, int N, int beams, int keep, int width)
  * gives the same outputs, free_pages' entries from *used on being read only.
  * None of the outputs may be an input's memory but free_pages, which is both.
  * B, B_after <= KV_FORK_MAX_ROWS, and group divides B_after.  B_after = 0 frees
- * every page.
+ * every page.  table_stride * page_size and pages are below 2^31 - 2^20.
  */
 int kv_fork(const int *block_table, const int *lengths, const int *parents, const int *keep, int *free_pages,
             const int *used, int *table_after, int *lengths_after, int *copies, int *n_copies, int *shared,
@@ -109,7 +109,8 @@ size_t kv_fork_workspace_bytes(int B_after, int pages);
  *   copies       [n_free / 2][2] pages to copy, from and to, then -1; n_copies
  *   free_pages   [n_free] first_page, first_page + 1, ...; used_after = n, so
  *                that free_pages[n ..] are the free pages
- * B <= KV_FORK_MAX_ROWS.
+ * B <= KV_FORK_MAX_ROWS; table_stride * page_size and n_free are below 2^31 -
+ * 2^20, first_page + n_free below 2^31.
  */
 int kv_compact(const int *block_table, const int *lengths, int *table_after, int *free_pages, int *copies,
                int *n_copies, int *used_after, int B, int n_free, int table_stride, int page_size, int first_page,

@@ -667,6 +667,8 @@ int shift_of(int page_size) {
     return s;
 }
 bool page_size_ok(int page_size) { return page_size >= 1 && !(page_size & (page_size - 1)) && page_size <= (1 << 20); }
+// Places of a row and pages: below 2^31 by more than any loop's step.
+constexpr long long kMaxCount = (1LL << 31) - (1 << 20);
 bool misaligned4(const void* p) { return (uintptr_t)p & 3; }
 
 size_t fork_words(int pages) { return ((size_t)pages + 31) / 32; }
@@ -693,7 +695,7 @@ extern "C" int kv_fork(const int* block_table, const int* lengths, const int* pa
                        void* ws, size_t ws_bytes, void* stream) {
     if (B < 0 || B_after < 0 || n_free < 0 || table_stride < 0 || pages < 0 || group < 1 || B_after % group) return RING_EINVAL;
     if (!page_size_ok(page_size)) return RING_EINVAL;
-    if (B > KV_FORK_MAX_ROWS || B_after > KV_FORK_MAX_ROWS || (long long)table_stride * page_size >= (1LL << 31))
+    if (B > KV_FORK_MAX_ROWS || B_after > KV_FORK_MAX_ROWS || (long long)table_stride * page_size >= kMaxCount || pages >= kMaxCount)
         return RING_EUNSUPPORTED;
     if (!used || !used_after || !n_copies || (B && !lengths) || (B && table_stride && !block_table) || (n_free && !free_pages) ||
         (B_after && (!parents || !lengths_after || !copies)) || (B_after && table_stride && !table_after))
@@ -757,7 +759,8 @@ extern "C" int kv_compact(const int* block_table, const int* lengths, int* table
                           int* n_copies, int* used_after, int B, int n_free, int table_stride, int page_size, int first_page,
                           void* ws, size_t ws_bytes, void* stream) {
     if (B < 0 || n_free < 0 || table_stride < 0 || first_page < 0 || !page_size_ok(page_size)) return RING_EINVAL;
-    if (B > KV_FORK_MAX_ROWS || (long long)table_stride * page_size >= (1LL << 31) || (long long)first_page + n_free >= (1LL << 31))
+    if (B > KV_FORK_MAX_ROWS || (long long)table_stride * page_size >= kMaxCount || n_free >= kMaxCount ||
+        (long long)first_page + n_free >= (1LL << 31))
         return RING_EUNSUPPORTED;
     if (!used_after || !n_copies || (B && !lengths) || (B && table_stride && (!block_table || !table_after)) ||
         (n_free && !free_pages) || (n_free > 1 && !copies))

@@ -64,7 +64,9 @@ def fork(B=4, B2=4, group=2, n_free=20, W=3, page=16, pages=30, ws=WS, **kw):
     (dict(n_free=-1), N.RING_EINVAL), (dict(W=-1), N.RING_EINVAL), (dict(pages=-1), N.RING_EINVAL), (dict(page=0), N.RING_EINVAL),
     (dict(page=24), N.RING_EINVAL), (dict(page=1 << 21), N.RING_EINVAL), (dict(B=8193), N.RING_EUNSUPPORTED),
     (dict(B2=8194), N.RING_EUNSUPPORTED), (dict(W=1 << 27), N.RING_EUNSUPPORTED), (dict(table=None), N.RING_EINVAL),
-    (dict(lens=None), N.RING_EINVAL), (dict(parents=None), N.RING_EINVAL), (dict(free=None), N.RING_EINVAL),
+    # counts that a loop's step would carry past 31 bits
+    (dict(W=(1 << 27) - 1), N.RING_EUNSUPPORTED), (dict(W=(1 << 31) - (1 << 20), page=1), N.RING_EUNSUPPORTED),
+    (dict(pages=(1 << 31) - (1 << 20)), N.RING_EUNSUPPORTED), (dict(lens=None), N.RING_EINVAL), (dict(parents=None), N.RING_EINVAL), (dict(free=None), N.RING_EINVAL),
     (dict(used=None), N.RING_EINVAL), (dict(table2=None), N.RING_EINVAL), (dict(lens2=None), N.RING_EINVAL),
     (dict(copies=None), N.RING_EINVAL), (dict(n=None), N.RING_EINVAL), (dict(used2=None), N.RING_EINVAL),
     (dict(used2=0x5000), N.RING_EINVAL), (dict(lens2=0x2000), N.RING_EINVAL), (dict(table2=0x1000), N.RING_EINVAL),
@@ -84,6 +86,7 @@ def compact(B=4, n=20, W=3, page=16, first=0, ws=WS, **kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(B=-1), N.RING_EINVAL), (dict(n=-1), N.RING_EINVAL), (dict(W=-1), N.RING_EINVAL), (dict(first=-1), N.RING_EINVAL),
     (dict(page=3), N.RING_EINVAL), (dict(B=8193), N.RING_EUNSUPPORTED), (dict(W=1 << 27), N.RING_EUNSUPPORTED),
+    (dict(W=(1 << 31) - (1 << 20), page=1), N.RING_EUNSUPPORTED), (dict(n=(1 << 31) - (1 << 20)), N.RING_EUNSUPPORTED),
     (dict(first=(1 << 31) - 10), N.RING_EUNSUPPORTED), (dict(table=None), N.RING_EINVAL), (dict(lens=None), N.RING_EINVAL),
     (dict(table2=None), N.RING_EINVAL), (dict(table2=0x1000), N.RING_EINVAL), (dict(free=None), N.RING_EINVAL),
     (dict(copies=None), N.RING_EINVAL), (dict(nc=None), N.RING_EINVAL), (dict(used2=None), N.RING_EINVAL),
