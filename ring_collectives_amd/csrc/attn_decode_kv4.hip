@@ -41,7 +41,11 @@ namespace {
 constexpr int kWaves = 4;
 constexpr int kKeys = 32;              // of a tile
 constexpr int kOwnCost = 2;            // of a tile of own keys
-constexpr int kItemCost = 4;           // of an item besides its tiles: its look-ups, and storing its part
+// Of an item besides its tiles: its look-ups, and storing its part.  60 groups
+// of 4 rows of 1000 keys on 8 ranks 43.7 us, with half of it 44.9; 6 groups of 16
+// of 3000 27.6 and 28.6; 2 groups of 4 of 300 12.0 and 13.0; 8 groups of 8 of
+// 3000 24.0 and 23.9.
+constexpr int kItemCost = 8;
 // Rows of at most as many tiles are a workgroup's each.  3 requests of up to 600 /
 // 1100 keys on 2 ranks of 2 key heads 7.6 / 9.2 us so, shared out 12; 64 on 4
 // ranks 12.7 / 17.5, shared out 17.9 / 21.7, of 2200 27.7 and 29.7; but the only
