@@ -300,14 +300,25 @@ template <bool LDS> __device__ __forceinline__ void finish_fork(const ForkArgs& 
 
 // Where tables and pages are few, one workgroup does it all with its sets in
 // LDS: two trips to memory (lengths, then entries, all in flight together) and
-// none to the sets.  32 rows of 44 pages 9.4 us by the kernel below, 6.7 so.
+// none to the sets.  The call takes 5.1 us instead of the 8.0 of the kernel below
+// for 4 rows of 7 entries, 6.0 and 9.4 for 32 of 46, 7.6 and 9.4 for 16 of 252,
+// and as long as it, 10.4 and 11, at the limits (96 of 77, 240 of 34).
 constexpr int kSmallRows = 256, kSmallEntries = 8192, kSmallPages = 8192;
+
+// x / y of numbers up to kSmallEntries: the quotient of x + 1/2 is 1 / 2y or more
+// from a whole number, and the fp32 product off by less than a hundredth of that.
+struct SmallDiv {
+    float inv;
+    int y;
+    __device__ __forceinline__ explicit SmallDiv(int n) : inv(1.0f / (float)n), y(n) {}
+    __device__ __forceinline__ int operator()(int x) const { return (int)(((float)x + 0.5f) * inv); }
+};
 __global__ __launch_bounds__(kThreads) void kv_fork_small_kernel(ForkArgs a) {
     __shared__ int rows[4 * kSmallRows], entry[kSmallEntries], owner[kSmallPages];
     __shared__ int parent[kSmallRows], tokens[kSmallRows], lengths[kSmallRows], apart[kSmallRows];
     __shared__ unsigned sets[3][kSmallPages / 32];
     __shared__ unsigned long long last[kSmallRows];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), page = 1 << a.shift;
+    const int tid = threadIdx.x, page = 1 << a.shift;
     const int used = *a.used;
     int p0 = -1, keep0 = 0x7fffffff;
     if (tid < a.B2) {
@@ -334,50 +345,43 @@ __global__ __launch_bounds__(kThreads) void kv_fork_small_kernel(ForkArgs a) {
     }
     __syncthreads();
     auto held = [&](int n) { return (n + page - 1) >> a.shift; };
-    // new rows, then old ones: four a wave at a time, their loads in flight together
+    // the entries of new rows and of old ones, one after the other over the
+    // threads (a wave a row took 23 us for 240 rows of 34)
     static_assert(kSmallPages / 32 <= kThreads, "a word of a set a thread");
     constexpr int U = 4;
-    for (int r0 = wave; r0 < a.B2 + a.B; r0 += U * kRowWaves)
-        for (int j = lane; j < a.width; j += 64) {
-            int e[U];
+    const SmallDiv by_width(a.width), by_group(a.group);
+    const int fresh = a.B2 * a.width, old = a.B * a.width, both = fresh > old ? fresh : old;
+    for (int x0 = tid; x0 < both; x0 += U * kThreads) {
+        int e[U], f[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = r0 + u * kRowWaves, b = i < a.B2 ? parent[i] : i - a.B2;
-                e[u] = i < a.B2 + a.B && j < held(i < a.B2 ? tokens[i] : lengths[b]) ? a.table[b * a.width + j] : -1;
-            }
+        for (int u = 0; u < U; ++u) {
+            const int x = x0 + u * kThreads, i = by_width(x), j = x - i * a.width;
+            e[u] = x < fresh && j < held(tokens[i]) ? a.table[parent[i] * a.width + j] : -1;
+            f[u] = x < old && j < held(lengths[i]) ? a.table[x] : -1;
+        }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int i = r0 + u * kRowWaves;
-                const bool valid = is_page(e[u], a.pages);
-                if (i >= a.B2) {
-                    if (valid) mark<true>(sets[0], e[u]);
-                    continue;
-                }
-                const bool part = j == tokens[i] >> a.shift && j < held(tokens[i]);
-                entry[i * a.width + j] = e[u];
-                if (!part || !valid) a.table_after[i * a.width + j] = e[u];
-                if (!valid) continue;
-                if (part) {
-                    mark<true>(sets[2], e[u]);
-                    raise_to<true>(owner + e[u], a.B2 - i);
-                    last[i] = (unsigned long long)(unsigned)j << 32 | (unsigned)(e[u] + 1);
-                } else {
-                    mark<true>(sets[1], e[u]);
-                }
+        for (int u = 0; u < U; ++u) {
+            const int x = x0 + u * kThreads, i = by_width(x), j = x - i * a.width;
+            if (is_page(f[u], a.pages)) mark<true>(sets[0], f[u]);
+            if (x >= fresh) continue;
+            const bool valid = is_page(e[u], a.pages), part = j == tokens[i] >> a.shift && j < held(tokens[i]);
+            entry[x] = e[u];
+            if (!part || !valid) a.table_after[x] = e[u];
+            if (valid) mark<true>(sets[part ? 2 : 1], e[u]);
+            if (valid && part) {
+                raise_to<true>(owner + e[u], a.B2 - i);
+                last[i] = (unsigned long long)(unsigned)j << 32 | (unsigned)(e[u] + 1);
             }
         }
+    }
     __syncthreads();
     if (a.shared && a.group > 1)
-        for (int i = wave; i < a.B2; i += kRowWaves) {
-            if (i % a.group == 0) continue;
-            const int n = held(tokens[i] < tokens[i - 1] ? tokens[i] : tokens[i - 1]);
-            for (int j0 = 0; j0 < n; j0 += 64) {
-                const int j = j0 + lane;
-                const unsigned long long other = __ballot(j < n && entry[i * a.width + j] != entry[(i - 1) * a.width + j]);
-                if (!other) continue;
-                if (lane == 0) raise_to<true>(apart + i / a.group, room - ((j0 + __builtin_ctzll(other)) << a.shift));
-                break;
-            }
+        for (int x = tid; x < fresh; x += kThreads) {
+            const int i = by_width(x), j = x - i * a.width, g = by_group(i);
+            if (i == g * a.group || j >= held(tokens[i] < tokens[i - 1] ? tokens[i] : tokens[i - 1])) continue;
+            // where this row is another than the one above, for the first time or again
+            if (entry[x] != entry[x - a.width] && (!j || entry[x - 1] == entry[x - 1 - a.width]))
+                raise_to<true>(apart + g, room - (j << a.shift));
         }
     __syncthreads();
     a.old = sets[0];
@@ -569,32 +573,29 @@ __global__ __launch_bounds__(256) void kv_renumber_kernel(CompactArgs a) {
 }
 
 // Where tables and pools are few, one workgroup does it all, sets, moves and
-// table in LDS: 9 rows of 32 pages and a pool of 300 4.8 us instead of 6.5 and 2.7 by two kernels.
+// table in LDS: the call takes 5.0 us instead of 9.9 for 9 rows of 32 entries and
+// a pool of 300, 7.7 and 12.7 for 256 of 29 and a pool of 8000.
 __global__ __launch_bounds__(kThreads) void kv_compact_small_kernel(CompactArgs a) {
-    __shared__ int entry[kSmallEntries], to[kSmallPages / 2], lengths[kSmallRows], before[kSmallPages / 32], below;
+    __shared__ int to[kSmallPages / 2], lengths[kSmallRows], before[kSmallPages / 32], below;
     __shared__ unsigned live[kSmallPages / 32];
-    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int tid = threadIdx.x;
     if (tid < a.B) lengths[tid] = held_pages(a, tid);
     if (tid < a.words) live[tid] = 0;
     __syncthreads();
-    constexpr int U = 4;
-    for (int b0 = wave; b0 < a.B; b0 += U * kRowWaves)
-        for (int j = lane; j < a.width; j += 64) {
-            int e[U];
+    constexpr int U = kSmallEntries / kThreads;
+    const SmallDiv by_width(a.width);
+    int e[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int b = b0 + u * kRowWaves;
-                e[u] = b < a.B && j < lengths[b] ? a.table[b * a.width + j] : -1;
-            }
+    for (int u = 0; u < U; ++u) {
+        const int x = tid + u * kThreads, b = by_width(x);
+        e[u] = x < a.B * a.width && x - b * a.width < lengths[b] ? a.table[x] : -1;
+    }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int b = b0 + u * kRowWaves;
-                if (b >= a.B) break;
-                entry[b * a.width + j] = e[u];
-                const long long i = (long long)e[u] - a.first;
-                if (j < lengths[b] && i >= 0 && i < a.n) mark<true>(live, (int)i);
-            }
-        }
+    for (int u = 0; u < U; ++u) {
+        const int x = tid + u * kThreads, b = by_width(x);
+        const long long i = (long long)e[u] - a.first;
+        if (x < a.B * a.width && x - b * a.width < lengths[b] && i >= 0 && i < a.n) mark<true>(live, (int)i);
+    }
     __syncthreads();
     const unsigned bits = tid < a.words ? live[tid] : 0u;
     int n;
@@ -613,12 +614,14 @@ __global__ __launch_bounds__(kThreads) void kv_compact_small_kernel(CompactArgs 
     __syncthreads();
     for (int i = tid; i < a.n; i += kThreads) a.free_pages[i] = a.first + i;
     for (int i = moves + tid; i < a.n / 2; i += kThreads) a.copies[2 * i] = a.copies[2 * i + 1] = -1;
-    for (int x = tid; x < a.B * a.width; x += kThreads) {
-        int e = entry[x];
-        const long long i = (long long)e - a.first;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int x = tid + u * kThreads;
+        if (x >= a.B * a.width) break;
+        const long long i = (long long)e[u] - a.first;
         // (what is no row's is -1 here, and before the pool)
-        if (i >= n && i < a.n) e = to[before[i >> 5] + __builtin_popcount(live[i >> 5] & ((1u << (i & 31)) - 1)) - stay];
-        a.table_after[x] = e;
+        if (i >= n && i < a.n) e[u] = to[before[i >> 5] + __builtin_popcount(live[i >> 5] & ((1u << (i & 31)) - 1)) - stay];
+        a.table_after[x] = e[u];
     }
     if (tid == 0) {
         *a.used_after = n;
