@@ -217,7 +217,9 @@ def fork_state(B, page, longest, width, spare, seed, common=0.6, group=1):
 
 @pytest.mark.parametrize("B,B2,group,page,longest,width", [
     (1, 1, 1, 16, 5, 1), (4, 4, 4, 16, 100, 8), (4, 8, 2, 16, 100, 7), (6, 3, 3, 1, 9, 12), (33, 40, 5, 8, 600, 76), (64, 64, 8, 16, 1500, 130),
-    (100, 1000, 4, 4, 70, 20), (1030, 1030, 5, 16, 300, 19), (2048, 1025, 1, 32, 400, 13), (8192, 8192, 8, 16, 60, 5), (3, 8192, 1, 16, 500, 40)])
+    (100, 1000, 4, 4, 70, 20), (1030, 1030, 5, 16, 300, 19), (2048, 1025, 1, 32, 400, 13), (8192, 8192, 8, 16, 60, 5), (3, 8192, 1, 16, 500, 40),
+    # rows of several waves' pieces
+    (3, 6, 2, 1, 5000, 5003), (1, 4, 4, 16, 40000, 2501), (6, 4, 4, 2, 2050, 1025), (20, 30, 3, 1, 2049, 2048)])
 @pytest.mark.parametrize("cut", [False, True])
 def test_fork(B, B2, group, page, longest, width, cut):
     note("kv_fork B=%d to %d group=%d page=%d cut=%s" % (B, B2, group, page, cut))
@@ -320,7 +322,8 @@ def check_compact(table, lengths, first, pool, page, ws=None):
 
 @pytest.mark.parametrize("B,page,longest,width,spare,first", [
     (1, 16, 10, 1, 0, 0), (1, 16, 10, 1, 1, 5), (3, 16, 100, 8, 20, 0), (40, 8, 300, 40, 500, 3), (200, 32, 2500, 80, 9000, 0),
-    (1500, 16, 90, 7, 0, 1), (8192, 1, 6, 6, 100, 0), (20, 16, 900, 60, 200000, 77)])
+    (1500, 16, 90, 7, 0, 1), (8192, 1, 6, 6, 100, 0), (20, 16, 900, 60, 200000, 77),
+    (2, 1, 5000, 5003, 20, 3), (1, 16, 50000, 3126, 9000, 0), (9, 2, 2050, 1025, 300, 0)])
 def test_compact(B, page, longest, width, spare, first):
     note("kv_compact B=%d page=%d spare=%d" % (B, page, spare))
     table, lens, _, _, pool = fork_state(B, page, longest, width, spare, B + 1, group=3)
