@@ -36,9 +36,9 @@ namespace ringc {
 namespace {
 
 constexpr int kChunk = 1024;           // columns of a wave's step, 16 a lane
-constexpr int kLists = 64;             // of a group, unless there are more rows and ranks
+constexpr int kLists = 64;             // of a group, that a wave joins at once
 constexpr int kMaxLists = BEAM_SELECT_MAX * RING_MAX_RANKS;
-constexpr int kLdsEntries = 4096;      // of all lists of a group, kept in LDS
+constexpr int kLdsEntries = 6144, kLdsLists = 1024;        // of a group, kept in LDS
 
 struct BeamArgs {
     const void* logits[RING_MAX_RANKS];
@@ -239,7 +239,14 @@ template <bool F32> __global__ __launch_bounds__(1024) void beam_join_kernel(Bea
     __shared__ double lse[BEAM_SELECT_MAX], score[BEAM_SELECT_MAX];
     __shared__ unsigned char head[kMaxLists], ended[BEAM_SELECT_MAX];      // entries of a list that are taken; done
     __shared__ int2 group[BEAM_SELECT_MAX];                // the best maxima: list and entry
-    __shared__ Cand cand[16 * BEAM_SELECT_MAX];
+    __shared__ union {
+        Cand cand[16 * BEAM_SELECT_MAX];
+        struct {                                           // before them: the best of each wave's lists
+            unsigned long long score[16][BEAM_SELECT_MAX];
+            int2 group[16][BEAM_SELECT_MAX];
+        } of_wave;
+    } both;
+    Cand* cand = both.cand;
     __shared__ unsigned long long least;                   // the last of the best maxima
     __shared__ int count;
     const int n = blockIdx.x, tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -306,65 +313,89 @@ template <bool F32> __global__ __launch_bounds__(1024) void beam_join_kernel(Bea
         }
         __syncthreads();
     }
-    if (wave == 0) {
-        // The wave's best head by the score's halves.  Of equals the first beam's,
-        // of its (a large score takes the difference away) the largest logit,
-        // of equals the first list's: lists are in the order of beams and columns.
-        unsigned long long top = 0, u = 0;
-        int list = lane;
-        auto best = [&](int& owner, int h) {
-            const unsigned hi = wave_umax((unsigned)(top >> 32));
-            const unsigned lo = wave_umax((unsigned)(top >> 32) == hi ? (unsigned)top : 0u);
-            u = (unsigned long long)hi << 32 | lo;
-            const unsigned long long tie = __ballot(top == u);
-            owner = __builtin_ctzll(tie);
-            if (!u || !(tie & (tie - 1))) return;
-            const int w = (int)((unsigned)list / (unsigned)per), w0 = wave_min(top == u ? w : 0x7fffffff);
-            const bool mine = top == u && w == w0;
-            const float x = !mine || ended[w0] ? -INFINITY : in_lds ? entries[list * a.K + h].x : from[list * a.K + h].x;
-            const float most = wave_max(x);
-            owner = wave_min(mine && x == most ? list : 0x7fffffff) & 63;
-        };
-        int owner;
-        if (in_lds && lists <= 64) {
-            // a list a lane, its next score at hand (a look at LDS in every
-            // round took it from 350 to 1300 cycles)
-            const unsigned long long* mine = keys + (lane < lists ? lane : 0) * a.K;
-            int h = 0;
-            if (lane < lists) top = mine[0];
-            unsigned long long next = lane < lists && a.K > 1 ? mine[1] : 0;
+    // The wave's best of one score a lane, by its halves.  Of equals the first
+    // beam's, of its (a large score takes the difference away) the largest logit,
+    // of equals the first list's: lists are in the order of beams and columns.
+    auto best = [&](unsigned long long top, int list, int h, int& owner) {
+        const unsigned hi = wave_umax((unsigned)(top >> 32));
+        const unsigned lo = wave_umax((unsigned)(top >> 32) == hi ? (unsigned)top : 0u);
+        const unsigned long long u = (unsigned long long)hi << 32 | lo, tie = __ballot(top == u);
+        owner = __builtin_ctzll(tie);
+        if (!u || !(tie & (tie - 1))) return u;
+        const int w = (int)((unsigned)list / (unsigned)per), w0 = wave_min(top == u ? w : 0x7fffffff);
+        const bool mine = top == u && w == w0;
+        const float x = !mine || ended[w0] ? -INFINITY : in_lds ? entries[list * a.K + h].x : from[list * a.K + h].x;
+        const float most = wave_max(x);
+        const int first = wave_min(mine && x == most ? list : 0x7fffffff);
+        owner = __builtin_ctzll(__ballot(mine && list == first));
+        return u;
+    };
+    const int joins = (lists + kLists - 1) / kLists;       // waves that join a list a lane
+    if (in_lds && wave < joins) {
+        // its next score at hand (a look at LDS in every round took it from 350
+        // to 1300 cycles)
+        const int list = wave * kLists + lane;
+        const unsigned long long* mine = keys + (list < lists ? list : 0) * a.K;
+        int h = 0, owner;
+        unsigned long long top = list < lists ? mine[0] : 0, next = list < lists && a.K > 1 ? mine[1] : 0, u = 0;
+        for (int k = 0; k < a.K; ++k) {
+            u = best(top, list, h, owner);
+            if (lane == owner) {
+                if (joins == 1) {
+                    if (u) group[k] = int2{list, h};
+                } else {
+                    both.of_wave.group[wave][k] = int2{list, h};
+                    both.of_wave.score[wave][k] = u;
+                }
+                top = next;
+                ++h;
+                next = h + 1 < a.K ? mine[h + 1] : 0;
+            }
+            if (!u && joins == 1) break;
+        }
+        if (joins == 1 && lane == 0) least = u;
+    }
+    if (in_lds && joins > 1) {
+        __syncthreads();
+        if (wave == 0) {
+            int h = 0, owner;
+            unsigned long long top = lane < joins ? both.of_wave.score[lane][0] : 0, u = 0;
+            int2 g = lane < joins ? both.of_wave.group[lane][0] : int2{0, 0};
             for (int k = 0; k < a.K; ++k) {
-                best(owner, h);
+                u = best(top, g.x, g.y, owner);
                 if (!u) break;
                 if (lane == owner) {
-                    group[k] = int2{lane, h};
-                    top = next;
-                    ++h;
-                    next = h + 1 < a.K ? mine[h + 1] : 0;
+                    group[k] = g;
+                    if (++h < a.K) g = both.of_wave.group[lane][h];
+                    top = h < a.K ? both.of_wave.score[lane][h] : 0;
                 }
             }
-        } else {
-            auto look = [&]() {
-                top = 0;
-                list = 0;
-                for (int i = lane; i < lists; i += 64) {
-                    const int h = head[i];
-                    if (h >= a.K) continue;
-                    const unsigned long long x = in_lds ? keys[i * a.K + h] : key(i, h, from[i * a.K + h]);
-                    if (x > top) {
-                        top = x;
-                        list = i;
-                    }
+            if (lane == 0) least = u;
+        }
+    }
+    if (!in_lds && wave == 0) {
+        unsigned long long top = 0, u = 0;
+        int list = 0, owner;
+        auto look = [&]() {
+            top = 0;
+            list = 0;
+            for (int i = lane; i < lists; i += 64) {
+                const int h = head[i];
+                if (h >= a.K) continue;
+                const unsigned long long x = key(i, h, from[i * a.K + h]);
+                if (x > top) {
+                    top = x;
+                    list = i;
                 }
-            };
-            look();
-            for (int k = 0; k < a.K; ++k) {
-                best(owner, head[list]);
-                if (!u) break;
-                if (lane == owner) {
-                    group[k] = int2{list, head[list]++};
-                    look();
-                }
+            }
+        };
+        look();
+        for (int k = 0; k < a.K; ++k) {
+            u = best(top, list, head[list], owner);
+            if (!u) break;
+            if (lane == owner) {
+                group[k] = int2{list, head[list]++};
+                look();
             }
         }
         if (lane == 0) least = u;
@@ -439,16 +470,20 @@ template <bool F32> __global__ __launch_bounds__(1024) void beam_join_kernel(Bea
 }
 
 // Parts of a row of one rank: as many as give every SIMD four waves (eight, each
-// with a list of its own to fill, took 71 us where four took 58), as far as
-// there are steps, and few enough that the join has a list a lane.
+// with a list of its own to fill, took 71 us where four took 58), as far as there
+// are steps; up to 64 lists a group, more only where a part has four steps, as the
+// join then takes two turns.  One group of 16 beams into 16 of 200000 tokens
+// takes 41 us with 352 lists, 70 with 64; of 8 into 8 of 150000 to 200000 23.
 struct BeamCut {
     int parts, cols;
 };
-BeamCut beam_cut(int P, int N, int beams, int width, int cus) {
+BeamCut beam_cut(int P, int N, int beams, int keep, int width, int cus) {
     const long long rows = (long long)N * beams * P, steps = ((long long)width + kChunk - 1) / kChunk;
+    const int each = beams * P, most = kLdsEntries / keep < kLdsLists ? kLdsEntries / keep : kLdsLists;
     long long n = rows ? (16LL * cus + rows - 1) / rows : 1;
     if (n > steps) n = steps;
-    if (n > kLists / (beams * P)) n = kLists / (beams * P);
+    if (n > kLists / each && n > steps / 4) n = kLists / each > steps / 4 ? kLists / each : steps / 4;
+    if (n > most / each && n > kLists / each) n = most / each > kLists / each ? most / each : kLists / each;
     if (n < 1) n = 1;
     const long long cols = (steps + n - 1) / n * kChunk;
     BeamCut c;
@@ -469,7 +504,7 @@ using namespace ringc;
 
 extern "C" size_t beam_select_workspace_bytes(int P, int N, int beams, int keep, int width) {
     if (!beam_shape(P, N, beams, keep, width)) return 0;
-    const BeamCut c = beam_cut(P, N, beams, width, dev_info().cus);
+    const BeamCut c = beam_cut(P, N, beams, keep, width, dev_info().cus);
     const size_t lists = (size_t)P * N * beams * c.parts;
     return kStatusBytes + (lists * (keep + 1) * sizeof(float2) + 255) / 256 * 256;
 }
@@ -493,7 +528,7 @@ extern "C" int beam_select(const void* const* logits, const float* scores, const
         if (!logits[r] || ((uintptr_t)logits[r] & 15)) return RING_EINVAL;
         a.logits[r] = logits[r];
     }
-    const BeamCut c = beam_cut(P, N, beams, width, dev_info().cus);
+    const BeamCut c = beam_cut(P, N, beams, keep, width, dev_info().cus);
     a.scores = scores;
     a.done = done;
     a.parents = parents;
@@ -521,8 +556,9 @@ extern "C" int beam_select(const void* const* logits, const float* scores, const
     if (dtype == RING_F32) hipLaunchKernelGGL(beam_scan_kernel<true>, grid, dim3(256), 0, s, a, (unsigned)lists);
     else hipLaunchKernelGGL(beam_scan_kernel<false>, grid, dim3(256), 0, s, a, (unsigned)lists);
     if (hipGetLastError() != hipSuccess) return RING_EHIP;
-    const int entries = beams * P * c.parts * keep, in_lds = entries <= kLdsEntries;
-    const dim3 block(64u * (beams < 4 ? 4 : beams < 16 ? beams : 16));
+    const int group_lists = beams * P * c.parts, entries = group_lists * keep, in_lds = entries <= kLdsEntries && group_lists <= kLdsLists;
+    const int joins = in_lds ? (group_lists + kLists - 1) / kLists : 1, rows = beams < 4 ? 4 : beams < 16 ? beams : 16;
+    const dim3 block(64u * (joins > rows ? joins : rows));
     const size_t dyn = in_lds ? entries * 16 : 0;
     if (dtype == RING_F32) hipLaunchKernelGGL(beam_join_kernel<true>, dim3((unsigned)N), block, dyn, s, a, in_lds);
     else hipLaunchKernelGGL(beam_join_kernel<false>, dim3((unsigned)N), block, dyn, s, a, in_lds);
