@@ -84,7 +84,9 @@ size_t beam_select_workspace_bytes(int P, int N, int beams, int keep, int width)
  *                  Copies take pages that become free first, by number, then
  *                  free_pages[*used] on; what is left of the former goes, by
  *                  number, to the entries right below *used.  Where pages run
- *                  out, the table gets -1 and *used_after exceeds n_free.
+ *                  out, the table gets -1 and *used_after exceeds n_free.  A
+ *                  *used above n_free (they had run out before, here or in
+ *                  kv_plan) counts as n_free.
  * Entries of the table outside [0, pages) are passed on; they are neither
  * copied nor freed.  A page belongs to the table alone: it is in no other
  * table and not among the free ones.  Repeating the call with the same inputs

@@ -73,6 +73,7 @@ def fork(table, lengths, parents, keep, free, used, page, pages, group, width=0)
     free_pages); width: of a table without rows."""
     width = len(table[0]) if len(table) else width
     free = [int(x) for x in free]
+    used = min(int(used), len(free))                   # more stands for entries that got no page
     before = {int(e) for row, n in zip(table, lengths) for e in row[:-(-_tokens(n, width, page) // page)] if 0 <= e < pages}
     rows, lens = [], []
     for i, p in enumerate(parents):

@@ -212,7 +212,9 @@ __device__ __forceinline__ void new_row(const ForkArgs& a, const RowPiece& piece
 
 // The workgroup that finishes: copies are counted in row order, freed pages by
 // number, and the one handed to the other.
-template <bool LDS> __device__ __forceinline__ void finish_fork(const ForkArgs& a, int used, int* lds) {
+template <bool LDS> __device__ __forceinline__ void finish_fork(const ForkArgs& a, int used_before, int* lds) {
+    // (what exceeds n_free stands for table entries that got no page)
+    const int used = used_before < a.n_free ? used_before : a.n_free;
     int *page = lds, *at = lds + a.B2, *rank = lds + 2 * a.B2, *taken = lds + 3 * a.B2;      // per row: as in last, and its copy; per copy: a freed page
     const int tid = threadIdx.x;
     const bool grouped = a.shared && a.group > 1;
