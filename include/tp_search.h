@@ -51,8 +51,9 @@ extern "C" {
  *   done_after    [N][keep] whether it was done or t is end_token (0 or 1)
  * Beams whose score is not finite have no candidates.  Places that no candidate
  * is left for hold parent -1, token -1, score -inf and done 0.
- * Scores are compared in 64 bits, log sum exp being the sum of fp32
- * exponentials (some 3e-8 off), and rounded once to fp32.
+ * Scores are compared in 64 bits, and rounded once to fp32.  log sum exp is a
+ * 64-bit sum of fp32 exponentials, 16 at a time added in fp32: some 1e-8 off,
+ * up to 2e-7 where one token has most of the weight, whatever the row's width.
  * done and done_after go together; end_token may be -1 (none) without them.
  * beams and keep are 1 .. BEAM_SELECT_MAX; outputs may not overlap inputs.
  */

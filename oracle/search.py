@@ -11,12 +11,12 @@ MAGNITUDES = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
 
 # ---------------------------------------------------------------- choice of continuations
 def log_probs(logits):
-    """Log softmax of a row over its finite logits, and the bound on an fp32
-    log sum exp whose lanes take 16 columns of every 1024 at a time: a term
-    exp(d) is off by (3 |d| + 8) U relative (the difference, the exponent's
-    fma and the hardware's exponential), the running sum by as much at every
-    rise of its maximum, and each of the additions on a term's way to the total
-    by U."""
+    """Log softmax of a row over its finite logits, and the bound on a log sum
+    exp whose lanes take 16 columns of every 1024 at a time: a term exp(d) is
+    off by (3 |d| + 8) U relative (the difference, the exponent's fma and the
+    hardware's exponential; exp(0) is 1), and the 16 are added in fp32 in four
+    levels of pairs, U each.  All further sums and what scales them are in 64
+    bits, off by less than another U."""
     x = np.where(np.isfinite(logits), logits.astype(np.float64), -np.inf)
     m = x.max(initial=-np.inf)
     if m == -np.inf:
@@ -24,9 +24,7 @@ def log_probs(logits):
     p = np.exp(x - m)
     s = p.sum()
     d = np.where(x > -np.inf, m - x, 0)
-    spread = d.max()
-    chunks = -(-len(x) // 1024)
-    bound = ((p * (3 * d + 8)).sum() / s + 9 * chunks + 3 * spread + 24) * U
+    bound = ((p * np.where(d > 0, 3 * d + 8, 0)).sum() / s + 5) * U
     return x - (m + np.log(s)), bound
 
 

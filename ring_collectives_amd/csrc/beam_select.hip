@@ -16,8 +16,8 @@
 // (Lists of values instead of maxima took a wave 144 operations where one is
 // put in, 25 so: of 512 rows of 100003 logits two thirds of all operations.)
 // The logits read bound it, and an exponential a logit, at a quarter of the
-// rate of a plain operation: the 184 MB of 460 such rows take 36 us, 5.1 TB/s
-// with the VALU 63% busy, and their join 8.  Four rows of 8000 take 5 and 6 us:
+// rate of a plain operation: the 184 MB of 460 such rows take 37 us, 4.9 TB/s,
+// and their join 8.5.  Four rows of 8000 take 5 and 6 us:
 // launches and five trips to memory one after another.  A join by a group's
 // last workgroup to finish instead of a launch was no faster (44 us for the
 // large case in all, 43 so; 11.2 for the small one, 10.5 so): what it reads
@@ -25,8 +25,11 @@
 //
 // The sum is of fp32 exponentials (the exponent's product with log2 e in two
 // parts, so that its error is the rounding of x - m alone), added 16 at a time
-// in pairs; its logarithm and the scores are 64-bit numbers, since beams whose
-// scores differ by less than fp32 shows are told apart by them.
+// in pairs.  All sums of those, their logarithm and the scores are 64-bit
+// numbers, since beams whose scores differ by less than fp32 shows are told
+// apart by them: a running fp32 sum rounds once a step, which next to one large
+// logit or on a slow ascent put the scores of 200000 tokens off by up to 4.7e-6,
+// where they are off by 1.2e-7 so, of like logits by 1e-8 (1 us of the 37).
 #include "attn_internal.h"
 #include "tp_search.h"
 
@@ -40,6 +43,12 @@ constexpr int kLists = 64;             // of a group, that a wave joins at once
 constexpr int kMaxLists = BEAM_SELECT_MAX * RING_MAX_RANKS;
 constexpr int kLdsEntries = 6144, kLdsLists = 1024;        // of a group, kept in LDS
 
+// A part's largest logit m, and the sum of exp(x - m).
+struct alignas(16) MaxSum {
+    double s;
+    float m;
+};
+
 struct BeamArgs {
     const void* logits[RING_MAX_RANKS];
     const float* scores;
@@ -51,7 +60,7 @@ struct BeamArgs {
     int P, N, W, K, width, vocab, end, parts, part_cols;       // parts of a row of one rank, of part_cols columns
     Status* status;
     WsSpan data;
-    float2* ms;                        // [row][rank][part] m, s
+    MaxSum* ms;                        // [row][rank][part]
     float2* list;                      // [row][rank][part][K] maximum and (bits of) its step and lane
 };
 
@@ -63,6 +72,25 @@ __device__ __forceinline__ float only_finite(float x) { return __builtin_fabsf(x
 __device__ __forceinline__ float exp2_of(float d) {            // 2^(d log2 e)
     constexpr float hi = kLog2e, lo = 1.92596299e-8f;          // log2 e - hi
     return exp2_hw(__builtin_fmaf(d, hi, d * lo));
+}
+
+// e^(m - top) for m <= top, off by less than 2^-35 of it (so that what many rises
+// of a maximum make of a sum adds up to nothing), 1 where they are equal and 0
+// where m is -inf: 2^n e^r with |r| <= ln 2 / 2, e^r by its series up to r^9.
+__device__ __forceinline__ double exp_below(float m, float top) {
+    const double x = fmax((double)m - (double)top, -1000.0), n = __builtin_rint(x * 1.4426950408889634);     // (NaN gives -1000)
+    const double r = __builtin_fma(n, -0.6931471805599453, x);
+    double p = 1.0 / 362880;
+    p = __builtin_fma(p, r, 1.0 / 40320);
+    p = __builtin_fma(p, r, 1.0 / 5040);
+    p = __builtin_fma(p, r, 1.0 / 720);
+    p = __builtin_fma(p, r, 1.0 / 120);
+    p = __builtin_fma(p, r, 1.0 / 24);
+    p = __builtin_fma(p, r, 1.0 / 6);
+    p = __builtin_fma(p, r, 0.5);
+    p = __builtin_fma(p, r, 1.0);
+    p = __builtin_fma(p, r, 1.0);
+    return __builtin_ldexp(p, (int)n);
 }
 
 // A wave's maximum, and its least number, in every lane: four steps within rows
@@ -123,7 +151,8 @@ template <bool F32> __global__ __launch_bounds__(256) void beam_scan_kernel(Beam
     const unsigned each = (unsigned)a.parts * a.P;
     const int v0 = (int)(blockIdx.x * 4 >= row * each ? 0 : row * each - blockIdx.x * 4);
     const int v1 = (int)((row + 1) * each - blockIdx.x * 4 < 4 ? (row + 1) * each - blockIdx.x * 4 : 4);
-    float m = -INFINITY, s = 0.0f;             // this lane's
+    float m = -INFINITY;                       // this lane's
+    double s = 0.0;
     float best = -INFINITY, last = -INFINITY;  // the list: lane i's maximum, and the K-th
     int at = -1;                               // the step and lane it is the maximum of
     auto load = [&](int c, u32x4 (&r)[E]) {
@@ -162,7 +191,7 @@ template <bool F32> __global__ __launch_bounds__(256) void beam_scan_kernel(Beam
             for (int d = 8; d; d /= 2)
 #pragma unroll
                 for (int e = 0; e < d; ++e) y[e] += y[e + d];
-            sum = s * exp2_of(m - sub) + y[0];
+            sum = y[0];
         };
         weigh();
         // NaN and infinity make NaN of the sum: once more without them
@@ -171,7 +200,8 @@ template <bool F32> __global__ __launch_bounds__(256) void beam_scan_kernel(Beam
             for (int e = 0; e < 16; ++e) x[e] = only_finite(x[e]);
             weigh();
         }
-        s = sum;
+        if (__any(mn > m)) s *= exp_below(m, mn);
+        s += sum;
         m = mn;
         float others = -INFINITY;
         for (int v = v0; v < v1; ++v) others = fmaxf(others, ((volatile float*)reached)[v]);
@@ -206,10 +236,10 @@ template <bool F32> __global__ __launch_bounds__(256) void beam_scan_kernel(Beam
         if (put && lane == 0) ((volatile float*)reached)[wave] = last;
     }
     const float mw = wave_max(m);
-    float sw = m > -INFINITY ? s * exp2_of(m - mw) : 0.0f;
+    double sw = m > -INFINITY ? s * exp_below(m, mw) : 0.0;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) sw += __shfl_xor(sw, d);
-    if (lane == 0) a.ms[w] = float2{mw, sw};
+    if (lane == 0) a.ms[w] = MaxSum{sw, mw};
     if (lane < a.K) a.list[(long long)w * a.K + lane] = float2{best, __builtin_bit_cast(float, at)};
 }
 
@@ -256,7 +286,7 @@ template <bool F32> __global__ __launch_bounds__(1024) void beam_join_kernel(Bea
     const int row0 = n * a.W + (wave < a.W ? wave : 0);
     const float sc0 = a.scores[row0];
     const bool done0 = a.done && a.done[row0];
-    const float2 first = lane < per ? a.ms[(long long)row0 * per + lane] : float2{-INFINITY, 0.0f};
+    const MaxSum first = lane < per ? a.ms[(long long)row0 * per + lane] : MaxSum{0.0, -INFINITY};
     float2* entries = (float2*)(keys + lists * a.K);
     constexpr int kEarly = 4;
     float2 early[kEarly];
@@ -269,17 +299,17 @@ template <bool F32> __global__ __launch_bounds__(1024) void beam_join_kernel(Bea
     for (int w = wave; w < a.W; w += waves) {
         const int row = n * a.W + w;
         const float sc = w == wave ? sc0 : a.scores[row];
-        const float2* p = a.ms + (long long)row * per;
-        const float2 p0 = w == wave ? first : lane < per ? p[lane] : float2{-INFINITY, 0.0f};
+        const MaxSum* p = a.ms + (long long)row * per;
+        const MaxSum p0 = w == wave ? first : lane < per ? p[lane] : MaxSum{0.0, -INFINITY};
         const bool live = __builtin_fabsf(sc) < INFINITY, done = w == wave ? done0 : a.done && a.done[row];
         double l = 0.0;
         if (live && !done) {
-            float m = p0.x;
-            for (int i = lane + 64; i < per; i += 64) m = fmaxf(m, p[i].x);
+            float m = p0.m;
+            for (int i = lane + 64; i < per; i += 64) m = fmaxf(m, p[i].m);
             m = wave_max(m);
-            double s = p0.x > -INFINITY ? (double)p0.y * exp2_of(p0.x - m) : 0.0;
+            double s = p0.m > -INFINITY ? p0.s * exp_below(p0.m, m) : 0.0;
             for (int i = lane + 64; i < per; i += 64)
-                if (p[i].x > -INFINITY) s += (double)p[i].y * exp2_of(p[i].x - m);
+                if (p[i].m > -INFINITY) s += p[i].s * exp_below(p[i].m, m);
             for (int d = 1; d < per && d < 64; d *= 2) s += __shfl_xor(s, d);
             l = (double)m + log(s);
         }
@@ -506,7 +536,7 @@ extern "C" size_t beam_select_workspace_bytes(int P, int N, int beams, int keep,
     if (!beam_shape(P, N, beams, keep, width)) return 0;
     const BeamCut c = beam_cut(P, N, beams, keep, width, dev_info().cus);
     const size_t lists = (size_t)P * N * beams * c.parts;
-    return kStatusBytes + (lists * (keep + 1) * sizeof(float2) + 255) / 256 * 256;
+    return kStatusBytes + (lists * (keep * sizeof(float2) + sizeof(MaxSum)) + 255) / 256 * 256;
 }
 
 extern "C" int beam_select(const void* const* logits, const float* scores, const unsigned char* done, int* parents,
@@ -548,8 +578,8 @@ extern "C" int beam_select(const void* const* logits, const float* scores, const
     a.status = (Status*)ws;
     a.data = WsSpan{kStatusBytes, need};
     const size_t lists = (size_t)P * N * beams * c.parts;
-    a.ms = (float2*)((char*)ws + kStatusBytes);
-    a.list = a.ms + lists;
+    a.ms = (MaxSum*)((char*)ws + kStatusBytes);
+    a.list = (float2*)(a.ms + lists);
     if (lists >= (1ull << 31)) return RING_EUNSUPPORTED;
     const dim3 grid((unsigned)((lists + 3) / 4));
     hipStream_t s = (hipStream_t)stream;
