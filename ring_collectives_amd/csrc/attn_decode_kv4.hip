@@ -172,8 +172,8 @@ __device__ __forceinline__ void run_tiles(State<D> (&st)[NT], const bf16x8 (&q)[
     // this lane's bytes of a tile's first half, from its keys' codes and scales on
     const unsigned kc = i * (D / 2) + quarter * (D / 8), vc = kc + page.codes(1, 0);
     const unsigned ksc = page.scales(0, i) + quarter * D / 128, vsc = ksc + page.scales(1, 0) - page.scales(0, 0);
-    const unsigned long long stride = (unsigned long long)(f.Hkv * (unsigned)page.bytes());
-    Global<const char> head = f.cache + kv_head * (unsigned)page.bytes();
+    const unsigned long long bytes = (unsigned)page.bytes(), stride = (unsigned)f.Hkv * bytes;       // a page of all heads may pass 4 GiB
+    Global<const char> head = f.cache + (unsigned)kv_head * bytes;
     const unsigned mask = (1u << f.shift) - 1;
     const int write = at + i * kRowBytes<D> + quarter * (D / 2);
     const int read = at + (4 * quarter + (i >> 2)) * kRowBytes<D> + (i & 3) * 8;
