@@ -148,8 +148,9 @@ int kv_copy_pages(void *const *caches, const int *copies, const int *n_copies, i
  * row s % page_size of page s / page_size.
  *
  * tp_kv4_write: rows k[r], v[r] (T rows of Hkv heads of D bf16) to cache rows
- * slots[t]; a slot outside the cache writes nothing, two tokens of one slot
- * give the bytes of either.
+ * slots[t]; a slot outside the cache writes nothing.  Two tokens of one slot
+ * leave a row that is neither's (codes and scales, keys and values may be of
+ * different ones, so a value may have any size), and change no other row.
  * tp_kv4_read: the values of cache rows slots[t] to k[r], v[r] (exact in bf16
  * but for values below 2^-133); zeros for a slot outside the cache.  With it,
  * a prompt that continues behind cached tokens runs through tp_attention.

@@ -83,7 +83,8 @@ def kv4_cache(pages: int, Hkv: int, D: int, page_size: int, device="cuda") -> to
 def tp_kv4_write(k, v, cache, slots, page_size: int, stream=None) -> None:
     """Keys and values k[r], v[r] (T, Hkv, D; bf16) to the cache rows slots[t]
     (T int64, as kv_plan gives them) of the 4-bit caches cache[r] (kv4_cache),
-    in blocks of 32 values with a power-of-two scale each."""
+    in blocks of 32 values with a power-of-two scale each.  Slots that are the
+    same leave a row that may mix their tokens."""
     N.check(_binding().tp_kv4_write(k, v, cache, slots, page_size, *_at(stream)), "tp_kv4_write")
 
 
