@@ -143,6 +143,8 @@ int kv_copy_pages(void *const *caches, const int *copies, const int *n_copies, i
  * format with e2m1 elements).  A block's scale is the least, from 2^-126 to
  * 2^125, with no magnitude above 7 times it, so that no value is off by more
  * than one scale; values round to the nearest code, halfway to the even one.
+ * (What is above 7 * 2^125 is stored as 6 * 2^125, up to two scales off: bf16
+ * could not hold 6 times the next scale.)
  * A block that holds a value that is not finite is stored as NaN.
  * page_size is a power of two of at least 16.  Slots are kv_plan's: slot s is
  * row s % page_size of page s / page_size.

@@ -2,8 +2,8 @@
 //
 // A block of 32 values x with the largest magnitude m has the scale 2^e, e the
 // least with m <= 7 * 2^e: m's exponent less 2, one more where m's mantissa is
-// above 1.75, both read off m's bits.  Codes are the nearest of the format's
-// numbers to x / 2^e.
+// above 1.75, both read off m's bits, and 125 at most (bf16 ends below 6 * 2^126).
+// Codes are the nearest of the format's numbers to x / 2^e.
 //
 // Memory bounds both.  Four lanes hold a block, 16 bytes of bf16 each, which
 // are four bytes of codes; a wave takes one head of kTokens tokens, keys or
