@@ -55,7 +55,8 @@ extern "C" {
  * 64-bit sum of fp32 exponentials, 16 at a time added in fp32: some 1e-8 off,
  * up to 2e-7 where one token has most of the weight, whatever the row's width.
  * done and done_after go together; end_token may be -1 (none) without them.
- * beams and keep are 1 .. BEAM_SELECT_MAX; outputs may not overlap inputs.
+ * beams and keep are 1 .. BEAM_SELECT_MAX; outputs may not overlap inputs (over
+ * scores or done: RING_EINVAL).
  */
 int beam_select(const void *const *logits, const float *scores, const unsigned char *done, int *parents, int *tokens,
                 float *scores_after, unsigned char *done_after, int P, int N, int beams, int keep, int width, int vocab,

@@ -522,6 +522,10 @@ BeamCut beam_cut(int P, int N, int beams, int keep, int width, int cus) {
     return c;
 }
 
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    return a && b && (uintptr_t)a < (uintptr_t)b + nb && (uintptr_t)b < (uintptr_t)a + na;
+}
+
 bool beam_shape(int P, int N, int beams, int keep, int width) {
     return P >= 1 && P <= RING_MAX_RANKS && N >= 0 && beams >= 1 && beams <= BEAM_SELECT_MAX && keep >= 1 && keep <= BEAM_SELECT_MAX &&
            width >= 1 && width <= (1 << 28) && (long long)P * width < (1LL << 31) && (long long)N * beams * P < (1LL << 24);
@@ -551,6 +555,11 @@ extern "C" int beam_select(const void* const* logits, const float* scores, const
     if (N == 0) return RING_OK;
     if (!logits || !scores || !parents || !tokens || !scores_after) return RING_EINVAL;
     if (((uintptr_t)scores | (uintptr_t)parents | (uintptr_t)tokens | (uintptr_t)scores_after) & 3) return RING_EINVAL;
+    // a group may write before another reads
+    const size_t in = (size_t)N * beams, out = (size_t)N * keep;
+    for (const void* p : {(const void*)parents, (const void*)tokens, (const void*)scores_after})
+        if (overlap(p, 4 * out, scores, 4 * in) || overlap(p, 4 * out, done, in)) return RING_EINVAL;
+    if (overlap(done_after, out, scores, 4 * in) || overlap(done_after, out, done, in)) return RING_EINVAL;
     const size_t need = beam_select_workspace_bytes(P, N, beams, keep, width);
     if (!ws || ((uintptr_t)ws & 255) || ws_bytes < need) return RING_EWORKSPACE;
     BeamArgs a;
