@@ -141,7 +141,8 @@ def quantise(x):
     """Codes (..., D) and scale bytes (..., D / 32) of rows of finite or other
     bf16 values, by the definition: the least scale with no magnitude above
     seven times it, and the nearest code."""
-    b = np.asarray(x, dtype=np.float64).reshape(x.shape[:-1] + (-1, 32))
+    with np.errstate(invalid="ignore"):                # (NaN of the signalling kind, on the way to 64 bits)
+        b = np.asarray(x, dtype=np.float64).reshape(x.shape[:-1] + (-1, 32))
     bad = ~np.isfinite(b).all(-1)
     a = np.where(bad, 0.0, np.abs(np.where(np.isfinite(b), b, 0)).max(-1))
     scale = np.full(a.shape, 1)
