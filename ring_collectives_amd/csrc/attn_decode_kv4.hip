@@ -52,7 +52,11 @@ constexpr int kItemCost = 8;
 // long row of a batch is one workgroup's too, and at 2048 keys that takes as
 // long as sharing out and joining.
 constexpr int kWholeTiles = 64;
-constexpr int kMinCost = 4;            // of a wave, if there is as much (and no less than a tile's)
+// Of a wave, if there is as much (and no less than a tile's).  3 requests of 200 /
+// 600 keys in a table of 8192 10.3 / 11.9 us, one of 10000 12.5; with 2 10.3 / 11.3
+// and 12.3, with 8 11.3 / 12.5 and 13.3, with 16 11.2 / 14.5 and 15.5; calls of many
+// keys alike.
+constexpr int kMinCost = 4;
 
 // An item's parts: a wave's each, those before the first and after the last
 // workgroup that is within the item, and one each for the workgroups between.
@@ -290,9 +294,11 @@ __device__ __forceinline__ void run_tiles(State<D> (&st)[NT], const bf16x8 (&q)[
                     for (int v = 0; v < 4; ++v) w[4 * h + v] = exp2_hw(__builtin_fmaf(s[n][h][v], f.c, -sub));
                 p[n] = __builtin_convertvector(w, bf16x8);
                 // the sum is of the weights as rounded, so that where few keys have
-                // most of the weight its rounding cancels (3 rows of 200 keys are off
-                // by 1.7e-3 so, 2.0e-3 with the sum of unrounded ones), and a product
-                // with ones (66.5 us for 4 rows of 120000 keys, 67.5 with additions)
+                // most of the weight its rounding cancels (over five inputs 24 groups of
+                // 4 rows of 3000 keys are off by 2.05e-3 to 2.10e-3 so, 2.15e-3 to
+                // 2.21e-3 with the sum of unrounded ones; 3 rows of 200 by 1.75e-3 to
+                // 1.84e-3 both ways), and a product with ones (66.5 us for 4 rows of
+                // 120000 keys, 67.5 with additions)
                 st[n].l = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, p[n], st[n].l, 0, 0, 0);
             }
             asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
@@ -737,7 +743,10 @@ extern "C" int tp_attention_decode_kv4(const void* const* q, const void* const* 
     const dim3 grid((unsigned)(units * a.blocks + a.planners));
     const size_t dyn = (2 * (size_t)B + (shared ? B / group : 0)) * sizeof(int);
     const long long rows = (long long)P * B * Hq;
-    const bool few = rows <= 2LL * dev_info().cus;           // 256 lanes a row, else 64
+    // 256 lanes a row, else 64: 8 rows of 60000 keys 17.3 us so, 31.4 with 64; 512 of
+    // 5000 22.3 and 22.7; 2048 of 5000 52.3 with 256, 51.2 so; 768 behind shared keys
+    // 32.6 and 29.7
+    const bool few = rows <= 2LL * dev_info().cus;
     const dim3 jg((unsigned)(few ? B * Hq : B * ((Hq + 3) / 4)), (unsigned)P);
     auto go = [&](auto d, auto nt) -> int {
         constexpr int kD = decltype(d)::value, kNT = decltype(nt)::value;

@@ -16,8 +16,8 @@
 // (Lists of values instead of maxima took a wave 144 operations where one is
 // put in, 25 so: of 512 rows of 100003 logits two thirds of all operations.)
 // The logits read bound it, and an exponential a logit, at a quarter of the
-// rate of a plain operation: the 184 MB of 460 such rows take 37 us, 4.9 TB/s,
-// and their join 8.5.  Four rows of 8000 take 5 and 6 us:
+// rate of a plain operation: the 184 MB of 460 such rows take 37 us, 4.9 TB/s
+// with the VALU 65% busy, and their join 8.5.  Four rows of 8000 take 5 and 6 us:
 // launches and five trips to memory one after another.  A join by a group's
 // last workgroup to finish instead of a launch was no faster (44 us for the
 // large case in all, 43 so; 11.2 for the small one, 10.5 so): what it reads
@@ -41,7 +41,11 @@ namespace {
 constexpr int kChunk = 1024;           // columns of a wave's step, 16 a lane
 constexpr int kLists = 64;             // of a group, that a wave joins at once
 constexpr int kMaxLists = BEAM_SELECT_MAX * RING_MAX_RANKS;
-constexpr int kLdsEntries = 6144, kLdsLists = 1024;        // of a group, kept in LDS
+// Of a group, kept in LDS, and so that a row's parts are no more: 96 KB beside the
+// kernel's own 30 of the 160.  16 beams into 16 of 200000 tokens take 41 us, 54 with
+// 2048, 39 with 8000; 2 groups of 16 into 32 of 100000 on 4 ranks 61, 70, 61; 8 of 8
+// into 16 of 100000 on 8 ranks 40, 39, 40.
+constexpr int kLdsEntries = 6144, kLdsLists = 1024;
 
 // A part's largest logit m, and the sum of exp(x - m).
 struct alignas(16) MaxSum {
@@ -503,7 +507,7 @@ template <bool F32> __global__ __launch_bounds__(1024) void beam_join_kernel(Bea
 // with a list of its own to fill, took 71 us where four took 58), as far as there
 // are steps; up to 64 lists a group, more only where a part has four steps, as the
 // join then takes two turns.  One group of 16 beams into 16 of 200000 tokens
-// takes 41 us with 352 lists, 70 with 64; of 8 into 8 of 150000 to 200000 23.
+// takes 41 us with 352 lists, 70 with 64; of 8 into 8 of 150000 to 200000 23 to 24.
 struct BeamCut {
     int parts, cols;
 };

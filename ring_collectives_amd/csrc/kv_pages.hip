@@ -17,7 +17,9 @@
 // same place: beams of one prompt hold mostly the same pages.  1024 rows of 250
 // pages out of 198000 take 22 us: 10 until the 62000 marks are made, 12 for the
 // last workgroup, 5 of them trips to the sets, 4 handing out 22000 freed pages.
-// 200 rows of 80 pages out of 48000, compacted, take 12 and 5 us.
+// 200 rows of 80 pages out of 48000, compacted, take 12 and 5 us.  The finishing
+// workgroup reads and clears the whole pool's sets: 4 rows of 44 pages out of 2^20
+// take 28 us, the 1024 rows there 46.
 #include "attn_internal.h"
 #include "tp_search.h"
 
@@ -860,6 +862,8 @@ extern "C" int kv_copy_pages(void* const* caches, const int* copies, const int* 
     a.chunks = (a.vecs + a.per - 1) / a.per;
     if ((long long)n_caches * a.chunks >= (1LL << 31)) return RING_EUNSUPPORTED;
     const long long items = ((long long)capacity * n_caches * a.chunks + 3) / 4;
+    // eight workgroups a compute unit: 48000 pages compacted 94.3 us (89.4 with four,
+    // 92.9 with sixteen), 9000 of two bf16 caches a rank 223 (218, 222)
     const long long most = 8LL * dev_info().cus;
     hipLaunchKernelGGL(kv_copy_kernel, dim3((unsigned)(items < most ? items : most)), dim3(256), 0, (hipStream_t)stream, a);
     return hipGetLastError() == hipSuccess ? RING_OK : RING_EHIP;
